@@ -92,7 +92,7 @@ def draw(rng):
         c["seqs"] = _log_int(rng, 1, max(1, min(64, most // c["hi"])))
         c["window"] = rng.choice([0, _log_int(rng, 1, 64)])
         if not c["causal"]:
-            c["qhi"] = _log_int(rng, 1, 2000)
+            c["qhi"] = _log_int(rng, 1, min(2000, 3_000_000 // (c["seqs"] * c["hq"])))
             c["qlo"] = rng.randint(0, c["qhi"])
     else:
         c["hi"] = _log_int(rng, 8, 131_000)
