@@ -370,6 +370,163 @@ quail_status quail_quantize_kv_fp8_with_scales(int32_t num_anchors,
                                                void* kv_e4m3, float* scale,
                                                quail_stream_t stream);
 
+/*
+ * A paged key/value cache: pages of page_size tokens, each [page_size, Hkv, d] (the token
+ * rows of every K/V tensor of this library, so a contiguous [T, Hkv, d] tensor is a pool of
+ * T / page_size pages as it stands), and a block table that names the pages of each
+ * sequence in order. It holds the anchor KV that [P1] "Como funciona" keeps between
+ * prefills, and lets it grow and be cut token by token.
+ *   k_pages, v_pages [num_pages, page_size, Hkv, d] bf16, or e4m3 codes (16-byte aligned)
+ *   block_table [num_seqs, max_pages_per_seq] int32; entries past a sequence's last page
+ *               are not read. Sequences may share pages that no call writes.
+ *   k_scale, v_scale [num_seqs, Hkv] fp32 (value = e4m3(code) * scale), with e4m3 pages
+ *               only; NULL with bf16 pages
+ * Block tables, lengths and positions are read on the device. What they name outside the
+ * pool, the table or max_seq_len is not touched; the call says below what becomes of the
+ * sequence, and quail_get_device_error() reports QUAIL_ERR_DEVICE_BOUNDS.
+ * Limits: page_size a power of two from 16 to 256; max_seq_len at most 2^30 and at most
+ * max_pages_per_seq * page_size; d in {64, 128}; Hq/Hkv in {1, 2, 4, 8, 16};
+ * num_seqs * Hq < 2^28.
+ */
+typedef struct {
+  int32_t num_seqs;              /* B >= 0 */
+  int32_t max_seq_len;           /* >= every length in the cache */
+  int32_t num_pages;             /* pages of the pool */
+  int32_t page_size;             /* tokens per page */
+  int32_t max_pages_per_seq;     /* row length of the block table */
+  int32_t num_q_heads;           /* Hq, a multiple of Hkv */
+  int32_t num_kv_heads;          /* Hkv */
+  int32_t head_dim;              /* d */
+  float softmax_scale;           /* 0 => 1/sqrt(d) */
+  int32_t kv_dtype;              /* quail_dtype of the pages */
+} quail_paged_desc;
+
+/*
+ * Writes new tokens' K and V rows into the pages: whole prompts (the rows that a causal
+ * prefill read) or one token per sequence. Row i of sequence b goes to position
+ * start_pos[b] + i. With e4m3 pages the code is e4m3(x / scale), x / scale rounded to fp32
+ * first, then to nearest even with saturation at +-448 - quail_quantize_kv_fp8's codes when
+ * the scales are.
+ *   num_new     T, new tokens of all sequences
+ *   k_new, v_new [T, Hkv, d] bf16, rows k_row_stride / v_row_stride elements apart (>=
+ *               Hkv * d, a multiple of 8; e.g. columns of a fused projection), 16-byte
+ *               aligned
+ *   new_offsets [B+1] int32 prefix sums into k_new / v_new, or NULL for one token per
+ *               sequence (then T = B)
+ *   start_pos   [B] int32: tokens that the sequence holds already
+ * A row whose position or page is out of range, or that no sequence holds, is skipped and
+ * reported (see above), and so are offsets that do not increase from 0 to T. A page that is written must belong to one sequence: of two rows
+ * that name the same slot an unspecified mixture remains.
+ */
+quail_status quail_paged_kv_append(const quail_paged_desc* desc, int64_t num_new,
+                                   const void* k_new, const void* v_new, int64_t k_row_stride,
+                                   int64_t v_row_stride, const int32_t* new_offsets,
+                                   const int32_t* start_pos, const int32_t* block_table,
+                                   const float* k_scale, const float* v_scale, void* k_pages,
+                                   void* v_pages, quail_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over its cached tokens (its own K and V appended
+ * before the call), and the weight that each cached token receives:
+ *   w[b, h, j] = exp(scale q[b, h] . k_j - lse[b, h]) for j < seq_lens[b],
+ *   out[b, h] = sum_j w[b, h, j] v_j,
+ *   score_out[b, g, j] = score_in[b, g, j] + sum over the heads h of KV head g of w[b, h, j].
+ * The batch's cached tokens are divided evenly over the GPU whatever the lengths, long
+ * sequences among many SMs, and joined; results do not depend on timing.
+ *   q [B, Hq, d] bf16, rows q_row_stride elements apart (>= Hq * d, a multiple of 8)
+ *   seq_lens [B] int32, the new token included. Length 0: out 0 and lse -inf. A length out
+ *            of range or a page outside the pool: out and lse NaN for that sequence (for
+ *            its KV heads), and its score_out as below with w = 0, or untouched where the
+ *            length is out of range.
+ *   out [B, Hq, d] bf16, 16-byte aligned; lse [B, Hq] fp32 (natural log), may be NULL
+ *   score_in, score_out [B, Hkv, score_stride] fp32, score_stride >= max_seq_len;
+ *            score_out NULL: no weights are formed; score_in NULL: zeros; both may be the
+ *            same buffer. Entries at seq_lens[b] and beyond are left as they were. A head
+ *            whose lse is NaN adds nothing.
+ *   workspace: at least quail_paged_decode_workspace_size(desc, score_out != NULL) bytes,
+ *            16-byte aligned, overwritten; calls that share one must not overlap on the GPU.
+ */
+quail_status quail_paged_decode_attn(const quail_paged_desc* desc, const void* q,
+                                     int64_t q_row_stride, const void* k_pages,
+                                     const void* v_pages, const int32_t* block_table,
+                                     const int32_t* seq_lens, const float* k_scale,
+                                     const float* v_scale, void* out, float* lse,
+                                     const float* score_in, float* score_out,
+                                     int64_t score_stride, void* workspace,
+                                     size_t workspace_bytes, quail_stream_t stream);
+
+/* Workspace bytes for quail_paged_decode_attn (0 when desc is not valid). With scores it
+ * holds 4 * B * Hq * max_seq_len bytes of raw scores (max_seq_len rounded up). */
+size_t quail_paged_decode_workspace_size(const quail_paged_desc* desc, int32_t with_scores);
+
+/*
+ * The attention weight that keys receive from many queries, from the lse that an attention
+ * call wrote:
+ *   score_out[s, g, j] = score_in[s, g, j] + sum over the queries i of sequence s that see
+ *       key j, and the heads h of KV head g, of exp(scale q[i, h] . k[j, g] - lse[i, h])
+ * for j < the number of keys of s. Queries: the last `window` of the sequence's nq (0: all).
+ * causal = 1: query i sees keys 0 .. i + (nk - nq), the last query all of them (a prompt's
+ * own prefill: q_offsets = k_offsets = seq_offsets of quail_causal_prefill_attn); causal = 0:
+ * every query sees every key (an anchor and all tokens of its suffixes:
+ * q_offsets[a] = suffix_offsets[anchor_suffix_ptr[a]], lse from quail_cascade_attn).
+ *   q [Tq, Hq, d], k [Tk, Hkv, d] bf16, rows q_row_stride / k_row_stride elements apart
+ *            (at least the row, a multiple of 8), 16-byte aligned
+ *   lse [Tq, Hq] fp32 natural log; a query whose lse is -inf gives no weight
+ *   q_offsets, k_offsets [num_seqs+1] int32 token prefix sums (checked on the device: a
+ *            sequence whose ranges lie outside the totals or exceed max_q_len / max_k_len
+ *            is left out and QUAIL_ERR_DEVICE_BOUNDS reported)
+ *   score_in, score_out [num_seqs, Hkv, score_stride] fp32, score_stride >= max_k_len;
+ *            score_in NULL: zeros; both may be the same buffer. Entries past the sequence's
+ *            keys are left as they were.
+ * Limits: d in {64, 128}, Hq/Hkv in {1, 2, 4, 8, 16}.
+ */
+quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t total_k_tokens,
+                               int32_t max_q_len, int32_t max_k_len, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, float softmax_scale,
+                               int32_t causal, int32_t window, const void* q,
+                               int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                               const float* lse, const int32_t* q_offsets,
+                               const int32_t* k_offsets, const float* score_in, float* score_out,
+                               int64_t score_stride, quail_stream_t stream);
+
+/*
+ * Eviction by accumulated weight (quail_kv_plan evicts whole anchors; this cuts a sequence
+ * down to a budget). Per sequence b and KV head g, of n = seq_lens[b] tokens
+ * new_lens[b] = min(n, budget) stay: the last min(recent, new_lens[b]), and of the others
+ * those with the largest score[b, g, j] (equal scores: the lower position; NaN counts as
+ * -inf). Their K and V rows are copied in order to positions 0 .. new_lens[b]-1 of the pages
+ * that dst_table names; heads keep their own positions (keys are already rotated). The
+ * source is not changed, so shared pages may be cut; the caller frees it.
+ *   budget >= 1, 0 <= recent <= budget
+ *   score [B, Hkv, score_stride] fp32, score_stride >= max_seq_len
+ *   dst_table [B, dst_max_pages_per_seq] int32 into the destination pool k_dst / v_dst
+ *            [dst_num_pages, page_size, Hkv, d]: either the same pool (same pointers and
+ *            page count) or one that does not overlap it. Each destination page belongs to
+ *            one sequence and is none that a sequence of the call holds; rows for pages
+ *            that break this are not written and new_lens[b] becomes -1, as it does for a
+ *            source page outside the pool and for a length out of range (all with
+ *            QUAIL_ERR_DEVICE_BOUNDS).
+ *   kept [B, Hkv, budget] int32 out: the kept positions in increasing order, then -1
+ *   new_lens [B] int32 out, not overlapping seq_lens
+ *   score_out [B, Hkv, score_out_stride] fp32 out or NULL, score_out_stride >= budget, not
+ *            overlapping score: the kept tokens' scores, zeros behind them
+ *   workspace: at least quail_paged_evict_workspace_size(desc, dst_num_pages) bytes,
+ *            16-byte aligned, overwritten; calls that share one must not overlap on the GPU.
+ * The scales of e4m3 pages stay those of the sequence. num_seqs * budget < 2^31.
+ */
+quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, int32_t recent,
+                                  const void* k_pages, const void* v_pages,
+                                  const int32_t* block_table, const int32_t* seq_lens,
+                                  const float* score, int64_t score_stride,
+                                  const int32_t* dst_table, int32_t dst_max_pages_per_seq,
+                                  int32_t dst_num_pages, void* k_dst, void* v_dst, int32_t* kept,
+                                  int32_t* new_lens, float* score_out, int64_t score_out_stride,
+                                  void* workspace, size_t workspace_bytes,
+                                  quail_stream_t stream);
+
+/* Workspace bytes for quail_paged_kv_evict (0 when an argument is not valid). */
+size_t quail_paged_evict_workspace_size(const quail_paged_desc* desc, int32_t dst_num_pages);
+
 /* Static, NUL-terminated name of a status code. */
 const char* quail_status_string(quail_status status);
 

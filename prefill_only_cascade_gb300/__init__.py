@@ -35,7 +35,9 @@ EXPORTED_SYMBOLS = (
     "quail_causal_prefill_workspace_size", "quail_kv_plan", "quail_shard_anchors",
     "quail_join_select", "quail_join_select_workspace_size", "quail_shard_batch",
     "quail_cascade_attn_two_pass", "quail_cascade_two_pass_workspace_size",
-    "quail_quantize_kv_fp8_with_scales",
+    "quail_quantize_kv_fp8_with_scales", "quail_paged_kv_append", "quail_paged_decode_attn",
+    "quail_paged_decode_workspace_size", "quail_attn_scores", "quail_paged_kv_evict",
+    "quail_paged_evict_workspace_size",
 )
 
 
@@ -73,6 +75,13 @@ class CascadeDesc(ctypes.Structure):
         ("softmax_scale", ctypes.c_float),
         ("kv_anchor_dtype", ctypes.c_int32),
     ]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_seqs", "max_seq_len", "num_pages", "page_size", "max_pages_per_seq", "num_q_heads",
+        "num_kv_heads", "head_dim")] + [("softmax_scale", ctypes.c_float),
+                                        ("kv_dtype", ctypes.c_int32)]
 
 
 def _load():
@@ -139,6 +148,24 @@ def _load():
     lib.quail_join_select.argtypes = [i32, i32, vp, vp, i32, vp, vp, vp, vp, vp,
                                       ctypes.c_size_t, vp]
     lib.quail_join_select.restype = ctypes.c_int
+    sz = ctypes.c_size_t
+    paged = ctypes.POINTER(PagedDesc)
+    lib.quail_paged_kv_append.argtypes = [paged, i64, vp, vp, i64, i64, i32p, i32p, i32p, f32p,
+                                          f32p, vp, vp, vp]
+    lib.quail_paged_kv_append.restype = ctypes.c_int
+    lib.quail_paged_decode_attn.argtypes = [paged, vp, i64, vp, vp, i32p, i32p, f32p, f32p, vp,
+                                            f32p, f32p, f32p, i64, vp, sz, vp]
+    lib.quail_paged_decode_attn.restype = ctypes.c_int
+    lib.quail_paged_decode_workspace_size.argtypes = [paged, i32]
+    lib.quail_paged_decode_workspace_size.restype = sz
+    lib.quail_attn_scores.argtypes = [i32, i64, i64, i32, i32, i32, i32, i32, ctypes.c_float, i32,
+                                      i32, vp, i64, vp, i64, f32p, i32p, i32p, f32p, f32p, i64, vp]
+    lib.quail_attn_scores.restype = ctypes.c_int
+    lib.quail_paged_kv_evict.argtypes = [paged, i32, i32, vp, vp, i32p, i32p, f32p, i64, i32p,
+                                         i32, i32, vp, vp, i32p, i32p, f32p, i64, vp, sz, vp]
+    lib.quail_paged_kv_evict.restype = ctypes.c_int
+    lib.quail_paged_evict_workspace_size.argtypes = [paged, i32]
+    lib.quail_paged_evict_workspace_size.restype = sz
     return lib
 
 
@@ -355,6 +382,198 @@ def quantize_kv_fp8_with_scales(kv_bf16, anchor_offsets, amax, codes, scale, str
         int(anchor_offsets.numel() - 1), _ptr(anchor_offsets), int(T), int(hkv), int(d),
         _ptr(kv_bf16), _ptr(amax), _ptr(codes), _ptr(scale), _stream(stream))
     _check(st, "quail_quantize_kv_fp8_with_scales")
+
+
+def make_paged_desc(num_seqs, max_seq_len, num_pages, page_size, max_pages_per_seq, num_q_heads,
+                    num_kv_heads, head_dim, softmax_scale=0.0, kv_fp8=False) -> PagedDesc:
+    return PagedDesc(int(num_seqs), int(max_seq_len), int(num_pages), int(page_size),
+                     int(max_pages_per_seq), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                     float(softmax_scale), QUAIL_FP8_E4M3 if kv_fp8 else QUAIL_BF16)
+
+
+def _code_dtypes(fp8):
+    return (torch.float8_e4m3fn, torch.uint8) if fp8 else (torch.bfloat16,)
+
+
+def _expect(what, t, shape, dtypes, device, rows=False):
+    """Checks a tensor that the library will address: its type, its shape (None: any size),
+    its device, and that it is contiguous (rows: apart from the stride of its first axis)."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if t.numel() and not (t[0] if rows else t).is_contiguous():
+        raise ValueError(f"{what}: not contiguous")
+
+
+class _on_device:
+    """The tensors' device as the current one, and a stream of that device."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got {device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream of {stream.device} with tensors on {device}")
+        self._guard = torch.cuda.device(device)
+        self._device, self._given = device, stream
+
+    def __enter__(self):
+        self._guard.__enter__()
+        return _stream(torch.cuda.current_stream(self._device) if self._given is None
+                       else self._given)
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def _expect_pool(desc, k_pages, v_pages, k_scale, v_scale, pages, device):
+    fp8 = desc.kv_dtype == QUAIL_FP8_E4M3
+    shape = (pages, desc.page_size, desc.num_kv_heads, desc.head_dim)
+    _expect("k_pages", k_pages, shape, _code_dtypes(fp8), device)
+    _expect("v_pages", v_pages, shape, _code_dtypes(fp8), device)
+    if fp8 and (k_scale is None or v_scale is None):
+        raise ValueError("e4m3 pages need k_scale and v_scale")
+    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if s is not None:
+            _expect(name, s, (desc.num_seqs, desc.num_kv_heads), (torch.float32,), device)
+
+
+def _expect_score(what, t, rows, heads, least, device):
+    _expect(what, t, (rows, heads, None), (torch.float32,), device)
+    if t.shape[2] < least:
+        raise ValueError(f"{what}: {t.shape[2]} entries a row, at least {least} are needed")
+
+
+def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pages, v_pages,
+                    new_offsets=None, k_scale=None, v_scale=None, stream=None):
+    """quail_paged_kv_append: rows k_new / v_new ([T, Hkv, d] bf16, any row stride) into the
+    pages at start_pos[b] + i; new_offsets ([B+1] int32) delimits the sequences' rows (None:
+    one token each). With e4m3 pages the rows become codes under the given scales."""
+    dev, i32 = k_new.device, (torch.int32,)
+    row = (k_new.shape[0], desc.num_kv_heads, desc.head_dim)
+    _expect("k_new", k_new, row, (torch.bfloat16,), dev, rows=True)
+    _expect("v_new", v_new, row, (torch.bfloat16,), dev, rows=True)
+    _expect("start_pos", start_pos, (desc.num_seqs,), i32, dev)
+    _expect("block_table", block_table, (desc.num_seqs, desc.max_pages_per_seq), i32, dev)
+    if new_offsets is not None:
+        _expect("new_offsets", new_offsets, (desc.num_seqs + 1,), i32, dev)
+    _expect_pool(desc, k_pages, v_pages, k_scale, v_scale, desc.num_pages, dev)
+    least = desc.num_kv_heads * desc.head_dim
+    with _on_device(dev, stream) as st:
+        code = lib.quail_paged_kv_append(
+            ctypes.byref(desc), row[0], _ptr(k_new), _ptr(v_new),
+            k_new.stride(0) if row[0] > 1 else least, v_new.stride(0) if row[0] > 1 else least,
+            _ptr(new_offsets), _ptr(start_pos), _ptr(block_table), _ptr(k_scale), _ptr(v_scale),
+            _ptr(k_pages), _ptr(v_pages), st)
+    _check(code, "quail_paged_kv_append")
+
+
+def paged_decode_workspace_size(desc: PagedDesc, with_scores=False) -> int:
+    return int(lib.quail_paged_decode_workspace_size(ctypes.byref(desc), 1 if with_scores else 0))
+
+
+def paged_decode_attn(desc: PagedDesc, q, k_pages, v_pages, block_table, seq_lens, out, workspace,
+                      lse=None, k_scale=None, v_scale=None, score_in=None, score_out=None,
+                      stream=None):
+    """quail_paged_decode_attn: attention of one new token per sequence (q [B, Hq, d] bf16, any
+    row stride) over its cached tokens; with score_out ([B, Hkv, n] fp32) also score_in plus
+    the weight that each cached token receives (score_in may be score_out)."""
+    if workspace is None:
+        raise ValueError("workspace is required (size: paged_decode_workspace_size(...))")
+    dev, i32, f32 = q.device, (torch.int32,), (torch.float32,)
+    shape = (desc.num_seqs, desc.num_q_heads, desc.head_dim)
+    _expect("q", q, shape, (torch.bfloat16,), dev, rows=True)
+    _expect("out", out, shape, (torch.bfloat16,), dev)
+    _expect("seq_lens", seq_lens, (desc.num_seqs,), i32, dev)
+    _expect("block_table", block_table, (desc.num_seqs, desc.max_pages_per_seq), i32, dev)
+    _expect("workspace", workspace, (None,), (torch.uint8,), dev)
+    _expect_pool(desc, k_pages, v_pages, k_scale, v_scale, desc.num_pages, dev)
+    if lse is not None:
+        _expect("lse", lse, shape[:2], f32, dev)
+    if score_in is not None and score_out is None:
+        raise ValueError("score_in without score_out")
+    width = 0
+    if score_out is not None:
+        _expect_score("score_out", score_out, desc.num_seqs, desc.num_kv_heads, desc.max_seq_len,
+                      dev)
+        width = score_out.shape[2]
+        if score_in is not None:
+            _expect("score_in", score_in, tuple(score_out.shape), f32, dev)
+    with _on_device(dev, stream) as st:
+        code = lib.quail_paged_decode_attn(
+            ctypes.byref(desc), _ptr(q),
+            q.stride(0) if shape[0] > 1 else desc.num_q_heads * desc.head_dim, _ptr(k_pages),
+            _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(k_scale), _ptr(v_scale),
+            _ptr(out), _ptr(lse), _ptr(score_in), _ptr(score_out), width, _ptr(workspace),
+            workspace.numel(), st)
+    _check(code, "quail_paged_decode_attn")
+
+
+def attn_scores(q, k, lse, q_offsets, k_offsets, score_out, max_q_len, max_k_len, causal=True,
+                window=0, score_in=None, softmax_scale=0.0, stream=None):
+    """quail_attn_scores: the attention weight that each key receives from the queries of its
+    sequence (q [Tq, Hq, d], k [Tk, Hkv, d] bf16 with any row stride, lse [Tq, Hq] from the
+    attention call), added to score_in into score_out [num_seqs, Hkv, n] fp32."""
+    dev, i32, f32 = k.device, (torch.int32,), (torch.float32,)
+    _expect("q", q, (None, None, None), (torch.bfloat16,), dev, rows=True)
+    _expect("k", k, (None, None, q.shape[2]), (torch.bfloat16,), dev, rows=True)
+    _expect("lse", lse, tuple(q.shape[:2]), f32, dev)
+    _expect("k_offsets", k_offsets, (None,), i32, dev)
+    _expect("q_offsets", q_offsets, tuple(k_offsets.shape), i32, dev)
+    seqs = k_offsets.numel() - 1
+    _expect_score("score_out", score_out, seqs, k.shape[1], int(max_k_len), dev)
+    if score_in is not None:
+        _expect("score_in", score_in, tuple(score_out.shape), f32, dev)
+    hq, hkv, d = q.shape[1], k.shape[1], q.shape[2]
+    with _on_device(dev, stream) as st:
+        code = lib.quail_attn_scores(
+            seqs, q.shape[0], k.shape[0], int(max_q_len), int(max_k_len), hq, hkv, d,
+            float(softmax_scale), 1 if causal else 0, int(window), _ptr(q),
+            q.stride(0) if q.shape[0] > 1 else hq * d, _ptr(k),
+            k.stride(0) if k.shape[0] > 1 else hkv * d, _ptr(lse), _ptr(q_offsets),
+            _ptr(k_offsets), _ptr(score_in), _ptr(score_out), score_out.shape[2], st)
+    _check(code, "quail_attn_scores")
+
+
+def paged_evict_workspace_size(desc: PagedDesc, dst_num_pages) -> int:
+    return int(lib.quail_paged_evict_workspace_size(ctypes.byref(desc), int(dst_num_pages)))
+
+
+def paged_kv_evict(desc: PagedDesc, budget, recent, k_pages, v_pages, block_table, seq_lens, score,
+                   dst_table, k_dst, v_dst, kept, new_lens, workspace, score_out=None,
+                   stream=None):
+    """quail_paged_kv_evict: per (sequence, KV head) the last `recent` tokens and the best
+    scored others, `budget` in all, copied in order into the pages that dst_table names (of
+    the same pool or another); kept [B, Hkv, budget] and new_lens [B] int32 say which and how
+    many, score_out [B, Hkv, n] takes their scores."""
+    if workspace is None:
+        raise ValueError("workspace is required (size: paged_evict_workspace_size(...))")
+    dev, i32, f32 = k_pages.device, (torch.int32,), (torch.float32,)
+    B, hkv = desc.num_seqs, desc.num_kv_heads
+    fp8 = desc.kv_dtype == QUAIL_FP8_E4M3
+    row = (desc.page_size, hkv, desc.head_dim)
+    for name, t, pages in (("k_pages", k_pages, desc.num_pages), ("v_pages", v_pages, desc.num_pages),
+                           ("k_dst", k_dst, None), ("v_dst", v_dst, k_dst.shape[0])):
+        _expect(name, t, (pages,) + row, _code_dtypes(fp8), dev)
+    _expect("block_table", block_table, (B, desc.max_pages_per_seq), i32, dev)
+    _expect("seq_lens", seq_lens, (B,), i32, dev)
+    _expect("dst_table", dst_table, (B, None), i32, dev)
+    _expect("kept", kept, (B, hkv, int(budget)), i32, dev)
+    _expect("new_lens", new_lens, (B,), i32, dev)
+    _expect("workspace", workspace, (None,), (torch.uint8,), dev)
+    _expect_score("score", score, B, hkv, desc.max_seq_len, dev)
+    if score_out is not None:
+        _expect_score("score_out", score_out, B, hkv, int(budget), dev)
+    with _on_device(dev, stream) as st:
+        code = lib.quail_paged_kv_evict(
+            ctypes.byref(desc), int(budget), int(recent), _ptr(k_pages), _ptr(v_pages),
+            _ptr(block_table), _ptr(seq_lens), _ptr(score), score.shape[2], _ptr(dst_table),
+            dst_table.shape[1], k_dst.shape[0], _ptr(k_dst), _ptr(v_dst), _ptr(kept),
+            _ptr(new_lens), _ptr(score_out), 0 if score_out is None else score_out.shape[2],
+            _ptr(workspace), workspace.numel(), st)
+    _check(code, "quail_paged_kv_evict")
 
 
 def get_device_error(stream=None) -> int:

@@ -17,8 +17,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libquail.so")
-SOURCES = ["api.cu", "cascade.cu", "head.cu", "kv_plan.cu", "noalloc.cu", "prefill.cu",
-           "quantize.cu", "select.cu", "shard.cu"]
+SOURCES = ["api.cu", "api_paged.cu", "cascade.cu", "evict.cu", "head.cu", "kv_plan.cu",
+           "noalloc.cu", "paged.cu", "prefill.cu", "quantize.cu", "scores.cu", "select.cu",
+           "shard.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -106,6 +106,30 @@ bool valid_group(int g) { return g == 1 || g == 2 || g == 4 || g == 8 || g == 16
 
 }  // namespace
 
+int quail::current_device_info(DeviceInfo* info) {
+  DeviceState* st = nullptr;
+  const quail_status s = device_state(&st);
+  if (s != QUAIL_OK) return s;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  *info = DeviceInfo{st->num_sms, st->err_word, g_timeout_ns};
+  return QUAIL_OK;
+}
+
+bool quail::encode_rows_bf16(CUtensorMap* m, const void* base, int64_t tokens, int64_t row_stride,
+                             int heads, int d, int box_heads, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
+                                 static_cast<cuuint64_t>(row_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" {
 
 const char* quail_version(void) { return "quail-gb300 0.1"; }

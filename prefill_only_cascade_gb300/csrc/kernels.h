@@ -3,6 +3,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "quail.h"
@@ -145,6 +146,120 @@ struct CascadeMaps {
 // Which d = 128 fused calls run the CTA-pair kernel: QUAIL_CTA_PAIRS_OFF / _AUTO (the
 // default) / _ALWAYS.
 void set_cta_pairs(int mode);
+
+// ---- paged cache (paged.cu, scores.cu, evict.cu)
+// What the entry points outside api.cu need of the current device.
+struct DeviceInfo {
+  int num_sms;
+  unsigned* err_word;
+  uint64_t timeout_ns;
+};
+// A quail_status; `info` is filled when it is QUAIL_OK.
+int current_device_info(DeviceInfo* info);
+// 3-D bf16 tensor map over [tokens, heads, d] rows `row_stride` elements apart, 128-byte
+// swizzle, box (64 of d, box_heads, box_rows); out-of-range rows read as zero.
+bool encode_rows_bf16(CUtensorMap* m, const void* base, int64_t tokens, int64_t row_stride,
+                      int heads, int d, int box_heads, int box_rows);
+
+struct PagedAppendArgs {
+  int num_seqs, hkv, head_dim, row_elems;  // row_elems = hkv * head_dim
+  int max_len, page_shift, max_pages, num_pages;
+  int64_t total_new, k_stride, v_stride;   // elements between token rows
+  const uint16_t* k_new;                   // bf16
+  const uint16_t* v_new;
+  const int32_t* new_offsets;              // NULL: one token per sequence
+  const int32_t* start_pos;
+  const int32_t* table;
+  const float* k_scale;
+  const float* v_scale;
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  unsigned* err_word;
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, bool fp8, int num_sms,
+                                cudaStream_t stream);
+
+// What a CTA of the decode attention leaves for the join: the (sequence, head) that begins
+// in it and goes on in the next CTAs (seq < 0: none), and the tile after its last.
+struct DecodeRec {
+  int64_t total;
+  int seq, head;
+  int64_t end;
+};
+struct PagedDecodeArgs {
+  int num_seqs, hq, hkv, group;
+  int max_len, page_shift, max_pages, num_pages;
+  float scale_log2;                 // softmax scale * log2(e)
+  const __nv_bfloat16* q;
+  int64_t q_stride;                 // elements between the sequences' rows
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const int32_t* table;
+  const int32_t* lens;
+  const float* k_scale;
+  const float* v_scale;
+  __nv_bfloat16* out;
+  float* lse;
+  const float* score_in;
+  float* score_out;
+  int64_t score_stride;
+  // workspace
+  DecodeRec* rec;                   // [CTAs]
+  float2* part_ml;                  // [2 CTAs][group] max (log2 units) and sum
+  float* part_o;                    // [2 CTAs][group][d]
+  float* lse2;                      // [B, Hq], with scores only
+  float* raw;                       // [B, Hq, raw_stride] scores in log2 units, or NULL
+  int64_t raw_stride;
+  unsigned* err_word;
+};
+constexpr int kDecodeMaxCtas = 480;
+int decode_tile_keys(int head_dim, bool fp8);
+int decode_ctas(int num_sms, int num_seqs, int hkv, int max_len, int tile, int nt);
+cudaError_t launch_paged_decode(PagedDecodeArgs& a, int head_dim, bool fp8, int num_sms,
+                                cudaStream_t stream);
+
+struct AttnScoresArgs {
+  int num_seqs, hq, hkv, group;
+  int64_t total_q, total_k;
+  int max_q, max_k, window;
+  bool causal;
+  float scale_log2;
+  const float* lse;
+  const int32_t* q_offsets;
+  const int32_t* k_offsets;
+  const float* score_in;
+  float* score_out;
+  int64_t score_stride;
+  unsigned* err_word;
+  uint64_t timeout_ns;
+};
+cudaError_t launch_attn_scores(const AttnScoresArgs& a, const CUtensorMap& q_map,
+                               const CUtensorMap& k_map, int head_dim, int num_sms,
+                               cudaStream_t stream);
+
+struct PagedEvictArgs {
+  int num_seqs, hkv, row_bytes;      // row_bytes of one (token, head)
+  int max_len, page_shift, max_pages, num_pages;
+  int budget, recent;
+  int dst_max_pages, dst_num_pages;
+  bool same_pool;
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const int32_t* table;
+  const int32_t* lens;
+  const float* score;
+  int64_t score_stride;
+  const int32_t* dst_table;
+  uint8_t* k_dst;
+  uint8_t* v_dst;
+  int32_t* kept;
+  int32_t* new_lens;
+  float* score_out;
+  int64_t score_out_stride;
+  int32_t* marks;                    // workspace: [dst_num_pages]
+  unsigned* err_word;
+};
+cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_t stream);
 
 constexpr int kFused = 0, kAnchorPass = 1, kSuffixPass = 2;
 

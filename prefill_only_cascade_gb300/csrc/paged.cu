@@ -1,0 +1,861 @@
+// paged.cu - a paged key/value cache: rows written into pages, and attention of one new
+// token per sequence over them. "Motor de inferência Quail atinge 1 bilhão de tokens por
+// minuto por GPU", section "Como funciona", keeps anchor KV between prefills; pages let it
+// be kept, grown and cut token by token. A page is [page_size, Hkv, d], the token-row
+// layout of every K/V tensor of the library, so a contiguous [T, Hkv, d] tensor is itself
+// a pool whose pages follow one another.
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace quail {
+
+namespace {
+
+// ------------------------------------------------------------------ append
+// One block takes `tok` consecutive new tokens: its first threads find each token's
+// sequence and slot, then all threads move 16-byte source vectors (8 values), K and V of
+// one token row after the other. Bound by HBM (2 bytes read, 2 or 1 written per value).
+constexpr int kAppendThreads = 256;
+constexpr int kAppendMaxTok = 64;
+
+// Eight bf16 -> eight E4M3 codes of RN32(x / s), rounded to nearest even, saturating at
+// +-448. r = RN(1/s). For an ordinary scale the quotient is RN(x r) with one FMA correction
+// by its exact residual (Markstein, "IA-64 and Elementary Functions", 2000), which is the
+// IEEE quotient wherever a code can be other than zero: |x| >= 2^-10 |s| keeps the residual
+// out of the subnormals for s in [2^-60, 2^60]. An infinite quotient (x infinite, or x / s
+// past fp32) has no residual and is used as it is. Other scales divide.
+__device__ __forceinline__ uint2 encode_bf16x8(const uint4& raw, float s, float r, bool plain) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t packed[2] = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float x[2] = {__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (plain) {
+        const float q = x[j] * r;
+        const float c = fmaf(fmaf(-q, s, x[j]), r, q);
+        // x's sign restores -0 / s, which the correction rounds to +0
+        x[j] = fabsf(q) < 1e30f ? copysignf(c, x[j]) : q;
+      } else {
+        x[j] = __fdiv_rn(x[j], s);
+      }
+    }
+    const __nv_fp8x2_storage_t c =
+        __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+    packed[k >> 1] |= static_cast<uint32_t>(c) << (16 * (k & 1));
+  }
+  return make_uint2(packed[0], packed[1]);
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const PagedAppendArgs a,
+                                                                      int tok) {
+  __shared__ int64_t s_slot[kAppendMaxTok];
+  __shared__ int s_seq[kAppendMaxTok];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
+  const int n = static_cast<int>(min(static_cast<int64_t>(tok), a.total_new - t0));
+  if (threadIdx.x < n) {
+    const int64_t t = t0 + threadIdx.x;
+    int b = static_cast<int>(t);
+    int64_t i = 0;
+    bool ok = true;
+    if (a.new_offsets != nullptr) {
+      int lo = 0, hi = a.num_seqs;  // the last sequence that begins at or before t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.new_offsets + mid) <= t) lo = mid; else hi = mid;
+      }
+      b = lo;
+      const int64_t o0 = __ldg(a.new_offsets + b);
+      i = t - o0;
+      ok = o0 <= t && t < __ldg(a.new_offsets + b + 1);
+    }
+    int64_t slot = -1;
+    if (ok) {
+      const int64_t start = __ldg(a.start_pos + b);
+      const int64_t pos = start + i;
+      if (start >= 0 && pos < a.max_len) {
+        const int page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages +
+                               (pos >> a.page_shift));
+        if (page >= 0 && page < a.num_pages)
+          slot = (static_cast<int64_t>(page) << a.page_shift) +
+                 (pos & ((1 << a.page_shift) - 1));
+      }
+    }
+    if (slot < 0) atomicOr(a.err_word, kErrDeviceBounds);
+    s_slot[threadIdx.x] = slot;
+    s_seq[threadIdx.x] = b;
+  }
+  // the offsets as a whole: increasing from 0 to the number of new rows
+  if (blockIdx.x == 0 && a.new_offsets != nullptr) {
+    for (int b = threadIdx.x; b <= a.num_seqs; b += kAppendThreads) {
+      const int64_t o = __ldg(a.new_offsets + b);
+      const int64_t next = b < a.num_seqs ? __ldg(a.new_offsets + b + 1) : a.total_new;
+      if ((b == 0 && o != 0) || (b < a.num_seqs ? next < o : next != o))
+        atomicOr(a.err_word, kErrDeviceBounds);
+    }
+  }
+  __syncthreads();
+  const int vecs = a.row_elems / 8;  // 16-byte source vectors of a token row
+  const int total = n * 2 * vecs;
+  for (int u = threadIdx.x; u < total; u += kAppendThreads) {
+    const int row = u / vecs, c = u - row * vecs;
+    const int t = row >> 1, is_v = row & 1;
+    const int64_t slot = s_slot[t];
+    if (slot < 0) continue;
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(
+        (is_v ? a.v_new : a.k_new) + (t0 + t) * (is_v ? a.v_stride : a.k_stride) + 8 * c));
+    if (FP8) {
+      const int g = (8 * c) / a.head_dim;
+      const float s = __ldg((is_v ? a.v_scale : a.k_scale) +
+                            static_cast<int64_t>(s_seq[t]) * a.hkv + g);
+      const bool plain = s >= 8.673617379884035e-19f && s <= 1.152921504606847e18f;  // 2^-60, 2^60
+      *reinterpret_cast<uint2*>((is_v ? a.v_pages : a.k_pages) + slot * a.row_elems + 8 * c) =
+          encode_bf16x8(x, s, __frcp_rn(s), plain);
+    } else {
+      *reinterpret_cast<uint4*>((is_v ? a.v_pages : a.k_pages) + 2 * (slot * a.row_elems + 8 * c)) =
+          x;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ decode attention
+// o[b, h] = sum_j w_j v_j with w_j = exp(c q.k_j - lse) over the j < len[b] cached tokens;
+// every K and V byte is read once for the G query heads that share it, so HBM bounds it.
+//
+// The tiles (kTile keys of one sequence and KV head) of the whole batch are numbered in
+// the order sequence, head, position, and each CTA takes an equal run of them, whatever
+// the lengths are: short sequences share a CTA, long ones spread over many. A sequence's
+// head that lies inside one CTA is finished there; the others leave (max, sum, O) partials
+// that paged_join_kernel rescales and adds. Each warp walks its own keys of the tile with a
+// running max and sum; K and V of its next keys are in registers while it works on the
+// present ones.
+//
+// Both products run on mma.sync m16n8k16: one new token gives at most 16 query rows per KV
+// head, so the padded products cost 3 % of the tensor rate of the legacy pipe and K/V need
+// no staging in shared memory: since sums over d (scores) and the order of d (output rows)
+// may be permuted freely, plain 16-byte row loads ARE the operand fragments.
+//   S  [16 heads x 8 keys]  A = Q (rows: heads), B = K: lane (r, q) holds key r, chunk q + 4i
+//   O^T [16 d x 8 heads]    A = V^T: lane (r, q) holds keys 2q, 2q+1, 2q+8, 2q+9, chunk r
+//                           (two keys' values interleaved by byte permutes), B = P, whose
+//                           fragment is the score fragment packed in place
+// bf16 pages: bf16 products, P as the sum of two bf16 (hi + lo: 16 bits of P). e4m3 pages:
+// f16 products (codes are exact in f16), P in f16 (11 bits, scaled by 2^14 so that weights
+// down to 2^-38 of the largest count), Q scaled per head by a power of two into f16's
+// range: q bits below 2^-38 of the head's largest |q| are lost, under fp32's own rounding.
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = kDecWarps * 32;
+
+template <int D, bool FP8>
+struct DecCfg {
+  static constexpr int kRB = D * (FP8 ? 1 : 2);      // bytes of a (token, head) row
+  static constexpr int kKChunks = kRB / 64;          // 16-byte K loads per lane and key
+  static constexpr int kKG = 8 / kKChunks;           // groups of 8 keys per warp step
+  static constexpr int kKeys = 8 * kKG;              // keys per warp step: 16, 32 or 64
+  static constexpr int kSteps16 = kKeys / 16;
+  static constexpr int kVWords = kRB / 32;           // 32-bit words per lane and V row
+  static constexpr int kTile = kDecWarps * kKeys;    // keys per CTA tile
+  static constexpr int kMT = D / 16;                 // 16-row tiles of O^T
+  static constexpr int kQS = D / 16;                 // k-steps of the score product
+};
+
+__device__ __forceinline__ uint4 ld_kv16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_kv8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "l"(p));
+  return v;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes (the low or the high half of w) -> f16x2, exact.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+      : "=r"(h)
+      : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+      : "=r"(h)
+      : "r"(w));
+  return h;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The d of lane row r's first output row in tile t (its second is the next d).
+template <int D, bool FP8>
+__device__ __forceinline__ int out_d(int r, int t) {
+  if (D == 128 && !FP8) return (r + 8 * (t >> 2)) * 8 + 2 * (t & 3);
+  if (D == 128) return r * 16 + 2 * t;
+  return r * 8 + 2 * t;
+}
+
+// First tile of CTA c when `total` tiles are dealt to n CTAs.
+__device__ __forceinline__ int64_t first_tile(int c, int64_t total, int n) {
+  return static_cast<int64_t>(c) * total / n;
+}
+
+// The length of sequence b if it is one the call allows, else -1.
+__device__ __forceinline__ int checked_len(const PagedDecodeArgs& a, int b) {
+  const int n = __ldg(a.lens + b);
+  return n >= 0 && n <= a.max_len ? n : -1;
+}
+
+// Where a CTA's run begins, and the record the join reads.
+struct RunStart {
+  int64_t total;   // tiles of the batch
+  int64_t begin;   // first tile of this CTA
+  int64_t end;     // one past its last
+  int seq;         // sequence of tile `begin`
+  int64_t seq_tile0;  // first tile of that sequence
+};
+
+// Scans the lengths: tiles of the batch, this CTA's run, the sequence it begins in. Every
+// CTA scans for itself (a few KB from L2), which costs less than a launch before this one.
+__device__ RunStart find_run(const PagedDecodeArgs& a, int tile, int cta, int ctas) {
+  __shared__ int64_t s_sum[kDecWarps];
+  __shared__ RunStart s_run;
+  const int per = (a.num_seqs + kDecThreads - 1) / kDecThreads;
+  const int b0 = min(static_cast<int>(threadIdx.x) * per, a.num_seqs);
+  const int b1 = min(b0 + per, a.num_seqs);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = checked_len(a, b);
+    mine += n > 0 ? (n + tile - 1) / tile : 0;
+  }
+  mine *= a.hkv;
+  int64_t x = mine;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) s_sum[warp] = x;
+  __syncthreads();
+  int64_t before = x - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  const int64_t begin = first_tile(cta, total, ctas);
+  if (threadIdx.x == 0) s_run = RunStart{total, begin, first_tile(cta + 1, total, ctas), -1, 0};
+  __syncthreads();
+  if (mine > 0 && begin >= before && begin < before + mine) {
+    int64_t at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int n = checked_len(a, b);
+      const int64_t t = n > 0 ? static_cast<int64_t>((n + tile - 1) / tile) * a.hkv : 0;
+      if (begin < at + t) {
+        s_run.seq = b;
+        s_run.seq_tile0 = at;
+        break;
+      }
+      at += t;
+    }
+  }
+  __syncthreads();
+  return s_run;
+}
+
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
+    paged_decode_kernel(const PagedDecodeArgs a) {
+  using C = DecCfg<D, FP8>;
+  __shared__ float s_m[kDecWarps][8 * NT], s_l[kDecWarps][8 * NT];
+  __shared__ alignas(16) float s_o[kDecWarps][8 * NT][D];
+  __shared__ int s_bad;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = lane >> 2, q4 = lane & 3;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int G = a.group;
+
+  // sequences without tokens (0 and -inf) and with lengths out of range (NaN)
+  for (int b = cta; b < a.num_seqs; b += ctas) {
+    const int n = checked_len(a, b);
+    if (n > 0) continue;
+    const float nan = __int_as_float(0x7FFFFFFF);
+    if (n < 0 && threadIdx.x == 0) atomicOr(a.err_word, kErrDeviceBounds);
+    for (int i = threadIdx.x; i < a.hq * D; i += kDecThreads)
+      a.out[static_cast<int64_t>(b) * a.hq * D + i] = __float2bfloat16(n < 0 ? nan : 0.f);
+    if (a.lse != nullptr)
+      for (int i = threadIdx.x; i < a.hq; i += kDecThreads)
+        a.lse[static_cast<int64_t>(b) * a.hq + i] = n < 0 ? nan : -INFINITY;
+  }
+
+  const RunStart run = find_run(a, C::kTile, cta, ctas);
+  if (threadIdx.x == 0) a.rec[cta] = DecodeRec{run.total, -1, -1, 0};
+  if (run.begin >= run.end) return;
+  int b = run.seq;
+  int len = checked_len(a, b);
+  int tiles = (len + C::kTile - 1) / C::kTile;
+  int g = static_cast<int>((run.begin - run.seq_tile0) / tiles);
+  int64_t piece0 = run.seq_tile0 + static_cast<int64_t>(g) * tiles;  // first tile of (b, g)
+  int64_t at = run.begin;
+
+  const int64_t row_stride = static_cast<int64_t>(a.hkv) * C::kRB;
+  while (true) {
+    // ---------------------------------------------------- one piece: keys [kb, ke) of (b, g)
+    const int64_t stop = min(run.end, piece0 + tiles);
+    const int kb = static_cast<int>(at - piece0) * C::kTile;
+    const int ke = min(len, static_cast<int>(stop - piece0) * C::kTile);
+    if (threadIdx.x == 0) s_bad = 0;
+
+    // Q fragments: 4 values of d per k-step; heads past the group are zero rows
+    uint32_t qa[C::kQS][2 * NT];
+    float c_log2[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = r + 8 * n;
+      const bool has = h < G;
+      const __nv_bfloat16* qp =
+          a.q + static_cast<int64_t>(b) * a.q_stride + static_cast<int64_t>(g * G + h) * D;
+      uint2 w[C::kQS];
+      constexpr int EC = FP8 ? 16 : 8;  // values per K chunk
+#pragma unroll
+      for (int ks = 0; ks < C::kQS; ++ks) {
+        const int off = (q4 + 4 * (ks / (EC / 4))) * EC + 4 * (ks % (EC / 4));
+        w[ks] = has ? __ldg(reinterpret_cast<const uint2*>(qp + off)) : make_uint2(0u, 0u);
+      }
+      c_log2[n] = a.scale_log2;
+      if (FP8) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int ks = 0; ks < C::kQS; ++ks)
+          top = absmax_bf16x2(absmax_bf16x2(top, w[ks].x), w[ks].y);
+        float mx = absmax_bf16x2_value(top);
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        // 2^e with mx 2^e in [2^14, 2^15); zero, infinite and NaN rows are left as they are
+        int e = mx > 0.f && mx < INFINITY ? 14 - (static_cast<int>(__float_as_uint(mx) >> 23) - 127) : 0;
+        e = min(e, 126);  // a power of two that is a normal float, as is its inverse
+        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        c_log2[n] *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        c_log2[n] *= __ldg(a.k_scale + static_cast<int64_t>(b) * a.hkv + g);
+#pragma unroll
+        for (int ks = 0; ks < C::kQS; ++ks) {
+          w[ks].x = pack2<true>(__uint_as_float(w[ks].x << 16) * up,
+                                __uint_as_float(w[ks].x & 0xFFFF0000u) * up);
+          w[ks].y = pack2<true>(__uint_as_float(w[ks].y << 16) * up,
+                                __uint_as_float(w[ks].y & 0xFFFF0000u) * up);
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < C::kQS; ++ks) {
+        qa[ks][2 * n] = w[ks].x;
+        qa[ks][2 * n + 1] = w[ks].y;
+      }
+    }
+
+    float o[NT][C::kMT][4];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n] = -INFINITY;
+      l[n] = 0.f;
+#pragma unroll
+      for (int t = 0; t < C::kMT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[n][t][j] = 0.f;
+    }
+
+    const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
+    const uint8_t* kg_base = a.k_pages + static_cast<int64_t>(g) * C::kRB;
+    const uint8_t* vg_base = a.v_pages + static_cast<int64_t>(g) * C::kRB;
+    bool bad = false;
+    uint4 kr[C::kKG][C::kKChunks];
+    uint32_t vr[C::kSteps16][4][C::kVWords];
+    int64_t slot[C::kSteps16];  // pool row of each 16-key block of the next step; < 0: none
+
+    auto lookup = [&](int key0) {
+#pragma unroll
+      for (int i = 0; i < C::kSteps16; ++i) {
+        const int pos = key0 + 16 * i;
+        slot[i] = -1;
+        if (pos < ke) {
+          const int page = __ldg(table + (pos >> a.page_shift));
+          if (page >= 0 && page < a.num_pages)
+            slot[i] = (static_cast<int64_t>(page) << a.page_shift) +
+                      (pos & ((1 << a.page_shift) - 1));
+          else
+            bad = true;
+        }
+      }
+    };
+    auto load_k = [&](int key0) {
+#pragma unroll
+      for (int kg = 0; kg < C::kKG; ++kg) {
+        const int64_t s = slot[kg >> 1];
+        const bool ok = s >= 0 && key0 + 8 * kg + r < ke;
+        const uint8_t* p = kg_base + (s + 8 * (kg & 1) + r) * row_stride + 16 * q4;
+#pragma unroll
+        for (int i = 0; i < C::kKChunks; ++i)
+          kr[kg][i] = ok ? ld_kv16(p + 64 * i) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto load_v = [&](int key0) {
+#pragma unroll
+      for (int i = 0; i < C::kSteps16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int kk = 2 * q4 + (j & 1) + 8 * (j >> 1);
+          const bool ok = slot[i] >= 0 && key0 + 16 * i + kk < ke;
+          const uint8_t* p = vg_base + (slot[i] + kk) * row_stride;
+          if constexpr (C::kVWords == 2) {
+            const uint2 x = ok ? ld_kv8(p + 8 * r) : make_uint2(0u, 0u);
+            vr[i][j][0] = x.x;
+            vr[i][j][1] = x.y;
+          } else {
+#pragma unroll
+            for (int c = 0; c < C::kVWords / 4; ++c) {
+              const uint4 x = ok ? ld_kv16(p + 16 * (r + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+              vr[i][j][4 * c] = x.x;
+              vr[i][j][4 * c + 1] = x.y;
+              vr[i][j][4 * c + 2] = x.z;
+              vr[i][j][4 * c + 3] = x.w;
+            }
+          }
+        }
+    };
+
+    int key0 = kb + warp * C::kKeys;
+    lookup(key0);
+    load_k(key0);
+    load_v(key0);
+    lookup(key0 + C::kTile);
+    for (; key0 < ke; key0 += C::kTile) {
+      // ---- scores of this step's keys
+      float s[C::kKG][4];
+#pragma unroll
+      for (int kg = 0; kg < C::kKG; ++kg) {
+        s[kg][0] = s[kg][1] = s[kg][2] = s[kg][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < C::kKChunks; ++i) {
+          const uint32_t w[4] = {kr[kg][i].x, kr[kg][i].y, kr[kg][i].z, kr[kg][i].w};
+          if (FP8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int ks = 4 * i + j;
+              mma16816<true>(s[kg], qa[ks][0], NT == 2 ? qa[ks][2 * NT - 2] : 0u, qa[ks][1],
+                             NT == 2 ? qa[ks][2 * NT - 1] : 0u, e4m3_lo(w[j]), e4m3_hi(w[j]));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int ks = 2 * i + j;
+              mma16816<false>(s[kg], qa[ks][0], NT == 2 ? qa[ks][2 * NT - 2] : 0u, qa[ks][1],
+                              NT == 2 ? qa[ks][2 * NT - 1] : 0u, w[2 * j], w[2 * j + 1]);
+            }
+          }
+        }
+      }
+      const int next = key0 + C::kTile;
+      if (next < ke) load_k(next);
+
+      // ---- running max and sum; x = score in log2 units
+      float p[NT][C::kKG][2];
+      float mx[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mx[n] = -INFINITY;
+#pragma unroll
+        for (int kg = 0; kg < C::kKG; ++kg)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const bool see = key0 + 8 * kg + 2 * q4 + j < ke;
+            const float x = see ? s[kg][2 * n + j] * c_log2[n] : -INFINITY;
+            p[n][kg][j] = x;
+            mx[n] = fmaxf(mx[n], x);
+          }
+        if (a.raw != nullptr && r + 8 * n < G) {
+          float* row = a.raw + (static_cast<int64_t>(b) * a.hq + g * G + r + 8 * n) * a.raw_stride;
+#pragma unroll
+          for (int kg = 0; kg < C::kKG; ++kg)  // rows are padded to whole tiles
+            *reinterpret_cast<float2*>(row + key0 + 8 * kg + 2 * q4) =
+                make_float2(p[n][kg][0], p[n][kg][1]);
+        }
+        mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xFFFFFFFFu, mx[n], 1));
+        mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xFFFFFFFFu, mx[n], 2));
+      }
+      bool grew = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) grew |= mx[n] > m[n];
+      if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float to = fmaxf(m[n], mx[n]);
+          const float f = m[n] == -INFINITY ? 0.f : ex2(m[n] - to);
+          l[n] *= f;
+          m[n] = to;
+          const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * q4);
+          const float f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * q4 + 4);
+#pragma unroll
+          for (int t = 0; t < C::kMT; ++t) {
+            o[n][t][0] *= f0;
+            o[n][t][1] *= f1;
+            o[n][t][2] *= f0;
+            o[n][t][3] *= f1;
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        // a row that has seen nothing but -inf takes 0 as its reference: its weights are 0
+        const float ref = (m[n] == -INFINITY ? 0.f : m[n]) - (FP8 ? 14.f : 0.f);
+#pragma unroll
+        for (int kg = 0; kg < C::kKG; ++kg)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            p[n][kg][j] = ex2(p[n][kg][j] - ref);
+            l[n] += p[n][kg][j];
+          }
+      }
+
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int i = 0; i < C::kSteps16; ++i) {
+        uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float* x = p[n][2 * i + h];
+            hi[n][h] = pack2<FP8>(x[0], x[1]);
+            lo[n][h] = FP8 ? 0u
+                           : pack2<false>(x[0] - __uint_as_float(hi[n][h] << 16),
+                                          x[1] - __uint_as_float(hi[n][h] & 0xFFFF0000u));
+          }
+        if (FP8) {
+#pragma unroll
+          for (int w = 0; w < C::kVWords; ++w)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;
+              const uint32_t x = __byte_perm(vr[i][0][w], vr[i][1][w], sel);
+              const uint32_t y = __byte_perm(vr[i][2][w], vr[i][3][w], sel);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma16816<true>(o[n][2 * w + h], e4m3_lo(x), e4m3_hi(x), e4m3_lo(y), e4m3_hi(y),
+                               hi[n][0], hi[n][1]);
+            }
+        } else {
+#pragma unroll
+          for (int t = 0; t < C::kMT; ++t) {
+            const uint32_t a0 = __byte_perm(vr[i][0][t], vr[i][1][t], 0x5410);
+            const uint32_t a1 = __byte_perm(vr[i][0][t], vr[i][1][t], 0x7632);
+            const uint32_t a2 = __byte_perm(vr[i][2][t], vr[i][3][t], 0x5410);
+            const uint32_t a3 = __byte_perm(vr[i][2][t], vr[i][3][t], 0x7632);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816<false>(o[n][t], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+              mma16816<false>(o[n][t], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+            }
+          }
+        }
+      }
+      if (next < ke) load_v(next);
+      lookup(next + C::kTile);
+    }
+
+    // ---------------------------------------------------- the four warps' parts together
+    __syncthreads();  // s_bad is 0, the last piece's s_* were read
+    if (bad) s_bad = 1;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 1);
+      l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 2);
+      if (q4 == 0) {
+        s_m[warp][8 * n + r] = m[n];
+        s_l[warp][8 * n + r] = l[n];
+      }
+#pragma unroll
+      for (int t = 0; t < C::kMT; ++t) {
+        const int d = out_d<D, FP8>(r, t);
+        const int h0 = 8 * n + 2 * q4;
+        if (h0 < G)
+          *reinterpret_cast<float2*>(&s_o[warp][h0][d]) = make_float2(o[n][t][0], o[n][t][2]);
+        if (h0 + 1 < G)
+          *reinterpret_cast<float2*>(&s_o[warp][h0 + 1][d]) = make_float2(o[n][t][1], o[n][t][3]);
+      }
+    }
+    __syncthreads();
+    const bool whole = at == piece0 && stop == piece0 + tiles;
+    // slot 0: the run began inside this (b, g); slot 1: the run's last, begun here
+    const int64_t part = 2 * static_cast<int64_t>(cta) + (at == piece0 ? 1 : 0);
+    const float vs = FP8 ? __ldg(a.v_scale + static_cast<int64_t>(b) * a.hkv + g) : 1.f;
+    for (int i = threadIdx.x; i < G * D; i += kDecThreads) {
+      const int h = i / D, d = i % D;
+      float top = s_m[0][h];
+#pragma unroll
+      for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, s_m[w][h]);
+      float sum = 0.f, acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float f = s_m[w][h] == -INFINITY ? 0.f : ex2(s_m[w][h] - top);
+        sum = fmaf(s_l[w][h], f, sum);
+        acc = fmaf(s_o[w][h][d], f, acc);
+      }
+      if (s_bad) sum = __int_as_float(0x7FFFFFFF);
+      const int64_t row = static_cast<int64_t>(b) * a.hq + g * G + h;
+      if (whole) {
+        a.out[row * D + d] = __float2bfloat16(acc / sum * vs);
+        if (d == 0) {
+          const float lse2 = top + (log2f(sum) - (FP8 ? 14.f : 0.f));
+          if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
+          if (a.lse2 != nullptr) a.lse2[row] = lse2;
+        }
+      } else {
+        a.part_o[(part * G + h) * D + d] = acc;
+        if (d == 0) a.part_ml[part * G + h] = make_float2(top, sum);
+      }
+    }
+    if (threadIdx.x == 0 && s_bad) atomicOr(a.err_word, kErrDeviceBounds);
+    if (threadIdx.x == 0 && !whole) {
+      if (at == piece0)  // begun here, goes on in the next CTAs: the join's entry
+        a.rec[cta] = DecodeRec{run.total, b, g, piece0 + tiles};
+    }
+
+    // ---------------------------------------------------- the next (sequence, head)
+    at = stop;
+    if (at >= run.end) return;
+    piece0 = stop;
+    if (++g == a.hkv) {
+      g = 0;
+      do {
+        len = checked_len(a, ++b);
+      } while (len <= 0);
+      tiles = (len + C::kTile - 1) / C::kTile;
+    }
+    __syncthreads();  // everyone has read s_bad
+  }
+}
+
+// Joins the partials of every (sequence, head) that more than one CTA worked on. Its CTAs
+// are c0 (where it begins, with its record) .. c1; their blocks here share its query heads:
+// block c0 + k takes heads k, k + (c1 - c0 + 1), ... One warp of lanes holds the head's
+// values (4 each) and the block's warps take the partials in turn.
+template <int D>
+__global__ void __launch_bounds__(kDecThreads) paged_join_kernel(const PagedDecodeArgs a, int ctas,
+                                                                 float l_shift) {
+  constexpr int kLanes = D / 4;                    // lanes that hold one head's output
+  constexpr int kRows = kDecThreads / kLanes;      // partials read at once
+  __shared__ alignas(16) float s_acc[kRows][D];
+  __shared__ float s_top[kRows], s_sum[kRows];
+  __shared__ int s_c0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int G = a.group;
+  // A block has up to two parts: the piece that begins in its CTA, and the one that began
+  // before and goes through or ends in it.
+  for (int pass = 0; pass < 2; ++pass) {
+    int c0 = blockIdx.x;
+    if (pass == 1) {  // the nearest of the G - 1 CTAs before this one that begins such a piece
+      __syncthreads();
+      if (threadIdx.x == 0) s_c0 = -1;
+      __syncthreads();
+      const int c = static_cast<int>(blockIdx.x) - 1 - static_cast<int>(threadIdx.x);
+      if (threadIdx.x < G - 1 && c >= 0 && a.rec[c].seq >= 0) atomicMax(&s_c0, c);
+      __syncthreads();
+      c0 = s_c0;
+      if (c0 < 0) continue;
+    }
+    const DecodeRec rec = a.rec[c0];
+    if (rec.seq < 0) continue;
+    // the last CTA of the piece: the one that holds tile end - 1
+    const int c1 = static_cast<int>((rec.end * ctas - 1) / rec.total);
+    const int k = static_cast<int>(blockIdx.x) - c0;
+    if (c0 + k > c1) continue;
+    for (int h = k; h < G; h += c1 - c0 + 1) {
+      const int rowi = threadIdx.x / kLanes, d = 4 * (threadIdx.x % kLanes);
+      float top = -INFINITY, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int c = c0 + rowi; c <= c1; c += kRows) {
+        // with fewer tiles than CTAs some have none
+        if (first_tile(c, rec.total, ctas) == first_tile(c + 1, rec.total, ctas)) continue;
+        const int64_t part = 2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0);
+        const float2 ml = a.part_ml[part * G + h];
+        const float4 x = *reinterpret_cast<const float4*>(a.part_o + (part * G + h) * D + d);
+        const float to = fmaxf(top, ml.x);
+        const float f = top == -INFINITY ? 0.f : ex2(top - to);
+        const float e = ml.x == -INFINITY ? 0.f : ex2(ml.x - to);
+        top = to;
+        sum = fmaf(sum, f, ml.y * e);
+        if (ml.y != ml.y) sum = ml.y;  // a bad page: NaN, whatever its max was
+        acc.x = fmaf(acc.x, f, x.x * e);
+        acc.y = fmaf(acc.y, f, x.y * e);
+        acc.z = fmaf(acc.z, f, x.z * e);
+        acc.w = fmaf(acc.w, f, x.w * e);
+      }
+      __syncthreads();
+      *reinterpret_cast<float4*>(&s_acc[rowi][d]) = acc;
+      if (d == 0) {
+        s_top[rowi] = top;
+        s_sum[rowi] = sum;
+      }
+      __syncthreads();
+      if (threadIdx.x < D) {
+        float t = s_top[0];
+#pragma unroll
+        for (int i = 1; i < kRows; ++i) t = fmaxf(t, s_top[i]);
+        float total = 0.f, val = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const float f = s_top[i] == -INFINITY ? 0.f : ex2(s_top[i] - t);
+          total = s_sum[i] != s_sum[i] ? s_sum[i] : fmaf(s_sum[i], f, total);
+          val = fmaf(s_acc[i][threadIdx.x], f, val);
+        }
+        const int64_t row = static_cast<int64_t>(rec.seq) * a.hq + rec.head * G + h;
+        const float vs =
+            a.v_scale != nullptr ? __ldg(a.v_scale + static_cast<int64_t>(rec.seq) * a.hkv + rec.head)
+                                 : 1.f;
+        a.out[row * D + threadIdx.x] = __float2bfloat16(val / total * vs);
+        if (threadIdx.x == 0) {
+          const float lse2 = t + (log2f(total) - l_shift);
+          if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
+          if (a.lse2 != nullptr) a.lse2[row] = lse2;
+        }
+      }
+    }
+  }
+}
+
+// score_out[b, g, j] = score_in + sum over the group's heads of exp2(x - lse2), from the
+// scores that the attention left in the workspace (4 bytes per (head, token) against 4 d
+// or 2 d bytes of K and V per G of them).
+__global__ void __launch_bounds__(256) paged_weights_kernel(const PagedDecodeArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.x / a.hkv, g = blockIdx.x % a.hkv;
+  const int n = checked_len(a, b);
+  const int64_t row = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(g) * a.group;
+  const int64_t out_row = (static_cast<int64_t>(b) * a.hkv + g) * a.score_stride;
+  for (int j = blockIdx.y * 256 + threadIdx.x; j < n; j += gridDim.y * 256) {
+    float w = 0.f;
+    for (int h = 0; h < a.group; ++h) {
+      const float lse2 = a.lse2[row + h];
+      if (lse2 == lse2) w += ex2(a.raw[(row + h) * a.raw_stride + j] - lse2);
+    }
+    a.score_out[out_row + j] = (a.score_in != nullptr ? a.score_in[out_row + j] : 0.f) + w;
+  }
+}
+
+template <int D, bool FP8, int NT>
+cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
+  using C = DecCfg<D, FP8>;
+  const int ctas = decode_ctas(num_sms, a.num_seqs, a.hkv, a.max_len, C::kTile, NT);
+  paged_decode_kernel<D, FP8, NT><<<ctas, kDecThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  // the join is left out where no (sequence, head) can have more than one tile, unless the
+  // weights follow (which rely on it having waited for the attention)
+  if (e == cudaSuccess && (a.max_len > C::kTile || a.raw != nullptr)) {
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kDecThreads);
+    e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, ctas, FP8 ? 14.f : 0.f);
+  }
+  if (e == cudaSuccess && a.raw != nullptr && a.max_len > 0) {
+    const int chunks = (a.max_len + 255) / 256;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * a.hkv, chunks < 4096 ? chunks : 4096);
+    cfg.blockDim = dim3(256);
+    e = cudaLaunchKernelEx(&cfg, paged_weights_kernel, a);
+  }
+  return e;
+}
+
+}  // namespace
+
+int decode_tile_keys(int head_dim, bool fp8) {
+  return kDecWarps * 16 * (256 / (head_dim * (fp8 ? 1 : 2)));
+}
+
+int decode_ctas(int num_sms, int num_seqs, int hkv, int max_len, int tile, int nt) {
+  const int64_t most = static_cast<int64_t>(num_seqs) * hkv * ((max_len + tile - 1) / tile);
+  int64_t full = static_cast<int64_t>(num_sms) * (nt == 1 ? 3 : 2);
+  if (full > kDecodeMaxCtas) full = kDecodeMaxCtas;  // the workspace holds so many partials
+  return static_cast<int>(most < 1 ? 1 : most < full ? most : full);
+}
+
+cudaError_t launch_paged_decode(PagedDecodeArgs& a, int head_dim, bool fp8, int num_sms,
+                                cudaStream_t stream) {
+  const bool two = a.group > 8;
+  if (head_dim == 128) {
+    if (fp8) return two ? launch_decode_t<128, true, 2>(a, num_sms, stream)
+                        : launch_decode_t<128, true, 1>(a, num_sms, stream);
+    return two ? launch_decode_t<128, false, 2>(a, num_sms, stream)
+               : launch_decode_t<128, false, 1>(a, num_sms, stream);
+  }
+  if (fp8) return two ? launch_decode_t<64, true, 2>(a, num_sms, stream)
+                      : launch_decode_t<64, true, 1>(a, num_sms, stream);
+  return two ? launch_decode_t<64, false, 2>(a, num_sms, stream)
+             : launch_decode_t<64, false, 1>(a, num_sms, stream);
+}
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, bool fp8, int num_sms,
+                                cudaStream_t stream) {
+  // about 2,048 vectors per block where there are enough tokens, else one block per token
+  int64_t tok = 2048 / (2 * (a.row_elems / 8));
+  const int64_t spread = (a.total_new + 2 * num_sms - 1) / (2 * num_sms);
+  if (tok > spread) tok = spread;
+  if (tok > kAppendMaxTok) tok = kAppendMaxTok;
+  if (tok < 1) tok = 1;
+  const unsigned blocks = static_cast<unsigned>((a.total_new + tok - 1) / tok);
+  if (fp8)
+    paged_append_kernel<true><<<blocks, kAppendThreads, 0, stream>>>(a, static_cast<int>(tok));
+  else
+    paged_append_kernel<false><<<blocks, kAppendThreads, 0, stream>>>(a, static_cast<int>(tok));
+  return cudaGetLastError();
+}
+
+}  // namespace quail
