@@ -512,7 +512,8 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
  *            overlapping score: the kept tokens' scores, zeros behind them
  *   workspace: at least quail_paged_evict_workspace_size(desc, dst_num_pages) bytes,
  *            16-byte aligned, overwritten; calls that share one must not overlap on the GPU.
- * The scales of e4m3 pages stay those of the sequence. num_seqs * budget < 2^31.
+ * The scales of e4m3 pages stay those of the sequence. Limit: num_seqs * budget * Hkv <
+ * 2^38.
  */
 quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, int32_t recent,
                                   const void* k_pages, const void* v_pages,

@@ -391,59 +391,102 @@ def make_paged_desc(num_seqs, max_seq_len, num_pages, page_size, max_pages_per_s
                      float(softmax_scale), QUAIL_FP8_E4M3 if kv_fp8 else QUAIL_BF16)
 
 
-def _code_dtypes(fp8):
-    return (torch.float8_e4m3fn, torch.uint8) if fp8 else (torch.bfloat16,)
+# The paged calls run once per generated token, so their checks are written to be cheap: one
+# test per tensor, the reason worked out only when it fails, the stream's handle without a
+# Stream object, the device switched only when it is not the current one.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _expect(what, t, shape, dtypes, device, rows=False):
-    """Checks a tensor that the library will address: its type, its shape (None: any size),
-    its device, and that it is contiguous (rows: apart from the stride of its first axis)."""
+def _explain(what, t, dtypes, shape, index):
+    """Why `t` is not a tensor of the given type and shape (None: any size) on CUDA device
+    `index`, contiguous in its last axes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
-    if t.numel() and not (t[0] if rows else t).is_contiguous():
-        raise ValueError(f"{what}: not contiguous")
+    if index < 0 or t.get_device() != index:
+        raise ValueError(f"{what}: on {t.device}, expected CUDA tensors of one device")
+    raise ValueError(f"{what}: strides {t.stride()} are not those of contiguous rows")
 
 
-class _on_device:
-    """The tensors' device as the current one, and a stream of that device."""
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got {device}")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream of {stream.device} with tensors on {device}")
-        self._guard = torch.cuda.device(device)
-        self._device, self._given = device, stream
-
-    def __enter__(self):
-        self._guard.__enter__()
-        return _stream(torch.cuda.current_stream(self._device) if self._given is None
-                       else self._given)
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+def _need(what, t, dtype, shape, index):
+    """A contiguous tensor of exactly this type, shape and device; its address."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != index
+            or not t.is_contiguous()):
+        _explain(what, t, (dtype,), shape, index)
+    return t.data_ptr()
 
 
-def _expect_pool(desc, k_pages, v_pages, k_scale, v_scale, pages, device):
-    fp8 = desc.kv_dtype == QUAIL_FP8_E4M3
+def _need_rows(what, t, shape, index):
+    """bf16 rows [n, heads, d] any distance apart: their address and that distance."""
+    st = t.stride()
+    if (t.dtype is not _BF16 or t.shape != shape or t.get_device() != index or len(st) != 3
+            or (st[2] != 1 and shape[0]) or (st[1] != shape[2] and shape[1] > 1 and shape[0])):
+        _explain(what, t, (_BF16,), shape, index)
+    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _need_pages(what, t, desc, pages, index):
+    """A pool of `pages` pages; its address."""
     shape = (pages, desc.page_size, desc.num_kv_heads, desc.head_dim)
-    _expect("k_pages", k_pages, shape, _code_dtypes(fp8), device)
-    _expect("v_pages", v_pages, shape, _code_dtypes(fp8), device)
-    if fp8 and (k_scale is None or v_scale is None):
-        raise ValueError("e4m3 pages need k_scale and v_scale")
-    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if s is not None:
-            _expect(name, s, (desc.num_seqs, desc.num_kv_heads), (torch.float32,), device)
+    fp8 = desc.kv_dtype == QUAIL_FP8_E4M3
+    if ((t.dtype not in _CODES if fp8 else t.dtype is not _BF16) or t.shape != shape
+            or t.get_device() != index or not t.is_contiguous()):
+        _explain(what, t, _CODES if fp8 else (_BF16,), shape, index)
+    return t.data_ptr()
 
 
-def _expect_score(what, t, rows, heads, least, device):
-    _expect(what, t, (rows, heads, None), (torch.float32,), device)
-    if t.shape[2] < least:
-        raise ValueError(f"{what}: {t.shape[2]} entries a row, at least {least} are needed")
+def _need_scales(desc, k_scale, v_scale, index):
+    if desc.kv_dtype != QUAIL_FP8_E4M3 and k_scale is None and v_scale is None:
+        return None, None
+    if k_scale is None or v_scale is None:
+        raise ValueError("e4m3 pages need k_scale and v_scale, bf16 pages neither")
+    shape = (desc.num_seqs, desc.num_kv_heads)
+    return (_need("k_scale", k_scale, _F32, shape, index),
+            _need("v_scale", v_scale, _F32, shape, index))
+
+
+def _need_score(what, t, rows, heads, least, index):
+    """[rows, heads, n] fp32 with n >= least: its address and n."""
+    shape = t.shape
+    if (t.dtype is not _F32 or len(shape) != 3 or shape[0] != rows or shape[1] != heads
+            or t.get_device() != index or not t.is_contiguous()):
+        _explain(what, t, (_F32,), (rows, heads, None), index)
+    if shape[2] < least:
+        raise ValueError(f"{what}: {shape[2]} entries a row, at least {least} are needed")
+    return t.data_ptr(), shape[2]
+
+
+def _need_workspace(t, index, size):
+    if t is None:
+        raise ValueError(f"workspace is required (size: {size})")
+    if t.dtype is not torch.uint8 or t.dim() != 1 or t.get_device() != index or not t.is_contiguous():
+        _explain("workspace", t, (torch.uint8,), (None,), index)
+    return t.data_ptr(), t.numel()
+
+
+def _on_device(fn, what, index, stream, *args):
+    """fn(*args, stream) with the tensors' device current and a stream of that device."""
+    if index < 0:
+        raise ValueError(f"{what}: expected CUDA tensors")
+    if stream is None:
+        handle = _raw_stream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"{what}: stream of cuda:{stream.device_index}, tensors on cuda:{index}")
+    else:
+        handle = stream.cuda_stream
+    if _current_device() == index:
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, handle)
+    if code != QUAIL_OK:
+        raise QuailError(code, what)
 
 
 def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pages, v_pages,
@@ -451,23 +494,20 @@ def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pag
     """quail_paged_kv_append: rows k_new / v_new ([T, Hkv, d] bf16, any row stride) into the
     pages at start_pos[b] + i; new_offsets ([B+1] int32) delimits the sequences' rows (None:
     one token each). With e4m3 pages the rows become codes under the given scales."""
-    dev, i32 = k_new.device, (torch.int32,)
-    row = (k_new.shape[0], desc.num_kv_heads, desc.head_dim)
-    _expect("k_new", k_new, row, (torch.bfloat16,), dev, rows=True)
-    _expect("v_new", v_new, row, (torch.bfloat16,), dev, rows=True)
-    _expect("start_pos", start_pos, (desc.num_seqs,), i32, dev)
-    _expect("block_table", block_table, (desc.num_seqs, desc.max_pages_per_seq), i32, dev)
+    dev, B, pages = k_new.get_device(), desc.num_seqs, desc.num_pages
+    shape = (k_new.shape[0], desc.num_kv_heads, desc.head_dim)
+    k, k_stride = _need_rows("k_new", k_new, shape, dev)
+    v, v_stride = _need_rows("v_new", v_new, shape, dev)
+    off = None
     if new_offsets is not None:
-        _expect("new_offsets", new_offsets, (desc.num_seqs + 1,), i32, dev)
-    _expect_pool(desc, k_pages, v_pages, k_scale, v_scale, desc.num_pages, dev)
-    least = desc.num_kv_heads * desc.head_dim
-    with _on_device(dev, stream) as st:
-        code = lib.quail_paged_kv_append(
-            ctypes.byref(desc), row[0], _ptr(k_new), _ptr(v_new),
-            k_new.stride(0) if row[0] > 1 else least, v_new.stride(0) if row[0] > 1 else least,
-            _ptr(new_offsets), _ptr(start_pos), _ptr(block_table), _ptr(k_scale), _ptr(v_scale),
-            _ptr(k_pages), _ptr(v_pages), st)
-    _check(code, "quail_paged_kv_append")
+        off = _need("new_offsets", new_offsets, _I32, (B + 1,), dev)
+    ks, vs = _need_scales(desc, k_scale, v_scale, dev)
+    _on_device(lib.quail_paged_kv_append, "quail_paged_kv_append", dev, stream,
+               ctypes.byref(desc), shape[0], k, v, k_stride, v_stride, off,
+               _need("start_pos", start_pos, _I32, (B,), dev),
+               _need("block_table", block_table, _I32, (B, desc.max_pages_per_seq), dev), ks, vs,
+               _need_pages("k_pages", k_pages, desc, pages, dev),
+               _need_pages("v_pages", v_pages, desc, pages, dev))
 
 
 def paged_decode_workspace_size(desc: PagedDesc, with_scores=False) -> int:
@@ -480,35 +520,28 @@ def paged_decode_attn(desc: PagedDesc, q, k_pages, v_pages, block_table, seq_len
     """quail_paged_decode_attn: attention of one new token per sequence (q [B, Hq, d] bf16, any
     row stride) over its cached tokens; with score_out ([B, Hkv, n] fp32) also score_in plus
     the weight that each cached token receives (score_in may be score_out)."""
-    if workspace is None:
-        raise ValueError("workspace is required (size: paged_decode_workspace_size(...))")
-    dev, i32, f32 = q.device, (torch.int32,), (torch.float32,)
-    shape = (desc.num_seqs, desc.num_q_heads, desc.head_dim)
-    _expect("q", q, shape, (torch.bfloat16,), dev, rows=True)
-    _expect("out", out, shape, (torch.bfloat16,), dev)
-    _expect("seq_lens", seq_lens, (desc.num_seqs,), i32, dev)
-    _expect("block_table", block_table, (desc.num_seqs, desc.max_pages_per_seq), i32, dev)
-    _expect("workspace", workspace, (None,), (torch.uint8,), dev)
-    _expect_pool(desc, k_pages, v_pages, k_scale, v_scale, desc.num_pages, dev)
-    if lse is not None:
-        _expect("lse", lse, shape[:2], f32, dev)
-    if score_in is not None and score_out is None:
-        raise ValueError("score_in without score_out")
+    dev, B, hq, pages = q.get_device(), desc.num_seqs, desc.num_q_heads, desc.num_pages
+    ws, ws_bytes = _need_workspace(workspace, dev, "paged_decode_workspace_size(...)")
+    shape = (B, hq, desc.head_dim)
+    qp, q_stride = _need_rows("q", q, shape, dev)
+    ks, vs = _need_scales(desc, k_scale, v_scale, dev)
+    si = so = None
     width = 0
     if score_out is not None:
-        _expect_score("score_out", score_out, desc.num_seqs, desc.num_kv_heads, desc.max_seq_len,
-                      dev)
-        width = score_out.shape[2]
+        so, width = _need_score("score_out", score_out, B, desc.num_kv_heads, desc.max_seq_len, dev)
         if score_in is not None:
-            _expect("score_in", score_in, tuple(score_out.shape), f32, dev)
-    with _on_device(dev, stream) as st:
-        code = lib.quail_paged_decode_attn(
-            ctypes.byref(desc), _ptr(q),
-            q.stride(0) if shape[0] > 1 else desc.num_q_heads * desc.head_dim, _ptr(k_pages),
-            _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(k_scale), _ptr(v_scale),
-            _ptr(out), _ptr(lse), _ptr(score_in), _ptr(score_out), width, _ptr(workspace),
-            workspace.numel(), st)
-    _check(code, "quail_paged_decode_attn")
+            si = _need("score_in", score_in, _F32, score_out.shape, dev)
+    elif score_in is not None:
+        raise ValueError("score_in without score_out")
+    _on_device(lib.quail_paged_decode_attn, "quail_paged_decode_attn", dev, stream,
+               ctypes.byref(desc), qp, q_stride,
+               _need_pages("k_pages", k_pages, desc, pages, dev),
+               _need_pages("v_pages", v_pages, desc, pages, dev),
+               _need("block_table", block_table, _I32, (B, desc.max_pages_per_seq), dev),
+               _need("seq_lens", seq_lens, _I32, (B,), dev), ks, vs,
+               _need("out", out, _BF16, shape, dev),
+               None if lse is None else _need("lse", lse, _F32, (B, hq), dev), si, so, width, ws,
+               ws_bytes)
 
 
 def attn_scores(q, k, lse, q_offsets, k_offsets, score_out, max_q_len, max_k_len, causal=True,
@@ -516,25 +549,21 @@ def attn_scores(q, k, lse, q_offsets, k_offsets, score_out, max_q_len, max_k_len
     """quail_attn_scores: the attention weight that each key receives from the queries of its
     sequence (q [Tq, Hq, d], k [Tk, Hkv, d] bf16 with any row stride, lse [Tq, Hq] from the
     attention call), added to score_in into score_out [num_seqs, Hkv, n] fp32."""
-    dev, i32, f32 = k.device, (torch.int32,), (torch.float32,)
-    _expect("q", q, (None, None, None), (torch.bfloat16,), dev, rows=True)
-    _expect("k", k, (None, None, q.shape[2]), (torch.bfloat16,), dev, rows=True)
-    _expect("lse", lse, tuple(q.shape[:2]), f32, dev)
-    _expect("k_offsets", k_offsets, (None,), i32, dev)
-    _expect("q_offsets", q_offsets, tuple(k_offsets.shape), i32, dev)
-    seqs = k_offsets.numel() - 1
-    _expect_score("score_out", score_out, seqs, k.shape[1], int(max_k_len), dev)
-    if score_in is not None:
-        _expect("score_in", score_in, tuple(score_out.shape), f32, dev)
-    hq, hkv, d = q.shape[1], k.shape[1], q.shape[2]
-    with _on_device(dev, stream) as st:
-        code = lib.quail_attn_scores(
-            seqs, q.shape[0], k.shape[0], int(max_q_len), int(max_k_len), hq, hkv, d,
-            float(softmax_scale), 1 if causal else 0, int(window), _ptr(q),
-            q.stride(0) if q.shape[0] > 1 else hq * d, _ptr(k),
-            k.stride(0) if k.shape[0] > 1 else hkv * d, _ptr(lse), _ptr(q_offsets),
-            _ptr(k_offsets), _ptr(score_in), _ptr(score_out), score_out.shape[2], st)
-    _check(code, "quail_attn_scores")
+    dev = k.get_device()
+    tq, hq, d = q.shape
+    tk, hkv, _ = k.shape
+    qp, q_stride = _need_rows("q", q, (tq, hq, d), dev)
+    kp, k_stride = _need_rows("k", k, (tk, hkv, d), dev)
+    seqs = k_offsets.shape[0] - 1
+    max_q_len, max_k_len = int(max_q_len), int(max_k_len)
+    so, width = _need_score("score_out", score_out, seqs, hkv, max_k_len, dev)
+    _on_device(lib.quail_attn_scores, "quail_attn_scores", dev, stream, seqs, tq, tk, max_q_len,
+               max_k_len, hq, hkv, d, softmax_scale, 1 if causal else 0, int(window), qp, q_stride,
+               kp, k_stride, _need("lse", lse, _F32, (tq, hq), dev),
+               _need("q_offsets", q_offsets, _I32, (seqs + 1,), dev),
+               _need("k_offsets", k_offsets, _I32, (seqs + 1,), dev),
+               None if score_in is None else _need("score_in", score_in, _F32, score_out.shape, dev),
+               so, width)
 
 
 def paged_evict_workspace_size(desc: PagedDesc, dst_num_pages) -> int:
@@ -548,32 +577,26 @@ def paged_kv_evict(desc: PagedDesc, budget, recent, k_pages, v_pages, block_tabl
     scored others, `budget` in all, copied in order into the pages that dst_table names (of
     the same pool or another); kept [B, Hkv, budget] and new_lens [B] int32 say which and how
     many, score_out [B, Hkv, n] takes their scores."""
-    if workspace is None:
-        raise ValueError("workspace is required (size: paged_evict_workspace_size(...))")
-    dev, i32, f32 = k_pages.device, (torch.int32,), (torch.float32,)
-    B, hkv = desc.num_seqs, desc.num_kv_heads
-    fp8 = desc.kv_dtype == QUAIL_FP8_E4M3
-    row = (desc.page_size, hkv, desc.head_dim)
-    for name, t, pages in (("k_pages", k_pages, desc.num_pages), ("v_pages", v_pages, desc.num_pages),
-                           ("k_dst", k_dst, None), ("v_dst", v_dst, k_dst.shape[0])):
-        _expect(name, t, (pages,) + row, _code_dtypes(fp8), dev)
-    _expect("block_table", block_table, (B, desc.max_pages_per_seq), i32, dev)
-    _expect("seq_lens", seq_lens, (B,), i32, dev)
-    _expect("dst_table", dst_table, (B, None), i32, dev)
-    _expect("kept", kept, (B, hkv, int(budget)), i32, dev)
-    _expect("new_lens", new_lens, (B,), i32, dev)
-    _expect("workspace", workspace, (None,), (torch.uint8,), dev)
-    _expect_score("score", score, B, hkv, desc.max_seq_len, dev)
+    budget, recent = int(budget), int(recent)
+    dev, B, hkv, pages = k_pages.get_device(), desc.num_seqs, desc.num_kv_heads, desc.num_pages
+    ws, ws_bytes = _need_workspace(workspace, dev, "paged_evict_workspace_size(...)")
+    sp, width = _need_score("score", score, B, hkv, desc.max_seq_len, dev)
+    so, out_width = None, 0
     if score_out is not None:
-        _expect_score("score_out", score_out, B, hkv, int(budget), dev)
-    with _on_device(dev, stream) as st:
-        code = lib.quail_paged_kv_evict(
-            ctypes.byref(desc), int(budget), int(recent), _ptr(k_pages), _ptr(v_pages),
-            _ptr(block_table), _ptr(seq_lens), _ptr(score), score.shape[2], _ptr(dst_table),
-            dst_table.shape[1], k_dst.shape[0], _ptr(k_dst), _ptr(v_dst), _ptr(kept),
-            _ptr(new_lens), _ptr(score_out), 0 if score_out is None else score_out.shape[2],
-            _ptr(workspace), workspace.numel(), st)
-    _check(code, "quail_paged_kv_evict")
+        so, out_width = _need_score("score_out", score_out, B, hkv, budget, dev)
+    dst_shape, dst_pages = dst_table.shape, k_dst.shape[0]
+    if len(dst_shape) != 2:
+        _explain("dst_table", dst_table, (_I32,), (B, None), dev)
+    _on_device(lib.quail_paged_kv_evict, "quail_paged_kv_evict", dev, stream, ctypes.byref(desc),
+               budget, recent, _need_pages("k_pages", k_pages, desc, pages, dev),
+               _need_pages("v_pages", v_pages, desc, pages, dev),
+               _need("block_table", block_table, _I32, (B, desc.max_pages_per_seq), dev),
+               _need("seq_lens", seq_lens, _I32, (B,), dev), sp, width,
+               _need("dst_table", dst_table, _I32, (B, dst_shape[1]), dev), dst_shape[1],
+               dst_pages, _need_pages("k_dst", k_dst, desc, dst_pages, dev),
+               _need_pages("v_dst", v_dst, desc, dst_pages, dev),
+               _need("kept", kept, _I32, (B, hkv, budget), dev),
+               _need("new_lens", new_lens, _I32, (B,), dev), so, out_width, ws, ws_bytes)
 
 
 def get_device_error(stream=None) -> int:

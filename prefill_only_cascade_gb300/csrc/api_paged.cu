@@ -317,8 +317,11 @@ quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, 
   const int64_t most = budget < d.max_seq_len ? budget : d.max_seq_len;
   if (most > static_cast<int64_t>(dst_max_pages_per_seq) * d.page_size) return QUAIL_ERR_INVALID_ARG;
   if (score_out != nullptr && score_out_stride < budget) return QUAIL_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(d.num_seqs) * budget > kInt32Max) return QUAIL_ERR_UNSUPPORTED;
   const int64_t pairs = static_cast<int64_t>(d.num_seqs) * d.num_kv_heads;
+  // blocks of 256 kept rows
+  if (d.num_seqs > 0 &&
+      (static_cast<int64_t>(budget) * d.num_kv_heads + 255) / 256 > kInt32Max / d.num_seqs)
+    return QUAIL_ERR_UNSUPPORTED;
   const int row_bytes = d.head_dim * elem_bytes(d);
   const size_t page_bytes = static_cast<size_t>(d.page_size) * d.num_kv_heads * row_bytes;
   const size_t src_bytes = page_bytes * d.num_pages, dst_bytes = page_bytes * dst_num_pages;

@@ -8,7 +8,8 @@
 //    histograms of the cluster's CTAs added through distributed shared memory) and writes
 //    the kept positions in order. The keys stay in shared memory between the passes: the
 //    scores are read once. It also marks the pages that are read and written.
-// 2. evict_copy_kernel    moves the kept rows, 16 bytes a thread and eight in flight.
+// 2. evict_copy_kernel    moves the kept rows: a block looks up the places of 256 (token,
+//    head) rows first, then moves them, 16 bytes a thread and eight in flight.
 #include <cstdint>
 
 #include "kernels.h"
@@ -23,6 +24,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBinsPerThread = kBins / kSelThreads;  // 4
 constexpr int kKeyCap = 20480;                       // keys a CTA holds (80 KB): two CTAs an SM
+constexpr int kLoads = 8;                            // scores in flight per thread
 constexpr int kMaxCluster = 8;
 
 constexpr int kMarkRead = 1, kMarkWritten = 2;       // a page's uses: bit 0, and 2 per write
@@ -39,6 +41,11 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
+constexpr uint32_t kKeyZero = 0x80000000u, kKeyLowest = 0x007FFFFFu;  // of +-0; of -inf and NaN
+__device__ __forceinline__ float key_score(uint32_t key) {
+  return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
+}
+
 __device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -51,7 +58,7 @@ __device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const PagedEvictArgs a,
                                                                    int cluster, int key_cap) {
   extern __shared__ uint32_t s_keys[];  // [key_cap]
-  __shared__ __align__(16) uint32_t s_hist[kBins];
+  __shared__ __align__(16) uint32_t s_hist[3][kBins];  // one per pass
   __shared__ uint32_t s_warp[kSelWarps];
   __shared__ uint32_t s_found[2];       // digit, and how many are above it
   __shared__ __align__(16) uint32_t s_count[4];  // this CTA's keys above / at the threshold
@@ -97,6 +104,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const PagedEv
   if (score_out != nullptr)
     for (int64_t i = fresh + tid; i < a.score_out_stride; i += threads) score_out[i] = 0.f;
   if (k == 0) return;  // the same for every CTA of the cluster
+  for (int i = threadIdx.x; i < 3 * kBins / 4; i += kSelThreads)
+    reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
 
   // this CTA's part of the competing tokens
   const int per = (elig + cluster - 1) / cluster;
@@ -112,31 +122,52 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const PagedEv
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
-      for (int i = threadIdx.x; i < kBins; i += kSelThreads) s_hist[i] = 0;
-      __syncthreads();
+      uint32_t* hist = s_hist[pass];
       if (pass == 0) {
-        for (int i = threadIdx.x; i < count; i += kSelThreads) {
-          const uint32_t key = score_key(__ldg(score + e0 + i));
-          if (i < key_cap) s_keys[i] = key;
-          atomicAdd(&s_hist[key >> 21], 1u);
+        for (int i0 = threadIdx.x; i0 < count; i0 += kSelThreads * kLoads) {
+          float x[kLoads];
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j) {
+            const int i = i0 + j * kSelThreads;
+            x[j] = i < count ? __ldg(score + e0 + i) : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j) {
+            const int i = i0 + j * kSelThreads;
+            const uint32_t key = score_key(x[j]);
+            if (i < count && i < key_cap) s_keys[i] = key;
+            if (i < count) atomicAdd(&hist[key >> 21], 1u);
+          }
         }
       } else {
         const int above = pass == 1 ? 21 : 10;
+#pragma unroll 4
         for (int i = threadIdx.x; i < count; i += kSelThreads) {
           const uint32_t key = key_at(i);
-          if (key >> above == prefix) atomicAdd(&s_hist[(key >> shift) & mask], 1u);
+          if (key >> above == prefix) atomicAdd(&hist[(key >> shift) & mask], 1u);
         }
       }
       if (cluster > 1) cluster_sync(); else __syncthreads();
       uint32_t bin[kBinsPerThread] = {0, 0, 0, 0};
-      for (int c = 0; c < cluster; ++c) {
-        const uint4 v = cluster > 1
-                            ? ld_cluster_u4(cluster_map(&s_hist[kBinsPerThread * threadIdx.x], c))
-                            : *reinterpret_cast<const uint4*>(&s_hist[kBinsPerThread * threadIdx.x]);
-        bin[0] += v.x;
-        bin[1] += v.y;
-        bin[2] += v.z;
-        bin[3] += v.w;
+      if (cluster == 1) {
+        const uint4 v = *reinterpret_cast<const uint4*>(&hist[kBinsPerThread * threadIdx.x]);
+        bin[0] = v.x;
+        bin[1] = v.y;
+        bin[2] = v.z;
+        bin[3] = v.w;
+      } else {
+        uint4 v[kMaxCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < cluster) v[c] = ld_cluster_u4(cluster_map(&hist[kBinsPerThread * threadIdx.x], c));
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < cluster) {
+            bin[0] += v[c].x;
+            bin[1] += v[c].y;
+            bin[2] += v[c].z;
+            bin[3] += v[c].w;
+          }
       }
       // how many keys lie in the bins of the threads after this one
       const uint32_t mine = bin[0] + bin[1] + bin[2] + bin[3];
@@ -158,7 +189,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const PagedEv
         }
         above += bin[j];
       }
-      if (cluster > 1) cluster_sync(); else __syncthreads();
+      __syncthreads();
       prefix = pass == 2 ? prefix << 10 | s_found[0] : prefix << 11 | s_found[0];
       need -= s_found[1];
     }
@@ -219,7 +250,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const PagedEv
       const uint32_t at = base_gt + __popc(bg & before) + min(eq_rank, need);
       if (at < static_cast<uint32_t>(k)) {  // else the scores changed meanwhile
         kept[at] = e0 + i;
-        if (score_out != nullptr) score_out[at] = __ldg(score + e0 + i);
+        if (score_out != nullptr) {
+          // the key gives the score back, but for the values that share one
+          score_out[at] = all || key == kKeyZero || key == kKeyLowest ? __ldg(score + e0 + i)
+                                                                     : key_score(key);
+        }
       }
     }
     base_gt += __popc(bg);
@@ -229,82 +264,72 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const PagedEv
 }
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 8;
+constexpr int kCopyUnroll = 4;   // rows' pieces in flight per thread, K and V each
 
-// A block moves `rows` consecutive kept places of one sequence, all heads, K and V.
-__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const PagedEvictArgs a,
-                                                                  int rows, int chunks) {
+// A block moves 256 consecutive (kept place, head) rows of one sequence, K and V.
+__global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const PagedEvictArgs a,
+                                                                     int chunks) {
+  __shared__ int64_t s_src[kCopyThreads], s_dst[kCopyThreads];  // byte offsets; < 0: none
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int s_bad;
   const int b = blockIdx.x / chunks;
-  const int i0 = (blockIdx.x % chunks) * rows;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x % chunks) * kCopyThreads;
   const int n = evict_len(a, b);
   const int fresh = min(n, a.budget);
-  if (i0 >= fresh) return;
-  const int count = min(rows, fresh - i0);
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  const int32_t* dst_table = a.dst_table + static_cast<int64_t>(b) * a.dst_max_pages;
-  const int p0 = i0 >> a.page_shift, p1 = (i0 + count - 1) >> a.page_shift;
-  for (int j = p0 + threadIdx.x; j <= p1; j += kCopyThreads) {
-    const int p = __ldg(dst_table + j);
-    // written once, by this sequence, and read by none
-    if (p < 0 || p >= a.dst_num_pages || a.marks[p] != kMarkWritten) s_bad = 1;
-  }
-  __syncthreads();
-  if (s_bad) {
-    if (threadIdx.x == 0) {
+  const int64_t rows = static_cast<int64_t>(fresh) * a.hkv;
+  if (r0 >= rows) return;
+  const int count = static_cast<int>(min(static_cast<int64_t>(kCopyThreads), rows - r0));
+  if (threadIdx.x < count) {
+    const int64_t r = r0 + threadIdx.x;
+    const int i = static_cast<int>(r / a.hkv), g = static_cast<int>(r % a.hkv);
+    const int mask = (1 << a.page_shift) - 1;
+    const int pos = a.kept[(static_cast<int64_t>(b) * a.hkv + g) * a.budget + i];
+    const int to = __ldg(a.dst_table + static_cast<int64_t>(b) * a.dst_max_pages +
+                         (i >> a.page_shift));
+    // the destination page is written once, by this sequence, and read by none
+    bool ok = to >= 0 && to < a.dst_num_pages && a.marks[to] == kMarkWritten;
+    int from = -1;
+    if (pos >= 0 && pos < n) {
+      from = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + (pos >> a.page_shift));
+      ok = ok && from >= 0 && from < a.num_pages;
+    } else {
+      ok = false;
+    }
+    if (!ok) {
       atomicOr(a.err_word, kErrDeviceBounds);
       a.new_lens[b] = -1;
     }
-    return;
+    s_src[threadIdx.x] =
+        ok ? (((static_cast<int64_t>(from) << a.page_shift) + (pos & mask)) * a.hkv + g) * a.row_bytes
+           : -1;
+    s_dst[threadIdx.x] =
+        ok ? (((static_cast<int64_t>(to) << a.page_shift) + (i & mask)) * a.hkv + g) * a.row_bytes
+           : -1;
   }
-  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
-  const int32_t* kept = a.kept + static_cast<int64_t>(b) * a.hkv * a.budget + i0;
-  const int vecs = a.row_bytes / 16;                 // of one (token, head) row
-  const int half = count * a.hkv * vecs;             // of K
-  const int mask = (1 << a.page_shift) - 1;
-  for (int u0 = threadIdx.x; u0 < 2 * half; u0 += kCopyThreads * kCopyUnroll) {
-    int pos[kCopyUnroll];
-    int64_t src[kCopyUnroll], dst[kCopyUnroll];
-    uint4 x[kCopyUnroll];
+  __syncthreads();
+  const int shift = a.row_bytes == 256 ? 4 : a.row_bytes == 128 ? 3 : 2;  // 16-byte pieces a row
+  const int pieces = count << shift;
+  for (int u0 = threadIdx.x; u0 < pieces; u0 += kCopyThreads * kCopyUnroll) {
+    uint4 x[kCopyUnroll], y[kCopyUnroll];
 #pragma unroll
     for (int j = 0; j < kCopyUnroll; ++j) {
       const int u = u0 + j * kCopyThreads;
-      pos[j] = -1;
-      if (u >= 2 * half) continue;
-      const int v = u < half ? u : u - half;
-      const int c = v % vecs, rest = v / vecs;
-      const int g = rest % a.hkv, i = rest / a.hkv;
-      pos[j] = kept[static_cast<int64_t>(g) * a.budget + i];
-      const int page = __ldg(dst_table + ((i0 + i) >> a.page_shift));
-      dst[j] = (((static_cast<int64_t>(page) << a.page_shift) + ((i0 + i) & mask)) * a.hkv + g) *
-                   a.row_bytes + 16 * c;
-      src[j] = static_cast<int64_t>(g) * a.row_bytes + 16 * c;
+      const int64_t s = u < pieces ? s_src[u >> shift] : -1;
+      if (s >= 0) {
+        const int64_t at = s + 16 * (u & ((1 << shift) - 1));
+        x[j] = *reinterpret_cast<const uint4*>(a.k_pages + at);
+        y[j] = *reinterpret_cast<const uint4*>(a.v_pages + at);
+      }
     }
 #pragma unroll
     for (int j = 0; j < kCopyUnroll; ++j) {
-      if (pos[j] < 0) continue;
-      const int page = __ldg(table + (pos[j] >> a.page_shift));
-      if (page < 0 || page >= a.num_pages) {
-        atomicOr(a.err_word, kErrDeviceBounds);
-        a.new_lens[b] = -1;
-        pos[j] = -1;
-        continue;
+      const int u = u0 + j * kCopyThreads;
+      const int64_t s = u < pieces ? s_dst[u >> shift] : -1;
+      if (s >= 0) {
+        const int64_t at = s + 16 * (u & ((1 << shift) - 1));
+        *reinterpret_cast<uint4*>(a.k_dst + at) = x[j];
+        *reinterpret_cast<uint4*>(a.v_dst + at) = y[j];
       }
-      src[j] += ((static_cast<int64_t>(page) << a.page_shift) + (pos[j] & mask)) *
-                static_cast<int64_t>(a.hkv) * a.row_bytes;
     }
-#pragma unroll
-    for (int j = 0; j < kCopyUnroll; ++j)
-      if (pos[j] >= 0)
-        x[j] = *reinterpret_cast<const uint4*>(
-            (u0 + j * kCopyThreads < half ? a.k_pages : a.v_pages) + src[j]);
-#pragma unroll
-    for (int j = 0; j < kCopyUnroll; ++j)
-      if (pos[j] >= 0)
-        *reinterpret_cast<uint4*>((u0 + j * kCopyThreads < half ? a.k_dst : a.v_dst) + dst[j]) =
-            x[j];
   }
 }
 
@@ -342,17 +367,14 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cluster, cap);
   if (e != cudaSuccess) return e;
-  // about 2,048 vectors a block
-  const int per_row = 2 * a.hkv * (a.row_bytes / 16);
-  int rows = kCopyThreads * kCopyUnroll / per_row;
-  if (rows < 1) rows = 1;
-  const int chunks = (a.budget + rows - 1) / rows;
+  const int chunks = static_cast<int>(
+      (static_cast<int64_t>(a.budget) * a.hkv + kCopyThreads - 1) / kCopyThreads);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * chunks));
   cfg.blockDim = dim3(kCopyThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, evict_copy_kernel, a, rows, chunks);
+  return cudaLaunchKernelEx(&cfg, evict_copy_kernel, a, chunks);
 }
 
 }  // namespace quail
