@@ -55,7 +55,7 @@ __device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
   return v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const PagedEvictArgs a,
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const PagedEvictArgs a,
                                                                    int cluster, int key_cap) {
   extern __shared__ uint32_t s_keys[];  // [key_cap]
   __shared__ __align__(16) uint32_t s_hist[3][kBins];  // one per pass

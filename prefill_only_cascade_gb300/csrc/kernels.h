@@ -212,9 +212,9 @@ struct PagedDecodeArgs {
   int64_t raw_stride;
   unsigned* err_word;
 };
-constexpr int kDecodeMaxCtas = 480;
+constexpr int kDecodeMaxCtas = 320;
 int decode_tile_keys(int head_dim, bool fp8);
-int decode_ctas(int num_sms, int num_seqs, int hkv, int max_len, int tile, int nt);
+int decode_ctas(int num_sms, int num_seqs, int hkv, int max_len, int tile);
 cudaError_t launch_paged_decode(PagedDecodeArgs& a, int head_dim, bool fp8, int num_sms,
                                 cudaStream_t stream);
 

@@ -133,16 +133,20 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 // the order sequence, head, position, and each CTA takes an equal run of them, whatever
 // the lengths are: short sequences share a CTA, long ones spread over many. A sequence's
 // head that lies inside one CTA is finished there; the others leave (max, sum, O) partials
-// that paged_join_kernel rescales and adds. Each warp walks its own keys of the tile with a
-// running max and sum; K and V of its next keys are in registers while it works on the
-// present ones.
+// that paged_join_kernel rescales and adds.
+//
+// Each warp walks its own keys of its CTA's run with a running max and sum. Their K and V
+// rows come through a ring of its own in shared memory, filled by 16-byte asynchronous
+// copies two steps (16 KB a warp, 128 KB an SM) ahead, also over the borders between
+// sequences and heads, so the loads never wait for the arithmetic. No warp waits for
+// another but where the parts of a (sequence, head) are put together.
 //
 // Both products run on mma.sync m16n8k16: one new token gives at most 16 query rows per KV
-// head, so the padded products cost 3 % of the tensor rate of the legacy pipe and K/V need
-// no staging in shared memory: since sums over d (scores) and the order of d (output rows)
-// may be permuted freely, plain 16-byte row loads ARE the operand fragments.
-//   S  [16 heads x 8 keys]  A = Q (rows: heads), B = K: lane (r, q) holds key r, chunk q + 4i
-//   O^T [16 d x 8 heads]    A = V^T: lane (r, q) holds keys 2q, 2q+1, 2q+8, 2q+9, chunk r
+// head, so the padded products cost a few per cent of the tensor rate of the legacy pipe.
+// Since sums over d (scores) and the order of d (output rows) may be permuted freely,
+// 16-byte pieces of plain rows ARE the operand fragments:
+//   S  [16 heads x 8 keys]  A = Q (rows: heads), B = K: lane (r, q) holds key r, piece q + 4i
+//   O^T [16 d x 8 heads]    A = V^T: lane (r, q) holds keys 2q, 2q+1, 2q+8, 2q+9, piece r
 //                           (two keys' values interleaved by byte permutes), B = P, whose
 //                           fragment is the score fragment packed in place
 // bf16 pages: bf16 products, P as the sum of two bf16 (hi + lo: 16 bits of P). e4m3 pages:
@@ -152,31 +156,53 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 
+constexpr int kStages = 3;                           // steps in a warp's ring
+constexpr int kStepBytes = 4096;                     // of K, and of V, in one step
+
 template <int D, bool FP8>
 struct DecCfg {
   static constexpr int kRB = D * (FP8 ? 1 : 2);      // bytes of a (token, head) row
-  static constexpr int kKChunks = kRB / 64;          // 16-byte K loads per lane and key
-  static constexpr int kKG = 8 / kKChunks;           // groups of 8 keys per warp step
-  static constexpr int kKeys = 8 * kKG;              // keys per warp step: 16, 32 or 64
-  static constexpr int kSteps16 = kKeys / 16;
-  static constexpr int kVWords = kRB / 32;           // 32-bit words per lane and V row
+  static constexpr int kNC = kRB / 16;               // its 16-byte pieces
+  static constexpr int kKeys = kStepBytes / kRB;     // keys per warp step: 16, 32 or 64
+  static constexpr int kKG = kKeys / 8;              // in groups of 8 (score tiles)
+  static constexpr int kKChunks = kRB / 64;          // K pieces per lane and key
+  static constexpr int kSteps16 = kKeys / 16;        // in 16s (products with V)
   static constexpr int kTile = kDecWarps * kKeys;    // keys per CTA tile
   static constexpr int kMT = D / 16;                 // 16-row tiles of O^T
   static constexpr int kQS = D / 16;                 // k-steps of the score product
+  static constexpr int kRing = kDecWarps * kStages * 2 * kStepBytes;
+  static constexpr int kSmem = kRing + kDecWarps * 8 * D * 4;  // + the warps' O, 8 heads
 };
 
-__device__ __forceinline__ uint4 ld_kv16(const uint8_t* p) {
+// Places of piece c of row `row` in a step's K and V buffers (in 16-byte units). A warp's
+// 16-byte reads go in phases of 8 lanes: two K rows x 4 pieces, or four V row pairs x 2
+// pieces; the exclusive-ors spread each phase over all banks.
+template <int NC>
+__device__ __forceinline__ int k_place(int row, int c) {
+  return NC >= 8 ? (row * NC + c) ^ ((row & 1) << 2) : row * NC + c;
+}
+template <int NC>
+__device__ __forceinline__ int v_place(int row, int c) {
+  return (row * NC + c) ^ (((row >> 1) & 3) << 1);
+}
+
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t smem, const uint8_t* p, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(p),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "r"(a)
+               : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld_kv8(const uint8_t* p) {
+__device__ __forceinline__ uint2 ld_shared8(uint32_t a) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
 
@@ -245,71 +271,91 @@ __device__ __forceinline__ int checked_len(const PagedDecodeArgs& a, int b) {
   return n >= 0 && n <= a.max_len ? n : -1;
 }
 
-// Where a CTA's run begins, and the record the join reads.
+// Where a CTA's run of tiles begins.
 struct RunStart {
-  int64_t total;   // tiles of the batch
-  int64_t begin;   // first tile of this CTA
-  int64_t end;     // one past its last
-  int seq;         // sequence of tile `begin`
+  int64_t total;      // tiles of the batch
+  int64_t begin;      // first tile of this CTA
+  int64_t end;        // one past its last
+  int seq;            // sequence of tile `begin`
   int64_t seq_tile0;  // first tile of that sequence
 };
 
-// Scans the lengths: tiles of the batch, this CTA's run, the sequence it begins in. Every
-// CTA scans for itself (a few KB from L2), which costs less than a launch before this one.
+// Every warp scans the lengths for itself (a few KB from L2, 32 at a time), which costs less
+// than a launch before this one, or a barrier.
 __device__ RunStart find_run(const PagedDecodeArgs& a, int tile, int cta, int ctas) {
-  __shared__ int64_t s_sum[kDecWarps];
-  __shared__ RunStart s_run;
-  const int per = (a.num_seqs + kDecThreads - 1) / kDecThreads;
-  const int b0 = min(static_cast<int>(threadIdx.x) * per, a.num_seqs);
-  const int b1 = min(b0 + per, a.num_seqs);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int n = checked_len(a, b);
-    mine += n > 0 ? (n + tile - 1) / tile : 0;
-  }
-  mine *= a.hkv;
-  int64_t x = mine;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  auto tiles_of = [&](int b) {
+    const int n = b < a.num_seqs ? checked_len(a, b) : 0;
+    return n > 0 ? static_cast<unsigned>((n + tile - 1) / tile) : 0u;
+  };
+  int64_t total = 0;
+#pragma unroll 4
+  for (int base = 0; base < a.num_seqs; base += 32)
+    total += __reduce_add_sync(0xFFFFFFFFu, tiles_of(base + lane));
+  total *= a.hkv;
+  RunStart run{total, first_tile(cta, total, ctas), first_tile(cta + 1, total, ctas), 0, 0};
+  if (run.begin >= run.end) return run;
+  int64_t at = 0;  // tiles of one head before `base`
+  for (int base = 0; base < a.num_seqs; base += 32) {
+    const unsigned t = tiles_of(base + lane);
+    const unsigned sum = __reduce_add_sync(0xFFFFFFFFu, t);
+    if (run.begin < (at + sum) * a.hkv) {
+      unsigned x = t;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, off);
-    if (lane >= off) x += y;
-  }
-  if (lane == 31) s_sum[warp] = x;
-  __syncthreads();
-  int64_t before = x - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
-  }
-  const int64_t begin = first_tile(cta, total, ctas);
-  if (threadIdx.x == 0) s_run = RunStart{total, begin, first_tile(cta + 1, total, ctas), -1, 0};
-  __syncthreads();
-  if (mine > 0 && begin >= before && begin < before + mine) {
-    int64_t at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int n = checked_len(a, b);
-      const int64_t t = n > 0 ? static_cast<int64_t>((n + tile - 1) / tile) * a.hkv : 0;
-      if (begin < at + t) {
-        s_run.seq = b;
-        s_run.seq_tile0 = at;
-        break;
+      for (int off = 1; off < 32; off <<= 1) {
+        const unsigned y = __shfl_up_sync(0xFFFFFFFFu, x, off);
+        if (lane >= off) x += y;
       }
-      at += t;
+      const int hit = __ffs(__ballot_sync(0xFFFFFFFFu, run.begin < (at + x) * a.hkv)) - 1;
+      run.seq = base + hit;
+      run.seq_tile0 = (at + __shfl_sync(0xFFFFFFFFu, x - t, hit)) * a.hkv;
+      break;
     }
+    at += sum;
   }
-  __syncthreads();
-  return s_run;
+  return run;
+}
+
+// A piece of the run: keys [kb, ke) of sequence b and KV head g.
+struct Piece {
+  int b, g, len, kb, ke;
+  int64_t at;      // its first tile
+  int64_t piece0;  // first tile of (b, g)
+  int64_t stop;    // one past its last tile
+  bool whole;      // all of (b, g)
+};
+
+template <int TILE>
+__device__ __forceinline__ void set_piece(const PagedDecodeArgs& a, int64_t end, Piece& p) {
+  const int tiles = (p.len + TILE - 1) / TILE;
+  p.stop = min(end, p.piece0 + tiles);
+  p.kb = static_cast<int>(p.at - p.piece0) * TILE;
+  p.ke = min(p.len, static_cast<int>(p.stop - p.piece0) * TILE);
+  p.whole = p.at == p.piece0 && p.stop == p.piece0 + tiles;
+}
+
+// The next piece; false at the end of the run.
+template <int TILE>
+__device__ __forceinline__ bool next_piece(const PagedDecodeArgs& a, int64_t end, Piece& p) {
+  if (p.stop >= end) return false;
+  p.at = p.piece0 = p.stop;
+  if (++p.g == a.hkv) {
+    p.g = 0;
+    do {
+      p.len = checked_len(a, ++p.b);
+    } while (p.len <= 0);
+  }
+  set_piece<TILE>(a, end, p);
+  return true;
 }
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
-    paged_decode_kernel(const PagedDecodeArgs a) {
+__global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const PagedDecodeArgs a) {
   using C = DecCfg<D, FP8>;
+  extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ float s_m[kDecWarps][8 * NT], s_l[kDecWarps][8 * NT];
-  __shared__ alignas(16) float s_o[kDecWarps][8 * NT][D];
-  __shared__ int s_bad;
+  __shared__ int s_bad[kDecWarps];
+  float(*s_o)[8][D] = reinterpret_cast<float(*)[8][D]>(dyn + C::kRing);  // [warp][head][d]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, q4 = lane & 3;
@@ -332,43 +378,107 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
   const RunStart run = find_run(a, C::kTile, cta, ctas);
   if (threadIdx.x == 0) a.rec[cta] = DecodeRec{run.total, -1, -1, 0};
   if (run.begin >= run.end) return;
-  int b = run.seq;
-  int len = checked_len(a, b);
-  int tiles = (len + C::kTile - 1) / C::kTile;
-  int g = static_cast<int>((run.begin - run.seq_tile0) / tiles);
-  int64_t piece0 = run.seq_tile0 + static_cast<int64_t>(g) * tiles;  // first tile of (b, g)
-  int64_t at = run.begin;
+  Piece cur;
+  cur.b = run.seq;
+  cur.len = checked_len(a, cur.b);
+  {
+    const int tiles = (cur.len + C::kTile - 1) / C::kTile;
+    cur.g = static_cast<int>((run.begin - run.seq_tile0) / tiles);
+    cur.piece0 = run.seq_tile0 + static_cast<int64_t>(cur.g) * tiles;
+  }
+  cur.at = run.begin;
+  set_piece<C::kTile>(a, run.end, cur);
 
+  // ------------------------------------------------------ loads: a cursor of their own
   const int64_t row_stride = static_cast<int64_t>(a.hkv) * C::kRB;
-  while (true) {
-    // ---------------------------------------------------- one piece: keys [kb, ke) of (b, g)
-    const int64_t stop = min(run.end, piece0 + tiles);
-    const int kb = static_cast<int>(at - piece0) * C::kTile;
-    const int ke = min(len, static_cast<int>(stop - piece0) * C::kTile);
-    if (threadIdx.x == 0) s_bad = 0;
+  const uint32_t ring = smem_u32(dyn) + warp * (kStages * 2 * kStepBytes);
+  Piece ld = cur;
+  int ld_key = ld.kb + warp * C::kKeys;  // first key of the next step to load
+  bool ld_more = true;
+  int page[C::kSteps16];                 // pages of its 16-key blocks
+  uint32_t bad_steps = 0;                // bit s: a page of the step in stage s is no page
+  auto seek = [&]() {                    // on to a piece that has a step for this warp
+    while (ld_more && ld_key >= ld.ke) {
+      ld_more = next_piece<C::kTile>(a, run.end, ld);
+      ld_key = ld.kb + warp * C::kKeys;
+    }
+    if (ld_more) {
+      const int32_t* table = a.table + static_cast<int64_t>(ld.b) * a.max_pages;
+#pragma unroll
+      for (int i = 0; i < C::kSteps16; ++i)
+        page[i] = ld_key + 16 * i < ld.ke ? __ldg(table + ((ld_key + 16 * i) >> a.page_shift)) : 0;
+    }
+  };
+  auto issue = [&](int stage) {
+    if (ld_more) {
+      const uint32_t kdst = ring + stage * 2 * kStepBytes, vdst = kdst + kStepBytes;
+      bool bad = false;
+      // lane + 32 j is the j-th piece of this lane: C::kNC pieces a row
+      const int row0 = lane / C::kNC, c = lane % C::kNC;
+      constexpr int kRows = 32 / C::kNC;  // rows per round of the warp
+      int64_t base[C::kSteps16];
+#pragma unroll
+      for (int i = 0; i < C::kSteps16; ++i) {
+        const int pos = ld_key + 16 * i;
+        const bool ok = page[i] >= 0 && page[i] < a.num_pages;
+        if (pos < ld.ke && !ok) bad = true;
+        base[i] = pos < ld.ke && ok
+                      ? ((static_cast<int64_t>(page[i]) << a.page_shift) +
+                         (pos & ((1 << a.page_shift) - 1))) * row_stride +
+                            static_cast<int64_t>(ld.g) * C::kRB + 16 * c
+                      : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int row = row0 + j * kRows;
+        const int64_t at = base[(j * kRows) >> 4];
+        const bool real = at >= 0 && ld_key + row < ld.ke;
+        const int64_t off = real ? at + (row & 15) * row_stride : 0;
+        copy16(kdst + 16 * k_place<C::kNC>(row, c), a.k_pages + off, real);
+        copy16(vdst + 16 * v_place<C::kNC>(row, c), a.v_pages + off, real);
+      }
+      bad_steps = bad ? bad_steps | (1u << stage) : bad_steps & ~(1u << stage);
+      ld_key += C::kTile;
+      seek();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 
-    // Q fragments: 4 values of d per k-step; heads past the group are zero rows
+  // Q of a piece as it is in memory: 4 values of d per k-step; heads past the group: zeros
+  uint2 qraw[NT][C::kQS];
+  constexpr int EC = FP8 ? 16 : 8;  // values per K piece
+  auto load_q = [&](int b, int g) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = r + 8 * n;
+      const __nv_bfloat16* qp =
+          a.q + static_cast<int64_t>(b) * a.q_stride + static_cast<int64_t>(g * G + h) * D;
+#pragma unroll
+      for (int ks = 0; ks < C::kQS; ++ks) {
+        const int off = (q4 + 4 * (ks / (EC / 4))) * EC + 4 * (ks % (EC / 4));
+        qraw[n][ks] = h < G ? __ldg(reinterpret_cast<const uint2*>(qp + off)) : make_uint2(0u, 0u);
+      }
+    }
+  };
+
+  seek();
+  load_q(cur.b, cur.g);
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue(s);
+  int stage = 0;
+
+  while (true) {
+    // ---------------------------------------------------- one piece
     uint32_t qa[C::kQS][2 * NT];
     float c_log2[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int h = r + 8 * n;
-      const bool has = h < G;
-      const __nv_bfloat16* qp =
-          a.q + static_cast<int64_t>(b) * a.q_stride + static_cast<int64_t>(g * G + h) * D;
-      uint2 w[C::kQS];
-      constexpr int EC = FP8 ? 16 : 8;  // values per K chunk
-#pragma unroll
-      for (int ks = 0; ks < C::kQS; ++ks) {
-        const int off = (q4 + 4 * (ks / (EC / 4))) * EC + 4 * (ks % (EC / 4));
-        w[ks] = has ? __ldg(reinterpret_cast<const uint2*>(qp + off)) : make_uint2(0u, 0u);
-      }
       c_log2[n] = a.scale_log2;
       if (FP8) {
         uint32_t top = 0;
 #pragma unroll
         for (int ks = 0; ks < C::kQS; ++ks)
-          top = absmax_bf16x2(absmax_bf16x2(top, w[ks].x), w[ks].y);
+          top = absmax_bf16x2(absmax_bf16x2(top, qraw[n][ks].x), qraw[n][ks].y);
         float mx = absmax_bf16x2_value(top);
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
@@ -377,19 +487,21 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
         e = min(e, 126);  // a power of two that is a normal float, as is its inverse
         const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
         c_log2[n] *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        c_log2[n] *= __ldg(a.k_scale + static_cast<int64_t>(b) * a.hkv + g);
+        c_log2[n] *= __ldg(a.k_scale + static_cast<int64_t>(cur.b) * a.hkv + cur.g);
 #pragma unroll
         for (int ks = 0; ks < C::kQS; ++ks) {
-          w[ks].x = pack2<true>(__uint_as_float(w[ks].x << 16) * up,
-                                __uint_as_float(w[ks].x & 0xFFFF0000u) * up);
-          w[ks].y = pack2<true>(__uint_as_float(w[ks].y << 16) * up,
-                                __uint_as_float(w[ks].y & 0xFFFF0000u) * up);
+          const uint2 w = qraw[n][ks];
+          qa[ks][2 * n] = pack2<true>(__uint_as_float(w.x << 16) * up,
+                                      __uint_as_float(w.x & 0xFFFF0000u) * up);
+          qa[ks][2 * n + 1] = pack2<true>(__uint_as_float(w.y << 16) * up,
+                                          __uint_as_float(w.y & 0xFFFF0000u) * up);
         }
-      }
+      } else {
 #pragma unroll
-      for (int ks = 0; ks < C::kQS; ++ks) {
-        qa[ks][2 * n] = w[ks].x;
-        qa[ks][2 * n + 1] = w[ks].y;
+        for (int ks = 0; ks < C::kQS; ++ks) {
+          qa[ks][2 * n] = qraw[n][ks].x;
+          qa[ks][2 * n + 1] = qraw[n][ks].y;
+        }
       }
     }
 
@@ -404,72 +516,16 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][t][j] = 0.f;
     }
-
-    const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
-    const uint8_t* kg_base = a.k_pages + static_cast<int64_t>(g) * C::kRB;
-    const uint8_t* vg_base = a.v_pages + static_cast<int64_t>(g) * C::kRB;
     bool bad = false;
-    uint4 kr[C::kKG][C::kKChunks];
-    uint32_t vr[C::kSteps16][4][C::kVWords];
-    int64_t slot[C::kSteps16];  // pool row of each 16-key block of the next step; < 0: none
 
-    auto lookup = [&](int key0) {
-#pragma unroll
-      for (int i = 0; i < C::kSteps16; ++i) {
-        const int pos = key0 + 16 * i;
-        slot[i] = -1;
-        if (pos < ke) {
-          const int page = __ldg(table + (pos >> a.page_shift));
-          if (page >= 0 && page < a.num_pages)
-            slot[i] = (static_cast<int64_t>(page) << a.page_shift) +
-                      (pos & ((1 << a.page_shift) - 1));
-          else
-            bad = true;
-        }
-      }
-    };
-    auto load_k = [&](int key0) {
-#pragma unroll
-      for (int kg = 0; kg < C::kKG; ++kg) {
-        const int64_t s = slot[kg >> 1];
-        const bool ok = s >= 0 && key0 + 8 * kg + r < ke;
-        const uint8_t* p = kg_base + (s + 8 * (kg & 1) + r) * row_stride + 16 * q4;
-#pragma unroll
-        for (int i = 0; i < C::kKChunks; ++i)
-          kr[kg][i] = ok ? ld_kv16(p + 64 * i) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    auto load_v = [&](int key0) {
-#pragma unroll
-      for (int i = 0; i < C::kSteps16; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int kk = 2 * q4 + (j & 1) + 8 * (j >> 1);
-          const bool ok = slot[i] >= 0 && key0 + 16 * i + kk < ke;
-          const uint8_t* p = vg_base + (slot[i] + kk) * row_stride;
-          if constexpr (C::kVWords == 2) {
-            const uint2 x = ok ? ld_kv8(p + 8 * r) : make_uint2(0u, 0u);
-            vr[i][j][0] = x.x;
-            vr[i][j][1] = x.y;
-          } else {
-#pragma unroll
-            for (int c = 0; c < C::kVWords / 4; ++c) {
-              const uint4 x = ok ? ld_kv16(p + 16 * (r + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
-              vr[i][j][4 * c] = x.x;
-              vr[i][j][4 * c + 1] = x.y;
-              vr[i][j][4 * c + 2] = x.z;
-              vr[i][j][4 * c + 3] = x.w;
-            }
-          }
-        }
-    };
+    for (int key0 = cur.kb + warp * C::kKeys; key0 < cur.ke; key0 += C::kTile) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();  // every lane's copies are there, and the stage before was read
+      bad |= (bad_steps >> stage) & 1u;
+      issue(stage == 0 ? kStages - 1 : stage - 1);
+      const uint32_t kbuf = ring + stage * 2 * kStepBytes, vbuf = kbuf + kStepBytes;
+      stage = stage == kStages - 1 ? 0 : stage + 1;
 
-    int key0 = kb + warp * C::kKeys;
-    lookup(key0);
-    load_k(key0);
-    load_v(key0);
-    lookup(key0 + C::kTile);
-    for (; key0 < ke; key0 += C::kTile) {
       // ---- scores of this step's keys
       float s[C::kKG][4];
 #pragma unroll
@@ -477,7 +533,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
         s[kg][0] = s[kg][1] = s[kg][2] = s[kg][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < C::kKChunks; ++i) {
-          const uint32_t w[4] = {kr[kg][i].x, kr[kg][i].y, kr[kg][i].z, kr[kg][i].w};
+          const uint4 v = ld_shared16(kbuf + 16 * k_place<C::kNC>(8 * kg + r, q4 + 4 * i));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           if (FP8) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -495,8 +552,6 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
           }
         }
       }
-      const int next = key0 + C::kTile;
-      if (next < ke) load_k(next);
 
       // ---- running max and sum; x = score in log2 units
       float p[NT][C::kKG][2];
@@ -508,13 +563,14 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
         for (int kg = 0; kg < C::kKG; ++kg)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const bool see = key0 + 8 * kg + 2 * q4 + j < ke;
+            const bool see = key0 + 8 * kg + 2 * q4 + j < cur.ke;
             const float x = see ? s[kg][2 * n + j] * c_log2[n] : -INFINITY;
             p[n][kg][j] = x;
             mx[n] = fmaxf(mx[n], x);
           }
         if (a.raw != nullptr && r + 8 * n < G) {
-          float* row = a.raw + (static_cast<int64_t>(b) * a.hq + g * G + r + 8 * n) * a.raw_stride;
+          float* row =
+              a.raw + (static_cast<int64_t>(cur.b) * a.hq + cur.g * G + r + 8 * n) * a.raw_stride;
 #pragma unroll
           for (int kg = 0; kg < C::kKG; ++kg)  // rows are padded to whole tiles
             *reinterpret_cast<float2*>(row + key0 + 8 * kg + 2 * q4) =
@@ -571,41 +627,65 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
                            : pack2<false>(x[0] - __uint_as_float(hi[n][h] << 16),
                                           x[1] - __uint_as_float(hi[n][h] & 0xFFFF0000u));
           }
-        if (FP8) {
+        constexpr int kParts = C::kNC == 16 ? 2 : 1;  // 16-byte (or one 8-byte) parts of a lane
+        constexpr int kWords = C::kNC == 4 ? 2 : 4;
 #pragma unroll
-          for (int w = 0; w < C::kVWords; ++w)
+        for (int part = 0; part < kParts; ++part) {
+          uint32_t w[4][kWords];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;
-              const uint32_t x = __byte_perm(vr[i][0][w], vr[i][1][w], sel);
-              const uint32_t y = __byte_perm(vr[i][2][w], vr[i][3][w], sel);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma16816<true>(o[n][2 * w + h], e4m3_lo(x), e4m3_hi(x), e4m3_lo(y), e4m3_hi(y),
-                               hi[n][0], hi[n][1]);
+          for (int j = 0; j < 4; ++j) {
+            const int row = 16 * i + 2 * q4 + (j & 1) + 8 * (j >> 1);
+            if constexpr (C::kNC == 4) {
+              const uint2 x =
+                  ld_shared8(vbuf + 16 * v_place<C::kNC>(row, r >> 1) + 8 * (r & 1));
+              w[j][0] = x.x;
+              w[j][1] = x.y;
+            } else {
+              const uint4 x = ld_shared16(vbuf + 16 * v_place<C::kNC>(row, r + 8 * part));
+              w[j][0] = x.x;
+              w[j][1] = x.y;
+              w[j][2] = x.z;
+              w[j][3] = x.w;
             }
-        } else {
+          }
 #pragma unroll
-          for (int t = 0; t < C::kMT; ++t) {
-            const uint32_t a0 = __byte_perm(vr[i][0][t], vr[i][1][t], 0x5410);
-            const uint32_t a1 = __byte_perm(vr[i][0][t], vr[i][1][t], 0x7632);
-            const uint32_t a2 = __byte_perm(vr[i][2][t], vr[i][3][t], 0x5410);
-            const uint32_t a3 = __byte_perm(vr[i][2][t], vr[i][3][t], 0x7632);
+          for (int k = 0; k < kWords; ++k) {
+            if (FP8) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816<false>(o[n][t], a0, a1, a2, a3, hi[n][0], hi[n][1]);
-              mma16816<false>(o[n][t], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = h == 0 ? 0x5140u : 0x7362u;
+                const uint32_t x = __byte_perm(w[0][k], w[1][k], sel);
+                const uint32_t y = __byte_perm(w[2][k], w[3][k], sel);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  mma16816<true>(o[n][2 * k + h], e4m3_lo(x), e4m3_hi(x), e4m3_lo(y), e4m3_hi(y),
+                                 hi[n][0], hi[n][1]);
+              }
+            } else {
+              const uint32_t a0 = __byte_perm(w[0][k], w[1][k], 0x5410);
+              const uint32_t a1 = __byte_perm(w[0][k], w[1][k], 0x7632);
+              const uint32_t a2 = __byte_perm(w[2][k], w[3][k], 0x5410);
+              const uint32_t a3 = __byte_perm(w[2][k], w[3][k], 0x7632);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma16816<false>(o[n][4 * part + k], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+                mma16816<false>(o[n][4 * part + k], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+              }
             }
           }
         }
       }
-      if (next < ke) load_v(next);
-      lookup(next + C::kTile);
     }
 
+    // the next piece's queries are on their way while this one is put together
+    Piece nxt = cur;
+    const bool more = next_piece<C::kTile>(a, run.end, nxt);
+    if (more) load_q(nxt.b, nxt.g);
+
     // ---------------------------------------------------- the four warps' parts together
-    __syncthreads();  // s_bad is 0, the last piece's s_* were read
-    if (bad) s_bad = 1;
+    const float vs = FP8 ? __ldg(a.v_scale + static_cast<int64_t>(cur.b) * a.hkv + cur.g) : 1.f;
+    // slot 0: the run began inside this (b, g); slot 1: the run's last, begun here
+    const int64_t part = 2 * static_cast<int64_t>(cta) + (cur.at == cur.piece0 ? 1 : 0);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 1);
@@ -614,65 +694,52 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
         s_m[warp][8 * n + r] = m[n];
         s_l[warp][8 * n + r] = l[n];
       }
+      if (lane == 0) s_bad[warp] = bad;
 #pragma unroll
       for (int t = 0; t < C::kMT; ++t) {
         const int d = out_d<D, FP8>(r, t);
-        const int h0 = 8 * n + 2 * q4;
-        if (h0 < G)
-          *reinterpret_cast<float2*>(&s_o[warp][h0][d]) = make_float2(o[n][t][0], o[n][t][2]);
-        if (h0 + 1 < G)
-          *reinterpret_cast<float2*>(&s_o[warp][h0 + 1][d]) = make_float2(o[n][t][1], o[n][t][3]);
+        *reinterpret_cast<float2*>(&s_o[warp][2 * q4][d]) = make_float2(o[n][t][0], o[n][t][2]);
+        *reinterpret_cast<float2*>(&s_o[warp][2 * q4 + 1][d]) = make_float2(o[n][t][1], o[n][t][3]);
       }
-    }
-    __syncthreads();
-    const bool whole = at == piece0 && stop == piece0 + tiles;
-    // slot 0: the run began inside this (b, g); slot 1: the run's last, begun here
-    const int64_t part = 2 * static_cast<int64_t>(cta) + (at == piece0 ? 1 : 0);
-    const float vs = FP8 ? __ldg(a.v_scale + static_cast<int64_t>(b) * a.hkv + g) : 1.f;
-    for (int i = threadIdx.x; i < G * D; i += kDecThreads) {
-      const int h = i / D, d = i % D;
-      float top = s_m[0][h];
+      __syncthreads();
+      const bool any_bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
+      const int heads = min(8, G - 8 * n);
+      for (int i = threadIdx.x; i < heads * D; i += kDecThreads) {
+        const int h = i / D, d = i % D, hh = 8 * n + h;
+        float top = s_m[0][hh];
 #pragma unroll
-      for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, s_m[w][h]);
-      float sum = 0.f, acc = 0.f;
+        for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, s_m[w][hh]);
+        float sum = 0.f, acc = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float f = s_m[w][h] == -INFINITY ? 0.f : ex2(s_m[w][h] - top);
-        sum = fmaf(s_l[w][h], f, sum);
-        acc = fmaf(s_o[w][h][d], f, acc);
-      }
-      if (s_bad) sum = __int_as_float(0x7FFFFFFF);
-      const int64_t row = static_cast<int64_t>(b) * a.hq + g * G + h;
-      if (whole) {
-        a.out[row * D + d] = __float2bfloat16(acc / sum * vs);
-        if (d == 0) {
-          const float lse2 = top + (log2f(sum) - (FP8 ? 14.f : 0.f));
-          if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
-          if (a.lse2 != nullptr) a.lse2[row] = lse2;
+        for (int w = 0; w < kDecWarps; ++w) {
+          const float f = s_m[w][hh] == -INFINITY ? 0.f : ex2(s_m[w][hh] - top);
+          sum = fmaf(s_l[w][hh], f, sum);
+          acc = fmaf(s_o[w][h][d], f, acc);
         }
-      } else {
-        a.part_o[(part * G + h) * D + d] = acc;
-        if (d == 0) a.part_ml[part * G + h] = make_float2(top, sum);
+        if (any_bad) sum = __int_as_float(0x7FFFFFFF);
+        const int64_t row = static_cast<int64_t>(cur.b) * a.hq + cur.g * G + hh;
+        if (cur.whole) {
+          a.out[row * D + d] = __float2bfloat16(acc / sum * vs);
+          if (d == 0) {
+            const float lse2 = top + (log2f(sum) - (FP8 ? 14.f : 0.f));
+            if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
+            if (a.lse2 != nullptr) a.lse2[row] = lse2;
+          }
+        } else {
+          a.part_o[(part * G + hh) * D + d] = acc;
+          if (d == 0) a.part_ml[part * G + hh] = make_float2(top, sum);
+        }
       }
+      if (n == 0 && threadIdx.x == 0) {
+        if (any_bad) atomicOr(a.err_word, kErrDeviceBounds);
+        if (!cur.whole && cur.at == cur.piece0)  // goes on in the next CTAs: the join's entry
+          a.rec[cta] = DecodeRec{run.total, cur.b, cur.g,
+                                 cur.piece0 + (cur.len + C::kTile - 1) / C::kTile};
+      }
+      __syncthreads();  // the shared parts may be overwritten
     }
-    if (threadIdx.x == 0 && s_bad) atomicOr(a.err_word, kErrDeviceBounds);
-    if (threadIdx.x == 0 && !whole) {
-      if (at == piece0)  // begun here, goes on in the next CTAs: the join's entry
-        a.rec[cta] = DecodeRec{run.total, b, g, piece0 + tiles};
-    }
-
-    // ---------------------------------------------------- the next (sequence, head)
-    at = stop;
-    if (at >= run.end) return;
-    piece0 = stop;
-    if (++g == a.hkv) {
-      g = 0;
-      do {
-        len = checked_len(a, ++b);
-      } while (len <= 0);
-      tiles = (len + C::kTile - 1) / C::kTile;
-    }
-    __syncthreads();  // everyone has read s_bad
+    if (!more) break;
+    cur = nxt;
   }
 }
 
@@ -788,9 +855,12 @@ __global__ void __launch_bounds__(256) paged_weights_kernel(const PagedDecodeArg
 template <int D, bool FP8, int NT>
 cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
   using C = DecCfg<D, FP8>;
-  const int ctas = decode_ctas(num_sms, a.num_seqs, a.hkv, a.max_len, C::kTile, NT);
-  paged_decode_kernel<D, FP8, NT><<<ctas, kDecThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const int ctas = decode_ctas(num_sms, a.num_seqs, a.hkv, a.max_len, C::kTile);
+  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D, FP8, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  paged_decode_kernel<D, FP8, NT><<<ctas, kDecThreads, C::kSmem, stream>>>(a);
+  e = cudaGetLastError();
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -817,12 +887,12 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
 }  // namespace
 
 int decode_tile_keys(int head_dim, bool fp8) {
-  return kDecWarps * 16 * (256 / (head_dim * (fp8 ? 1 : 2)));
+  return kDecWarps * kStepBytes / (head_dim * (fp8 ? 1 : 2));
 }
 
-int decode_ctas(int num_sms, int num_seqs, int hkv, int max_len, int tile, int nt) {
+int decode_ctas(int num_sms, int num_seqs, int hkv, int max_len, int tile) {
   const int64_t most = static_cast<int64_t>(num_seqs) * hkv * ((max_len + tile - 1) / tile);
-  int64_t full = static_cast<int64_t>(num_sms) * (nt == 1 ? 3 : 2);
+  int64_t full = static_cast<int64_t>(num_sms) * 2;
   if (full > kDecodeMaxCtas) full = kDecodeMaxCtas;  // the workspace holds so many partials
   return static_cast<int>(most < 1 ? 1 : most < full ? most : full);
 }

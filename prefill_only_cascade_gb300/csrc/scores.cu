@@ -231,20 +231,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
     float lost = 0.f;                 // what the running sum has rounded away
     bool ok = true;
-    // -lse log2(e) of this thread's query row of tile i; a row that saw nothing (-inf)
-    // gives no weight
-    auto row_nlse = [&](int i) {
+    // lse of this thread's query row of tile i, loaded a tile ahead
+    auto row_lse = [&](int i) {
       const int t = f + (t_first + rank + i * cluster) * tok + row / G;
-      if (i >= mine || t >= nq) return 0.f;
-      const float v = __ldg(a.lse + (q0 + t) * a.hq + g * G + row % G);
-      return v == -INFINITY ? -INFINITY : v * -1.4426950408889634f;
+      return i < mine && t < nq ? __ldg(a.lse + (q0 + t) * a.hq + g * G + row % G) : 0.f;
     };
-    float nl = row_nlse(0);
+    float l = row_lse(0);
     for (int i = 0; i < mine; ++i) {
       const int buf = i & 1;
-      sh.nlse[buf][row] = nl;
+      // a row that saw nothing (-inf) gives no weight
+      sh.nlse[buf][row] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      nl = row_nlse(i + 1);
+      l = row_lse(i + 1);
       // after a wait that ran out every warp still takes part in the barriers
       ok = ok && __all_sync(0xFFFFFFFFu, wait_parity(wc, &sh.s_full[buf], (i >> 1) & 1u));
       if (!ok) continue;
