@@ -6,14 +6,20 @@
 // GPU", section "Como funciona": the anchor is prefilled once and kept; these sums say which
 // of its tokens are worth keeping). No second softmax pass is needed, and no V.
 //
-// The product runs transposed, S^T = K Q^T, one 128-key tile of a (sequence, KV head) per
-// CTA: a key is one TMEM lane, so the sum over queries stays in one thread's registers and
-// nothing is reduced across lanes, and the result does not depend on any order of atomics.
-// K stays in shared memory, 128-row query tiles (128 / G tokens x G heads, as one TMA box)
-// stream through a ring, and S^T is double-buffered in TMEM: the tensor cores fill one tile
-// while four warps exponentiate the other. Bound: with many queries the exponentials (one
-// per (query row, key); ~30 results/clk/SM) and the MMA (~512 clk per 128 x 128 x 128) are
-// about equal, with few (a window) reading K once from HBM.
+// The product runs transposed, S^T = K Q^T, in 128 x 128 tiles: a key is one TMEM lane, so
+// the sum over queries stays in one thread's registers, nothing is reduced across lanes and
+// the result does not depend on any order of atomics. Two kernels:
+//   attn_scores_kernel   a CTA keeps 256 keys of a (sequence, KV head) in shared memory and
+//     streams 128-row query tiles (128 / G tokens x G heads, as one TMA box) past them. Per
+//     tile and SM the MMA (2 x ~512 clk) and the exponentials (2 x 512 clk of the MUFU) are
+//     about equal, and both bound it: 16 softmax warps (four warpgroups, one per key tile and
+//     parity of the query tile, each with its own S^T in TMEM) keep the MUFU fed while the
+//     tensor cores fill the other parity. 256 keys and not 128, so that a query tile is read
+//     from L2 once per two products (~9 TB/s at full rate instead of 18).
+//   attn_scores_window_kernel   where the queries of a (sequence, KV head) fit one tile (the
+//     last 32 tokens at G = 4), the tile stays and the keys stream past it: bound by reading
+//     K once from HBM.
+
 #include <cstddef>
 #include <cstdint>
 
@@ -26,29 +32,50 @@ namespace {
 
 constexpr int kBM = 128;            // keys per tile (TMEM lanes)
 constexpr int kBN = 128;            // query rows per tile (TMEM columns)
-constexpr int kThreads = 192;       // 4 softmax warps, the TMA warp, the MMA warp
-constexpr int kWarpLoad = 4, kWarpMma = 5;
-constexpr uint32_t kTmemCols = 256;  // two S^T tiles; two CTAs share an SM
 constexpr int kBlock = 128 * 128;   // bytes of 128 rows x 64 columns of bf16
+constexpr int kMaxCluster = 8;
+
+// attn_scores_kernel
+constexpr int kKeyTiles = 2;        // key tiles of a CTA
+constexpr int kGroups = 2 * kKeyTiles;  // softmax warpgroups: (key tile, query tile parity)
+constexpr int kThreads = 128 * kGroups + 64;  // + the TMA warp and the MMA warp
+constexpr int kWarpLoad = 4 * kGroups, kWarpMma = 4 * kGroups + 1;
+constexpr int kQStages = 4;
+
+// attn_scores_window_kernel
+constexpr int kWinThreads = 2 * 128 + 64;   // two warpgroups take the key tiles in turn
+constexpr int kWinLoad = 8, kWinMma = 9;
+constexpr int kWinStages = 2;               // key tiles in flight; two CTAs share an SM
 
 template <int D>
 struct Cfg {
   static constexpr int kKB = D / 64;               // 64-column blocks
-  static constexpr int kTileBytes = kKB * kBlock;  // of K, and of a query stage
-  static constexpr int kStages = 256 / D;
-  static constexpr int kSmem = kTileBytes * (1 + kStages) + 1024;  // + alignment slack
+  static constexpr int kTileBytes = kKB * kBlock;  // 128 rows of K or Q
+  static constexpr int kSmem = kTileBytes * (kKeyTiles + kQStages) + 1024;  // + alignment slack
+  static constexpr int kWinSmem = kTileBytes * (1 + kWinStages) + 1024;
 };
 
 struct Shared {
-  alignas(16) float nlse[2][kBN];   // -lse * log2(e) of the tile's query rows (16-byte loads)
-  alignas(16) float part[8][kBM];   // rank 0: the other CTAs' sums
+  alignas(16) float nlse[kGroups][2][kBN];  // -lse * log2(e) of a tile's query rows
+  alignas(16) float part[kMaxCluster][kKeyTiles * kBM];  // others' sums: rank 0's own odd
+                                            // tiles in row 0, the cluster's CTAs behind
   uint64_t k_full, drain;
-  uint64_t q_full[4], q_empty[4];
+  uint64_t q_full[kQStages], q_empty[kQStages];
+  uint64_t s_full[kGroups], s_empty[kGroups];
+  uint32_t tmem;
+  int abort_flag;
+};
+struct WinShared {
+  alignas(16) float nlse[kBN];
+  uint64_t q_full, drain;
+  uint64_t k_full[kWinStages], k_empty[kWinStages];
   uint64_t s_full[2], s_empty[2];
   uint32_t tmem;
   int abort_flag;
 };
-static_assert(offsetof(Shared, nlse) % 16 == 0 && alignof(Shared) == 16, "16-byte loads of nlse");
+static_assert(offsetof(Shared, nlse) % 16 == 0 && offsetof(WinShared, nlse) % 16 == 0 &&
+                  alignof(Shared) == 16 && alignof(WinShared) == 16,
+              "16-byte loads of nlse");
 
 // Waits until `bar` reaches the phase, at most until `deadline`: before leaving, no copy or
 // MMA of this CTA may be in flight.
@@ -92,8 +119,74 @@ __device__ __forceinline__ void add_columns(const uint32_t (&s)[32], const float
   }
 }
 
+// What sequence s asks for: key and query ranges, and the queries of the window.
+struct SeqRange {
+  int64_t k0, q0;
+  int nk, nq;
+  int w;    // queries of the window
+  int f;    // the first of them
+  int off;  // causal: query i sees keys 0 .. i + off
+};
+__device__ __forceinline__ bool seq_range(const AttnScoresArgs& a, int s, SeqRange& r) {
+  r.k0 = __ldg(a.k_offsets + s);
+  r.q0 = __ldg(a.q_offsets + s);
+  const int64_t nk = __ldg(a.k_offsets + s + 1) - r.k0, nq = __ldg(a.q_offsets + s + 1) - r.q0;
+  if (r.k0 < 0 || nk < 0 || nk > a.max_k || r.k0 + nk > a.total_k || r.q0 < 0 || nq < 0 ||
+      nq > a.max_q || r.q0 + nq > a.total_q)
+    return false;
+  r.nk = static_cast<int>(nk);
+  r.nq = static_cast<int>(nq);
+  r.w = a.window > 0 ? min(a.window, r.nq) : r.nq;
+  r.f = r.nq - r.w;
+  r.off = r.nk - r.nq;
+  return true;
+}
+
+// Adds the weights of one S^T tile (in TMEM at t_tile, this thread's lane) that this thread's
+// key receives. Query rows [lo, hi) see it; `whole`: all rows see all keys of the tile.
+// Releases the TMEM tile as soon as it is in registers.
+__device__ __forceinline__ float tile_weight(uint32_t t_tile, const float* nlse, uint64_t c2,
+                                             bool whole, int lo, int hi, uint64_t* s_empty) {
+  uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t v[32];
+    tmem_ld32(t_tile + 32 * q, v);
+    tmem_wait_ld_dep(v);
+    if (q == 3) {
+      tc_fence_before();
+      mbar_arrive(s_empty);
+    }
+    if (whole)
+      add_columns<false>(v, nlse + 32 * q, c2, 0, 0, acc);
+    else
+      add_columns<true>(v, nlse + 32 * q, c2, lo - 32 * q, hi - 32 * q, acc);
+  }
+  float x0, x1, y0, y1;
+  f2_split(f2_add(acc[0], acc[1]), x0, x1);
+  f2_split(f2_add(acc[2], acc[3]), y0, y1);
+  return (x0 + x1) + (y0 + y1);
+}
+
+// First query row of the tile at query token t0 that sees key j.
+__device__ __forceinline__ int first_row(int j, int off, int t0, int G) {
+  const int64_t n = (static_cast<int64_t>(j) - off - t0) * G;
+  return n < 0 ? 0 : n > kBN ? kBN : static_cast<int>(n);
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__device__ __forceinline__ void mma_tile(uint32_t d_tmem, uint32_t k_lo, uint32_t q_lo) {
+  constexpr uint32_t kIdesc = idesc_f16(kBM, kBN, 1, 0);
+  constexpr uint32_t kDescHi = sw128_desc_hi(1024);  // 8-row groups 1024 bytes apart
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t adv = (kk >> 2) * (kBlock >> 4) + (kk & 3) * 2;
+    mma_ss_lohi(d_tmem, k_lo + adv, kDescHi, q_lo + adv, kDescHi, kIdesc, kk > 0 ? 1u : 0u);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
     attn_scores_kernel(const AttnScoresArgs a, const __grid_constant__ CUtensorMap q_map,
                        const __grid_constant__ CUtensorMap k_map, int cluster) {
   using C = Cfg<D>;
@@ -101,48 +194,47 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~1023ull);
   uint8_t* s_k = smem;
-  uint8_t* s_q = smem + C::kTileBytes;
+  uint8_t* s_q = smem + kKeyTiles * C::kTileBytes;
   const int warp = threadIdx.x >> 5;
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
 
-  // blocks in the order key tile, sequence, head: with causal masking the first key tiles
-  // have the most queries, so the long CTAs start first
+  // blocks in the order keys, sequence, head: with causal masking the first keys have the
+  // most queries, so the long CTAs start first
   int id = blockIdx.x / cluster;
   const int g = id % a.hkv;
   id /= a.hkv;
-  const int s = id % a.num_seqs, tile = id / a.num_seqs;
-  const int64_t k0 = __ldg(a.k_offsets + s), nk64 = __ldg(a.k_offsets + s + 1) - k0;
-  const int64_t q0 = __ldg(a.q_offsets + s), nq64 = __ldg(a.q_offsets + s + 1) - q0;
-  if (k0 < 0 || nk64 < 0 || nk64 > a.max_k || k0 + nk64 > a.total_k || q0 < 0 || nq64 < 0 ||
-      nq64 > a.max_q || q0 + nq64 > a.total_q) {
+  const int s = id % a.num_seqs;
+  const int j0 = id / a.num_seqs * (kKeyTiles * kBM);
+  SeqRange sr;
+  if (!seq_range(a, s, sr)) {
     if (threadIdx.x == 0) atomicOr(a.err_word, kErrDeviceBounds);
     return;
   }
-  const int nk = static_cast<int>(nk64), nq = static_cast<int>(nq64);
-  const int j0 = tile * kBM;
-  if (j0 >= nk) return;
+  if (j0 >= sr.nk) return;
 
   const int G = a.group, tok = kBN / G;
-  const int w = a.window > 0 ? min(a.window, nq) : nq;
-  const int f = nq - w;               // first query token of the window
-  const int off = nk - nq;            // causal: query i sees keys 0 .. i + off
-  const int tiles = (w + tok - 1) / tok;
-  int t_first = 0;                    // first query tile that sees the key tile
-  if (a.causal) {
-    const int first_query = j0 - off;  // may be negative
-    if (first_query > f) t_first = min(tiles, (first_query - f) / tok);
+  const int tiles = (sr.w + tok - 1) / tok;
+  // first query tile that sees each key tile (tiles: none, or no such keys)
+  int t_first[kKeyTiles];
+#pragma unroll
+  for (int kt = 0; kt < kKeyTiles; ++kt) {
+    const int query = j0 + kt * kBM - sr.off - sr.f;  // of the window; may be negative
+    t_first[kt] = a.causal && query > 0 ? min(tiles, query / tok) : 0;
+    if (j0 + kt * kBM >= sr.nk) t_first[kt] = tiles;
   }
-  // the CTAs of a cluster take the query tiles in turn
-  const int mine = tiles - t_first > rank ? (tiles - t_first - rank + cluster - 1) / cluster : 0;
+  // the CTAs of a cluster take the query tiles in turn: this one's i-th is tile_at(i)
+  const int left = tiles - t_first[0];
+  const int mine = left > rank ? (left - rank + cluster - 1) / cluster : 0;
+  auto tile_at = [&](int i) { return t_first[0] + rank + i * cluster; };
 
   if (threadIdx.x == 0) {
     mbar_init(&sh.k_full, 1);
     mbar_init(&sh.drain, 1);
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < kQStages; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], 128);
     }
@@ -150,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     fence_mbar_init();
   }
   if (warp == kWarpMma) {
-    tmem_alloc(&sh.tmem, kTmemCols);
+    tmem_alloc(&sh.tmem, 128 * kGroups);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -167,21 +259,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint64_t keep = l2_policy_evict_last();  // queries: read by every key tile
       const uint64_t once = l2_policy_evict_first();
       if (leader) {
-        mbar_arrive_expect_tx(&sh.k_full, C::kTileBytes);
-        for (int kb = 0; kb < C::kKB; ++kb)
-          tma_load_3d_hint(&k_map, &sh.k_full, s_k + kb * kBlock, kb * 64, g,
-                           static_cast<int>(k0) + j0, once);
+        mbar_arrive_expect_tx(&sh.k_full, kKeyTiles * C::kTileBytes);
+        for (int kt = 0; kt < kKeyTiles; ++kt)  // keys past the tensor read as zeros
+          for (int kb = 0; kb < C::kKB; ++kb)
+            tma_load_3d_hint(&k_map, &sh.k_full, s_k + kt * C::kTileBytes + kb * kBlock, kb * 64,
+                             g, static_cast<int>(sr.k0) + j0 + kt * kBM, once);
       }
       __syncwarp();
       bool ok = true;
       int armed = 0;
       for (int i = 0; i < mine && ok; ++i) {
-        const int st = i % C::kStages;
-        ok = wait_parity_warp(wc, &sh.q_empty[st], ((i / C::kStages) & 1) ^ 1u);
+        const int st = i % kQStages;
+        ok = wait_parity_warp(wc, &sh.q_empty[st], ((i / kQStages) & 1) ^ 1u);
         if (!ok) break;
         if (leader) {
           mbar_arrive_expect_tx(&sh.q_full[st], C::kTileBytes);
-          const int t = static_cast<int>(q0) + f + (t_first + rank + i * cluster) * tok;
+          const int t = static_cast<int>(sr.q0) + sr.f + tile_at(i) * tok;
           for (int kb = 0; kb < C::kKB; ++kb)
             tma_load_3d_hint(&q_map, &sh.q_full[st], s_q + st * C::kTileBytes + kb * kBlock,
                              kb * 64, g * G, t, keep);
@@ -191,34 +284,43 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const uint64_t deadline = global_timer_ns() + 100000000ull;
       drain(&sh.k_full, 0, deadline);
-      for (int i = armed > C::kStages ? armed - C::kStages : 0; i < armed; ++i)
-        drain(&sh.q_full[i % C::kStages], (i / C::kStages) & 1u, deadline);
+      for (int i = armed > kQStages ? armed - kQStages : 0; i < armed; ++i)
+        drain(&sh.q_full[i % kQStages], (i / kQStages) & 1u, deadline);
     }
   } else if (warp == kWarpMma) {
     if (mine > 0) {
       const bool leader = elect_one();
-      constexpr uint32_t kIdesc = idesc_f16(kBM, kBN, 1, 0);
-      constexpr uint32_t kDescHi = sw128_desc_hi(1024);  // 8-row groups 1024 bytes apart
       const uint32_t k_lo = sw128_desc_lo(smem_u32(s_k), 16);
-      const uint32_t q_lo0 = sw128_desc_lo(smem_u32(s_q), 16);
+      const uint32_t q_lo = sw128_desc_lo(smem_u32(s_q), 16);
+      uint32_t used[kGroups] = {0, 0, 0, 0};
       bool ok = wait_parity_warp(wc, &sh.k_full, 0);
       for (int i = 0; i < mine && ok; ++i) {
-        const int st = i % C::kStages, buf = i & 1;
-        ok = wait_parity_warp(wc, &sh.q_full[st], (i / C::kStages) & 1u) &&
-             wait_parity_warp(wc, &sh.s_empty[buf], ((i >> 1) & 1) ^ 1u);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint32_t q_lo = q_lo0 + st * (C::kTileBytes >> 4);
+        const int st = i % kQStages;
+        ok = wait_parity_warp(wc, &sh.q_full[st], (i / kQStages) & 1u);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t adv = (kk >> 2) * (kBlock >> 4) + (kk & 3) * 2;
-            mma_ss_lohi(tmem + 128u * buf, k_lo + adv, kDescHi, q_lo + adv, kDescHi, kIdesc,
-                        kk > 0 ? 1u : 0u);
+        for (int kt = 0; kt < kKeyTiles; ++kt) {
+          if (!ok || tile_at(i) < t_first[kt]) continue;
+          const int grp = 2 * kt + (i & 1);
+          // the group's last tile is in its registers
+          const uint32_t parity = (kt == 0 ? ((i & 1) ? used[1] : used[0])
+                                           : ((i & 1) ? used[3] : used[2])) & 1u;
+          ok = wait_parity_warp(wc, &sh.s_empty[grp], parity ^ 1u);
+          if (!ok) continue;
+          tc_fence_after();
+          if (leader) {
+            mma_tile<D>(tmem + 128u * grp, k_lo + kt * (C::kTileBytes >> 4),
+                        q_lo + st * (C::kTileBytes >> 4));
+            mma_commit(&sh.s_full[grp]);
           }
-          mma_commit(&sh.q_empty[st]);
-          mma_commit(&sh.s_full[buf]);
+          __syncwarp();
+          if (kt == 0) {
+            if (i & 1) ++used[1]; else ++used[0];
+          } else {
+            if (i & 1) ++used[3]; else ++used[2];
+          }
         }
+        if (!ok) break;
+        if (leader) mma_commit(&sh.q_empty[st]);
         __syncwarp();
       }
       if (leader) mma_commit(&sh.drain);
@@ -226,80 +328,198 @@ __global__ void __launch_bounds__(kThreads, 2)
       drain(&sh.drain, 0, global_timer_ns() + 100000000ull);
     }
   } else {
-    const int row = threadIdx.x;      // key j0 + row, TMEM lane `row`
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int grp = warp >> 2, kt = grp >> 1;
+    const int row = threadIdx.x & 127;  // key j0 + 128 kt + row, TMEM lane `row`
+    const int key = j0 + kt * kBM + row;
+    const uint32_t t_tile = tmem + 128u * grp + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
-    float lost = 0.f;                 // what the running sum has rounded away
+    float lost = 0.f;                   // what the running sum has rounded away
     bool ok = true;
-    // lse of this thread's query row of tile i, loaded a tile ahead
+    // lse of this thread's query row of the i-th tile, loaded a tile ahead
     auto row_lse = [&](int i) {
-      const int t = f + (t_first + rank + i * cluster) * tok + row / G;
-      return i < mine && t < nq ? __ldg(a.lse + (q0 + t) * a.hq + g * G + row % G) : 0.f;
+      const int t = sr.f + tile_at(i) * tok + row / G;
+      return i < mine && t < sr.nq ? __ldg(a.lse + (sr.q0 + t) * a.hq + g * G + row % G) : 0.f;
     };
-    float l = row_lse(0);
-    for (int i = 0; i < mine; ++i) {
-      const int buf = i & 1;
+    int i = grp & 1;
+    while (i < mine && tile_at(i) < t_first[kt]) i += 2;
+    float l = row_lse(i);
+    for (uint32_t n = 0; i < mine; i += 2, ++n) {
+      float* nlse = sh.nlse[grp][n & 1];
       // a row that saw nothing (-inf) gives no weight
-      sh.nlse[buf][row] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      l = row_lse(i + 1);
+      nlse[row] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+      asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
+      l = row_lse(i + 2);
       // after a wait that ran out every warp still takes part in the barriers
-      ok = ok && __all_sync(0xFFFFFFFFu, wait_parity(wc, &sh.s_full[buf], (i >> 1) & 1u));
+      ok = ok && __all_sync(0xFFFFFFFFu, wait_parity(wc, &sh.s_full[grp], n & 1u));
       if (!ok) continue;
       tc_fence_after();
-      const int t0 = f + (t_first + rank + i * cluster) * tok;
-      // query rows [lo, hi) of the tile see this thread's key
-      const int hi = nq - t0 >= tok ? kBN : (nq - t0) * G;
-      int lo = 0;
-      if (a.causal) {
-        const int64_t first = (static_cast<int64_t>(j0) + row - off - t0) * G;
-        lo = first < 0 ? 0 : first > kBN ? kBN : static_cast<int>(first);
-      }
-      const bool masked = hi < kBN || (a.causal && j0 + kBM - 1 > t0 + off);
-      uint64_t acc[4] = {0, 0, 0, 0};
-      uint32_t v[2][32];
-      tmem_ld32(t_lane + 128u * buf, v[0]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        tmem_wait_ld_dep(v[q & 1]);
-        if (q < 3) {
-          tmem_ld32(t_lane + 128u * buf + 32 * (q + 1), v[(q + 1) & 1]);
-        } else {  // the tile is in registers: its TMEM may be overwritten
-          tc_fence_before();
-          mbar_arrive(&sh.s_empty[buf]);
-        }
-        if (masked)
-          add_columns<true>(v[q & 1], &sh.nlse[buf][32 * q], c2, lo - 32 * q, hi - 32 * q, acc);
-        else
-          add_columns<false>(v[q & 1], &sh.nlse[buf][32 * q], c2, 0, 0, acc);
-      }
-      float x0, x1, y0, y1;
-      f2_split(f2_add(acc[0], acc[1]), x0, x1);
-      f2_split(f2_add(acc[2], acc[3]), y0, y1);
+      const int t0 = sr.f + tile_at(i) * tok;
+      const bool whole =
+          t0 + tok <= sr.nq && !(a.causal && j0 + (kt + 1) * kBM - 1 > t0 + sr.off);
+      const int hi = sr.nq - t0 >= tok ? kBN : (sr.nq - t0) * G;
+      const int lo = a.causal && !whole ? first_row(key, sr.off, t0, G) : 0;
       // compensated: thousands of tiles may add up (Kahan)
-      const float y = ((x0 + x1) + (y0 + y1)) - lost;
-      const float t = total + y;
-      lost = fabsf(t) < INFINITY ? (t - total) - y : 0.f;
-      total = t;
+      const float y = tile_weight(t_tile, nlse, c2, whole, lo, hi, &sh.s_empty[grp]) - lost;
+      const float sum = total + y;
+      lost = fabsf(sum) < INFINITY ? (sum - total) - y : 0.f;
+      total = sum;
     }
+    if (grp & 1) sh.part[0][kt * kBM + row] = total;
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, 128 * kGroups);
   }
+  const bool owner = warp < kWarpLoad && !((warp >> 2) & 1);  // the even groups
+  const int at = (warp >> 3) * kBM + (threadIdx.x & 127);     // key of the thread
+  if (owner) total += sh.part[0][at];
   if (cluster > 1) {  // the cluster's sums, added in rank order by its first CTA
-    if (rank > 0 && threadIdx.x < kBM)
-      st_cluster_f32(cluster_map(&sh.part[rank][threadIdx.x], 0), total);
+    if (rank > 0 && owner) st_cluster_f32(cluster_map(&sh.part[rank][at], 0), total);
     cluster_sync();
     if (rank > 0) return;
-    if (threadIdx.x < kBM)
-      for (int r = 1; r < cluster; ++r) total += sh.part[r][threadIdx.x];
+    if (owner)
+      for (int r = 1; r < cluster; ++r) total += sh.part[r][at];
   }
-  if (threadIdx.x < kBM && j0 + static_cast<int>(threadIdx.x) < nk) {
-    const int64_t at = (static_cast<int64_t>(s) * a.hkv + g) * a.score_stride + j0 + threadIdx.x;
-    a.score_out[at] = a.score_in != nullptr ? a.score_in[at] + total : total;
+  if (owner && j0 + at < sr.nk) {
+    const int64_t out = (static_cast<int64_t>(s) * a.hkv + g) * a.score_stride + j0 + at;
+    a.score_out[out] = a.score_in != nullptr ? a.score_in[out] + total : total;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWinThreads, 2)
+    attn_scores_window_kernel(const AttnScoresArgs a, const __grid_constant__ CUtensorMap q_map,
+                              const __grid_constant__ CUtensorMap k_map, int run) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t dyn[];
+  __shared__ WinShared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~1023ull);
+  uint8_t* s_q = smem;
+  uint8_t* s_k = smem + C::kTileBytes;
+  const int warp = threadIdx.x >> 5;
+  int id = blockIdx.x;
+  const int g = id % a.hkv;
+  id /= a.hkv;
+  const int s = id % a.num_seqs;
+  const int j0 = id / a.num_seqs * run * kBM;
+  SeqRange sr;
+  if (!seq_range(a, s, sr)) {
+    if (threadIdx.x == 0) atomicOr(a.err_word, kErrDeviceBounds);
+    return;
+  }
+  if (j0 >= sr.nk) return;
+  const int G = a.group;
+  const int count = min(run, (sr.nk - j0 + kBM - 1) / kBM);  // key tiles of this CTA
+  const int64_t out0 = (static_cast<int64_t>(s) * a.hkv + g) * a.score_stride;
+  if (sr.w == 0) {  // no queries
+    for (int j = j0 + threadIdx.x; j < min(sr.nk, j0 + count * kBM); j += kWinThreads)
+      a.score_out[out0 + j] = a.score_in != nullptr ? a.score_in[out0 + j] : 0.f;
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.drain, 1);
+    for (int i = 0; i < kWinStages; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_empty[i], 128);
+    }
+    sh.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWinMma) {
+    tmem_alloc(&sh.tmem, 256);
+    tmem_relinquish();
+  }
+  if (threadIdx.x < kBN) {
+    const int t = sr.f + threadIdx.x / G;
+    const float l = t < sr.nq ? __ldg(a.lse + (sr.q0 + t) * a.hq + g * G + threadIdx.x % G) : 0.f;
+    sh.nlse[threadIdx.x] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const WaitCtl wc{a.timeout_ns, &sh.abort_flag, a.err_word};
+
+  if (warp == kWinLoad) {
+    const bool leader = elect_one();
+    const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+    bool ok = true;
+    int armed = 0;
+    for (int i = 0; i < count && ok; ++i) {
+      const int st = i % kWinStages;
+      ok = wait_parity_warp(wc, &sh.k_empty[st], ((i / kWinStages) & 1) ^ 1u);
+      if (!ok) break;
+      if (leader) {
+        mbar_arrive_expect_tx(&sh.k_full[st], C::kTileBytes);
+        for (int kb = 0; kb < C::kKB; ++kb)
+          tma_load_3d_hint(&k_map, &sh.k_full[st], s_k + st * C::kTileBytes + kb * kBlock, kb * 64,
+                           g, static_cast<int>(sr.k0) + j0 + i * kBM, once);
+        if (i == 0) {
+          mbar_arrive_expect_tx(&sh.q_full, C::kTileBytes);
+          for (int kb = 0; kb < C::kKB; ++kb)
+            tma_load_3d_hint(&q_map, &sh.q_full, s_q + kb * kBlock, kb * 64, g * G,
+                             static_cast<int>(sr.q0) + sr.f, keep);
+        }
+      }
+      __syncwarp();
+      ++armed;
+    }
+    const uint64_t deadline = global_timer_ns() + 100000000ull;
+    if (armed > 0) drain(&sh.q_full, 0, deadline);
+    for (int i = armed > kWinStages ? armed - kWinStages : 0; i < armed; ++i)
+      drain(&sh.k_full[i % kWinStages], (i / kWinStages) & 1u, deadline);
+  } else if (warp == kWinMma) {
+    const bool leader = elect_one();
+    const uint32_t k_lo = sw128_desc_lo(smem_u32(s_k), 16);
+    const uint32_t q_lo = sw128_desc_lo(smem_u32(s_q), 16);
+    bool ok = wait_parity_warp(wc, &sh.q_full, 0);
+    for (int i = 0; i < count && ok; ++i) {
+      const int st = i % kWinStages, buf = i & 1;
+      ok = wait_parity_warp(wc, &sh.k_full[st], (i / kWinStages) & 1u) &&
+           wait_parity_warp(wc, &sh.s_empty[buf], ((i >> 1) & 1) ^ 1u);
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+        mma_tile<D>(tmem + 128u * buf, k_lo + st * (C::kTileBytes >> 4), q_lo);
+        mma_commit(&sh.k_empty[st]);
+        mma_commit(&sh.s_full[buf]);
+      }
+      __syncwarp();
+    }
+    if (leader) mma_commit(&sh.drain);
+    __syncwarp();
+    drain(&sh.drain, 0, global_timer_ns() + 100000000ull);
+  } else {
+    const int grp = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t t_tile = tmem + 128u * grp + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
+    const int rows = sr.w * G;
+    for (int i = grp; i < count; i += 2) {
+      const int key = j0 + i * kBM + row;
+      const bool real = key < sr.nk;
+      const float base = real && a.score_in != nullptr ? a.score_in[out0 + key] : 0.f;
+      if (!__all_sync(0xFFFFFFFFu, wait_parity(wc, &sh.s_full[grp], (i >> 1) & 1u))) break;
+      tc_fence_after();
+      const bool whole =
+          rows == kBN && !(a.causal && j0 + (i + 1) * kBM - 1 > sr.f + sr.off);
+      const int lo = a.causal && !whole ? first_row(key, sr.off, sr.f, G) : 0;
+      const float w = tile_weight(t_tile, sh.nlse, c2, whole, lo, rows, &sh.s_empty[grp]);
+      if (real) a.score_out[out0 + key] = base + w;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWinMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -307,16 +527,32 @@ template <int D>
 cudaError_t launch_t(const AttnScoresArgs& a, const CUtensorMap& q_map, const CUtensorMap& k_map,
                      int num_sms, cudaStream_t stream) {
   using C = Cfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(attn_scores_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  const int64_t blocks =
-      static_cast<int64_t>((a.max_k + kBM - 1) / kBM) * a.num_seqs * a.hkv;
-  // Few key tiles: the query tiles of each are split over a cluster, at least four apiece.
+  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
   const int most = a.window > 0 && a.window < a.max_q ? a.window : a.max_q;
+  cudaError_t e;
+  if (static_cast<int64_t>(most) * a.group <= kBN) {
+    // runs of key tiles: long ones fill the ring's pipeline, short ones the GPU
+    const int key_tiles = (a.max_k + kBM - 1) / kBM;
+    int run = 8;
+    while (run > 1 && pairs * ((key_tiles + run - 1) / run) < 8 * num_sms) run /= 2;
+    e = cudaFuncSetAttribute(attn_scores_window_kernel<D>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kWinSmem);
+    if (e != cudaSuccess) return e;
+    const unsigned blocks = static_cast<unsigned>(pairs * ((key_tiles + run - 1) / run));
+    attn_scores_window_kernel<D><<<blocks, kWinThreads, C::kWinSmem, stream>>>(a, q_map, k_map,
+                                                                               run);
+    return cudaGetLastError();
+  }
+  e = cudaFuncSetAttribute(attn_scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (a.max_k + kKeyTiles * kBM - 1) / (kKeyTiles * kBM) * pairs;
+  // Few blocks for the GPU: the query tiles of each are split over a cluster, until there
+  // are several blocks per SM, at least eight tiles apiece.
   const int64_t tiles = (static_cast<int64_t>(most) * a.group + kBN - 1) / kBN;
   int cluster = 1;
-  while (cluster < 8 && blocks * cluster < 2 * num_sms && tiles >= 8 * cluster) cluster *= 2;
+  while (cluster < kMaxCluster && blocks * cluster < 4 * num_sms && tiles >= 16 * cluster)
+    cluster *= 2;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
