@@ -350,8 +350,8 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   int cap = (a.max_len + cluster - 1) / cluster;
   if (cap > kKeyCap) cap = kKeyCap;
   const size_t smem = static_cast<size_t>(cap < 4 ? 4 : cap) * 4;
-  e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kKeyCap * 4);
+  static std::atomic<uint64_t> ready{0};
+  e = allow_smem(reinterpret_cast<const void*>(evict_select_kernel), kKeyCap * 4, ready);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

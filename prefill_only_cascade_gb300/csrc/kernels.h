@@ -1,5 +1,6 @@
 // kernels.h - internal launch interface between the C ABI (api.cu) and the kernels.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -148,6 +149,16 @@ struct CascadeMaps {
 void set_cta_pairs(int mode);
 
 // ---- paged cache (paged.cu, scores.cu, evict.cu)
+// Allows kernel `fn` `bytes` of dynamic shared memory on the current device, once per device
+// (`ready`: the devices done so far, kept by the caller).
+inline cudaError_t allow_smem(const void* fn, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (ready.load(std::memory_order_relaxed) >> dev & 1u)) return e;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 // What the entry points outside api.cu need of the current device.
 struct DeviceInfo {
   int num_sms;
@@ -180,11 +191,10 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, bool fp8, int num_sms,
                                 cudaStream_t stream);
 
 // What a CTA of the decode attention leaves for the join: the (sequence, head) that begins
-// in it and goes on in the next CTAs (seq < 0: none), and the tile after its last.
+// in it and goes on in the next CTAs (seq < 0: none) up to CTA `last`; sparse: the number of
+// tiles where there are fewer than CTAs (some then have none), else 0.
 struct DecodeRec {
-  int64_t total;
-  int seq, head;
-  int64_t end;
+  int seq, head, last, sparse;
 };
 struct PagedDecodeArgs {
   int num_seqs, hq, hkv, group;

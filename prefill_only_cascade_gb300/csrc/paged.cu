@@ -4,6 +4,7 @@
 // be kept, grown and cut token by token. A page is [page_size, Hkv, d], the token-row
 // layout of every K/V tensor of the library, so a contiguous [T, Hkv, d] tensor is itself
 // a pool whose pages follow one another.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
   }
 
   const RunStart run = find_run(a, C::kTile, cta, ctas);
-  if (threadIdx.x == 0) a.rec[cta] = DecodeRec{run.total, -1, -1, 0};
+  if (threadIdx.x == 0) a.rec[cta] = DecodeRec{-1, 0, 0, 0};
   if (run.begin >= run.end) return;
   Piece cur;
   cur.b = run.seq;
@@ -732,9 +733,12 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
       }
       if (n == 0 && threadIdx.x == 0) {
         if (any_bad) atomicOr(a.err_word, kErrDeviceBounds);
-        if (!cur.whole && cur.at == cur.piece0)  // goes on in the next CTAs: the join's entry
-          a.rec[cta] = DecodeRec{run.total, cur.b, cur.g,
-                                 cur.piece0 + (cur.len + C::kTile - 1) / C::kTile};
+        if (!cur.whole && cur.at == cur.piece0) {  // goes on in the next CTAs: the join's entry
+          const int64_t end = cur.piece0 + (cur.len + C::kTile - 1) / C::kTile;
+          // the last CTA of (b, g) is the one that holds tile end - 1
+          a.rec[cta] = DecodeRec{cur.b, cur.g, static_cast<int>((end * ctas - 1) / run.total),
+                                 run.total < ctas ? static_cast<int>(run.total) : 0};
+        }
       }
       __syncthreads();  // the shared parts may be overwritten
     }
@@ -745,89 +749,136 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
 
 // Joins the partials of every (sequence, head) that more than one CTA worked on. Its CTAs
 // are c0 (where it begins, with its record) .. c1; their blocks here share its query heads:
-// block c0 + k takes heads k, k + (c1 - c0 + 1), ... One warp of lanes holds the head's
-// values (4 each) and the block's warps take the partials in turn.
+// block c0 + k takes heads k, k + (c1 - c0 + 1), ... A block so has at most two such jobs
+// (the piece that begins in its CTA, and the one that began before); each of their heads is
+// a task for one warp, or for several where there are fewer tasks than warps. What counts is
+// latency: records of the candidates in one load, eight partials per warp in flight.
+constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kDecThreads) paged_join_kernel(const PagedDecodeArgs a, int ctas,
-                                                                 float l_shift) {
-  constexpr int kLanes = D / 4;                    // lanes that hold one head's output
-  constexpr int kRows = kDecThreads / kLanes;      // partials read at once
-  __shared__ alignas(16) float s_acc[kRows][D];
-  __shared__ float s_top[kRows], s_sum[kRows];
-  __shared__ int s_c0;
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PagedDecodeArgs a,
+                                                                     int ctas, float l_shift) {
+  constexpr int V = D / 32;  // values of a lane
+  __shared__ alignas(16) float s_acc[kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int G = a.group;
-  // A block has up to two parts: the piece that begins in its CTA, and the one that began
-  // before and goes through or ends in it.
-  for (int pass = 0; pass < 2; ++pass) {
-    int c0 = blockIdx.x;
-    if (pass == 1) {  // the nearest of the G - 1 CTAs before this one that begins such a piece
-      __syncthreads();
-      if (threadIdx.x == 0) s_c0 = -1;
-      __syncthreads();
-      const int c = static_cast<int>(blockIdx.x) - 1 - static_cast<int>(threadIdx.x);
-      if (threadIdx.x < G - 1 && c >= 0 && a.rec[c].seq >= 0) atomicMax(&s_c0, c);
-      __syncthreads();
-      c0 = s_c0;
-      if (c0 < 0) continue;
-    }
-    const DecodeRec rec = a.rec[c0];
-    if (rec.seq < 0) continue;
-    // the last CTA of the piece: the one that holds tile end - 1
-    const int c1 = static_cast<int>((rec.end * ctas - 1) / rec.total);
-    const int k = static_cast<int>(blockIdx.x) - c0;
-    if (c0 + k > c1) continue;
-    for (int h = k; h < G; h += c1 - c0 + 1) {
-      const int rowi = threadIdx.x / kLanes, d = 4 * (threadIdx.x % kLanes);
-      float top = -INFINITY, sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int c = c0 + rowi; c <= c1; c += kRows) {
+  const int G = a.group, block = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  DecodeRec rec{-1, 0, 0, 0};
+  if (lane < G && lane <= block) rec = a.rec[block - lane];
+  const unsigned begun = __ballot_sync(0xFFFFFFFFu, rec.seq >= 0);
+  // job 0: begins here; job 1: the nearest before that reaches this block
+  int from[2], job_seq[2], job_head[2], last[2], step[2], first[2], tasks[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const unsigned mask = j == 0 ? begun & 1u : begun & ~1u;
+    const int back = mask ? __ffs(mask) - 1 : 0;
+    job_seq[j] = __shfl_sync(0xFFFFFFFFu, rec.seq, back);
+    job_head[j] = __shfl_sync(0xFFFFFFFFu, rec.head, back);
+    last[j] = __shfl_sync(0xFFFFFFFFu, rec.last, back);
+    from[j] = block - back;
+    first[j] = back;
+    step[j] = last[j] - from[j] + 1;
+    tasks[j] = mask && block <= last[j] && back < G ? (G - back + step[j] - 1) / step[j] : 0;
+  }
+  const int sparse = __shfl_sync(0xFFFFFFFFu, rec.sparse, begun ? __ffs(begun) - 1 : 0);
+  const int total = tasks[0] + tasks[1];
+  int wpt = 1;  // warps of a task
+  while (wpt < kJoinWarps && 2 * wpt * total <= kJoinWarps) wpt *= 2;
+  const int sub = warp % wpt;
+  for (int t0 = 0; t0 < total; t0 += kJoinWarps / wpt) {
+    const int task = t0 + warp / wpt;
+    const int j = task < tasks[0] ? 0 : 1;
+    const bool active = task < total;
+    const int c0 = j ? from[1] : from[0], c1 = j ? last[1] : last[0];
+    const int h = j ? first[1] + (task - tasks[0]) * step[1] : first[0] + task * step[0];
+    float top = -INFINITY, sum = 0.f, acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (int base = c0 + sub; active && base <= c1; base += 8 * wpt) {
+      float2 ml[8];
+      float x[8][V];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int c = base + u * wpt;
+        ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[u][v] = 0.f;
         // with fewer tiles than CTAs some have none
-        if (first_tile(c, rec.total, ctas) == first_tile(c + 1, rec.total, ctas)) continue;
-        const int64_t part = 2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0);
-        const float2 ml = a.part_ml[part * G + h];
-        const float4 x = *reinterpret_cast<const float4*>(a.part_o + (part * G + h) * D + d);
-        const float to = fmaxf(top, ml.x);
+        if (c <= c1 && (sparse == 0 || first_tile(c, sparse, ctas) != first_tile(c + 1, sparse, ctas))) {
+          const int64_t part = (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * G + h;
+          ml[u] = a.part_ml[part];
+          const float* p = a.part_o + part * D + V * lane;
+          if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p);
+            x[u][0] = y.x;
+            x[u][1] = y.y;
+            x[u][2] = y.z;
+            x[u][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(p);
+            x[u][0] = y.x;
+            x[u][1] = y.y;
+          }
+        }
+      }
+      float to = top;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) to = fmaxf(to, ml[u].x);
+      const float f = top == -INFINITY ? 0.f : ex2(top - to);
+      sum *= f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {  // a bad page's sum is NaN and stays it
+        const float e = ml[u].x == -INFINITY ? 0.f : ex2(ml[u].x - to);
+        sum = fmaf(ml[u].y, e, sum);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(x[u][v], e, acc[v]);
+      }
+      top = to;
+    }
+    if (wpt > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) s_acc[warp][V * lane + v] = acc[v];
+      if (lane == 0) s_ml[warp] = make_float2(top, sum);
+      __syncthreads();
+      if (sub == 0) {
+        float to = top;
+        for (int w = 1; w < wpt; ++w) to = fmaxf(to, s_ml[warp + w].x);
         const float f = top == -INFINITY ? 0.f : ex2(top - to);
-        const float e = ml.x == -INFINITY ? 0.f : ex2(ml.x - to);
+        sum *= f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= f;
+        for (int w = 1; w < wpt; ++w) {
+          const float2 ml = s_ml[warp + w];
+          const float e = ml.x == -INFINITY ? 0.f : ex2(ml.x - to);
+          sum = fmaf(ml.y, e, sum);
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] = fmaf(s_acc[warp + w][V * lane + v], e, acc[v]);
+        }
         top = to;
-        sum = fmaf(sum, f, ml.y * e);
-        if (ml.y != ml.y) sum = ml.y;  // a bad page: NaN, whatever its max was
-        acc.x = fmaf(acc.x, f, x.x * e);
-        acc.y = fmaf(acc.y, f, x.y * e);
-        acc.z = fmaf(acc.z, f, x.z * e);
-        acc.w = fmaf(acc.w, f, x.w * e);
       }
-      __syncthreads();
-      *reinterpret_cast<float4*>(&s_acc[rowi][d]) = acc;
-      if (d == 0) {
-        s_top[rowi] = top;
-        s_sum[rowi] = sum;
-      }
-      __syncthreads();
-      if (threadIdx.x < D) {
-        float t = s_top[0];
+    }
+    if (active && sub == 0) {
+      const int seq = j ? job_seq[1] : job_seq[0], head = j ? job_head[1] : job_head[0];
+      const int64_t row = static_cast<int64_t>(seq) * a.hq + head * G + h;
+      const float vs = a.v_scale != nullptr
+                           ? __ldg(a.v_scale + static_cast<int64_t>(seq) * a.hkv + head) : 1.f;
+      uint32_t packed[V / 2];
 #pragma unroll
-        for (int i = 1; i < kRows; ++i) t = fmaxf(t, s_top[i]);
-        float total = 0.f, val = 0.f;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const float f = s_top[i] == -INFINITY ? 0.f : ex2(s_top[i] - t);
-          total = s_sum[i] != s_sum[i] ? s_sum[i] : fmaf(s_sum[i], f, total);
-          val = fmaf(s_acc[i][threadIdx.x], f, val);
-        }
-        const int64_t row = static_cast<int64_t>(rec.seq) * a.hq + rec.head * G + h;
-        const float vs =
-            a.v_scale != nullptr ? __ldg(a.v_scale + static_cast<int64_t>(rec.seq) * a.hkv + rec.head)
-                                 : 1.f;
-        a.out[row * D + threadIdx.x] = __float2bfloat16(val / total * vs);
-        if (threadIdx.x == 0) {
-          const float lse2 = t + (log2f(total) - l_shift);
-          if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
-          if (a.lse2 != nullptr) a.lse2[row] = lse2;
-        }
+      for (int v = 0; v < V; v += 2)
+        packed[v / 2] = pack2<false>(acc[v] / sum * vs, acc[v + 1] / sum * vs);
+      uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * D + V * lane);
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(packed[0], packed[1]);
+      else
+        out[0] = packed[0];
+      if (lane == 0) {
+        const float lse2 = top + (log2f(sum) - l_shift);
+        if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
+        if (a.lse2 != nullptr) a.lse2[row] = lse2;
       }
     }
   }
@@ -835,20 +886,40 @@ __global__ void __launch_bounds__(kDecThreads) paged_join_kernel(const PagedDeco
 
 // score_out[b, g, j] = score_in + sum over the group's heads of exp2(x - lse2), from the
 // scores that the attention left in the workspace (4 bytes per (head, token) against 4 d
-// or 2 d bytes of K and V per G of them).
-__global__ void __launch_bounds__(256) paged_weights_kernel(const PagedDecodeArgs a) {
+// or 2 d bytes of K and V per G of them, and mostly still in L2).
+constexpr int kWeightThreads = 256, kWeightPer = 4;
+__global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(const PagedDecodeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x / a.hkv, g = blockIdx.x % a.hkv;
   const int n = checked_len(a, b);
   const int64_t row = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(g) * a.group;
   const int64_t out_row = (static_cast<int64_t>(b) * a.hkv + g) * a.score_stride;
-  for (int j = blockIdx.y * 256 + threadIdx.x; j < n; j += gridDim.y * 256) {
-    float w = 0.f;
+  const int64_t chunk = static_cast<int64_t>(gridDim.y) * (kWeightThreads * kWeightPer);
+  for (int64_t j0 = static_cast<int64_t>(blockIdx.y) * (kWeightThreads * kWeightPer) + threadIdx.x;
+       j0 < n; j0 += chunk) {
+    float w[kWeightPer];
+#pragma unroll
+    for (int k = 0; k < kWeightPer; ++k) {
+      const int64_t j = j0 + k * kWeightThreads;
+      w[k] = 0.f;
+      if (a.score_in != nullptr && j < n) w[k] = a.score_in[out_row + j];
+    }
+    float add[kWeightPer] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int h = 0; h < a.group; ++h) {
       const float lse2 = a.lse2[row + h];
-      if (lse2 == lse2) w += ex2(a.raw[(row + h) * a.raw_stride + j] - lse2);
+      const float* raw = a.raw + (row + h) * a.raw_stride;
+#pragma unroll
+      for (int k = 0; k < kWeightPer; ++k) {
+        const int64_t j = j0 + k * kWeightThreads;
+        if (j < n && lse2 == lse2) add[k] += ex2(raw[j] - lse2);
+      }
     }
-    a.score_out[out_row + j] = (a.score_in != nullptr ? a.score_in[out_row + j] : 0.f) + w;
+#pragma unroll
+    for (int k = 0; k < kWeightPer; ++k) {
+      const int64_t j = j0 + k * kWeightThreads;
+      if (j < n) a.score_out[out_row + j] = w[k] + add[k];
+    }
   }
 }
 
@@ -856,8 +927,9 @@ template <int D, bool FP8, int NT>
 cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
   using C = DecCfg<D, FP8>;
   const int ctas = decode_ctas(num_sms, a.num_seqs, a.hkv, a.max_len, C::kTile);
-  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D, FP8, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT>),
+                             C::kSmem, ready);
   if (e != cudaSuccess) return e;
   paged_decode_kernel<D, FP8, NT><<<ctas, kDecThreads, C::kSmem, stream>>>(a);
   e = cudaGetLastError();
@@ -872,13 +944,14 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
   // weights follow (which rely on it having waited for the attention)
   if (e == cudaSuccess && (a.max_len > C::kTile || a.raw != nullptr)) {
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kDecThreads);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, ctas, FP8 ? 14.f : 0.f);
   }
   if (e == cudaSuccess && a.raw != nullptr && a.max_len > 0) {
-    const int chunks = (a.max_len + 255) / 256;
+    constexpr int kPer = kWeightThreads * kWeightPer;
+    const int chunks = (a.max_len + kPer - 1) / kPer;
     cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * a.hkv, chunks < 4096 ? chunks : 4096);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kWeightThreads);
     e = cudaLaunchKernelEx(&cfg, paged_weights_kernel, a);
   }
   return e;

@@ -535,16 +535,16 @@ cudaError_t launch_t(const AttnScoresArgs& a, const CUtensorMap& q_map, const CU
     const int key_tiles = (a.max_k + kBM - 1) / kBM;
     int run = 8;
     while (run > 1 && pairs * ((key_tiles + run - 1) / run) < 8 * num_sms) run /= 2;
-    e = cudaFuncSetAttribute(attn_scores_window_kernel<D>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kWinSmem);
+    static std::atomic<uint64_t> ready{0};
+    e = allow_smem(reinterpret_cast<const void*>(attn_scores_window_kernel<D>), C::kWinSmem, ready);
     if (e != cudaSuccess) return e;
     const unsigned blocks = static_cast<unsigned>(pairs * ((key_tiles + run - 1) / run));
     attn_scores_window_kernel<D><<<blocks, kWinThreads, C::kWinSmem, stream>>>(a, q_map, k_map,
                                                                                run);
     return cudaGetLastError();
   }
-  e = cudaFuncSetAttribute(attn_scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           C::kSmem);
+  static std::atomic<uint64_t> ready{0};
+  e = allow_smem(reinterpret_cast<const void*>(attn_scores_kernel<D>), C::kSmem, ready);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (a.max_k + kKeyTiles * kBM - 1) / (kKeyTiles * kBM) * pairs;
   // Few blocks for the GPU: the query tiles of each are split over a cluster, until there
