@@ -5,9 +5,11 @@
 //
 // 1. evict_select_kernel  a thread-block cluster per (sequence, KV head) finds the k-th
 //    largest score by a radix select over 32-bit keys (digits of 11, 11 and 10 bits,
-//    histograms of the cluster's CTAs added through distributed shared memory) and writes
-//    the kept positions in order. The keys stay in shared memory between the passes: the
-//    scores are read once. It also marks the pages that are read and written.
+//    histograms of the cluster's CTAs added through distributed shared memory; it stops
+//    early where a digit settles it, which distinct scores mostly do after two) and writes
+//    the kept positions in order. The keys stay in registers between the passes: the scores
+//    are read once, up to 16,384 per CTA. It also marks the pages that are read and written.
+//    Bound by latency: about ten barriers and dependent steps of a microsecond or less.
 // 2. evict_copy_kernel    moves the kept rows: a block looks up the places of 256 (token,
 //    head) rows first, then moves them, 16 bytes a thread and eight in flight.
 #include <cstdint>
@@ -23,9 +25,9 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBinsPerThread = kBins / kSelThreads;  // 4
-constexpr int kKeyCap = 20480;                       // keys a CTA holds (80 KB): two CTAs an SM
-constexpr int kLoads = 8;                            // scores in flight per thread
+constexpr int kSub = 4;                              // copies of the first histogram
 constexpr int kMaxCluster = 8;
+constexpr int kMaxKeys = 32;                         // keys a thread holds at most
 
 constexpr int kMarkRead = 1, kMarkWritten = 2;       // a page's uses: bit 0, and 2 per write
 
@@ -55,16 +57,23 @@ __device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
   return v;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const PagedEvictArgs a,
-                                                                   int cluster, int key_cap) {
-  extern __shared__ uint32_t s_keys[];  // [key_cap]
-  __shared__ __align__(16) uint32_t s_hist[3][kBins];  // one per pass
+// KPT: keys a thread holds. A CTA's part of the competing tokens is walked in rounds of
+// kSelThreads * KPT (one, unless the part is longer: then the scores are read again in every
+// pass); in a round each warp has a contiguous run, lane by lane, so that the order of the
+// tokens is (round, warp, i, lane).
+template <int KPT>
+__global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1)
+    evict_select_kernel(const PagedEvictArgs a, int cluster) {
+  // Scores of one octave share few first digits, so lanes often add to the same bin: four
+  // copies, by lane, keep those additions from queueing.
+  __shared__ __align__(16) uint32_t s_first[kSub][kBins];
+  __shared__ __align__(16) uint32_t s_second[kBins], s_third[kBins / 2];
   __shared__ uint32_t s_warp[kSelWarps];
-  __shared__ uint32_t s_found[2];       // digit, and how many are above it
+  __shared__ uint32_t s_found[3];       // digit, how many are above it, how many have it
   __shared__ __align__(16) uint32_t s_count[4];  // this CTA's keys above / at the threshold
   __shared__ uint32_t s_gt[kSelWarps], s_eq[kSelWarps];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int pair = blockIdx.x / cluster;
   const int b = pair / a.hkv, g = pair % a.hkv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -73,12 +82,36 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Page
   const int recent = min(a.recent, fresh);
   const int elig = (n < 0 ? 0 : n) - recent;          // tokens that compete
   const int k = fresh - recent;                       // for so many places
-  const int64_t out_row = static_cast<int64_t>(pair);
-  int32_t* kept = a.kept + out_row * a.budget;
-  const float* score = a.score + out_row * a.score_stride;
-  float* score_out = a.score_out != nullptr ? a.score_out + out_row * a.score_out_stride : nullptr;
-  const int tid = rank * kSelThreads + threadIdx.x, threads = cluster * kSelThreads;
+  const float* score = a.score + static_cast<int64_t>(pair) * a.score_stride;
 
+  // this CTA's part of the competing tokens
+  const int per = (elig + cluster - 1) / cluster;
+  const int e0 = min(rank * per, elig), count = min(per, elig - e0);
+  constexpr int kRound = kSelThreads * KPT;
+  const int rounds = (per + kRound - 1) / kRound;
+  uint32_t key[KPT];                    // 0: none (every score's key is larger)
+  int w0 = 0;                           // the warp's first token of the round
+  auto load = [&](int round) {
+    const int left = max(0, min(kRound, count - round * kRound));
+    const int run = (left + 32 * kSelWarps - 1) / (32 * kSelWarps) * 32;
+    const int end = round * kRound + left;
+    w0 = round * kRound + warp * run;
+    const int w1 = min(w0 + run, end);
+    float x[KPT];
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      const int at = w0 + 32 * i + lane;
+      x[i] = at < w1 ? __ldg(score + e0 + at) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) key[i] = w0 + 32 * i + lane < w1 ? score_key(x[i]) : 0u;
+  };
+  if (k > 0) load(0);
+
+  int32_t* kept = a.kept + static_cast<int64_t>(pair) * a.budget;
+  float* score_out =
+      a.score_out != nullptr ? a.score_out + static_cast<int64_t>(pair) * a.score_out_stride : nullptr;
+  const int tid = rank * kSelThreads + threadIdx.x, threads = cluster * kSelThreads;
   if (g == 0) {  // the sequence's pages and its new length, once
     if (tid == 0) {
       a.new_lens[b] = n < 0 ? -1 : fresh;
@@ -104,72 +137,69 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Page
   if (score_out != nullptr)
     for (int64_t i = fresh + tid; i < a.score_out_stride; i += threads) score_out[i] = 0.f;
   if (k == 0) return;  // the same for every CTA of the cluster
-  for (int i = threadIdx.x; i < 3 * kBins / 4; i += kSelThreads)
-    reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-  __syncthreads();
 
-  // this CTA's part of the competing tokens
-  const int per = (elig + cluster - 1) / cluster;
-  const int e0 = min(rank * per, elig), e1 = min(e0 + per, elig);
-  const int count = e1 - e0;
-  auto key_at = [&](int i) { return i < key_cap ? s_keys[i] : score_key(__ldg(score + e0 + i)); };
-
-  uint32_t threshold = 0, need = 0;   // keys above it stay, and `need` of those at it
+  // keys above the threshold stay, and `need` of those at it; k >= elig: every key
+  uint32_t threshold = 0, need = 0;
   if (k < elig) {
+    for (int i = threadIdx.x; i < kSub * kBins / 4; i += kSelThreads)
+      reinterpret_cast<uint4*>(s_first)[i] = make_uint4(0u, 0u, 0u, 0u);
+    reinterpret_cast<uint4*>(s_second)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x < kBins / 8) reinterpret_cast<uint4*>(s_third)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
     need = static_cast<uint32_t>(k);
     uint32_t prefix = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t mask = pass == 2 ? 1023u : 2047u;
-      uint32_t* hist = s_hist[pass];
-      if (pass == 0) {
-        for (int i0 = threadIdx.x; i0 < count; i0 += kSelThreads * kLoads) {
-          float x[kLoads];
+      uint32_t* hist = pass == 0 ? s_first[0] : pass == 1 ? s_second : s_third;
+      for (int round = 0; round < rounds; ++round) {
+        if (rounds > 1 && (pass > 0 || round > 0)) load(round);
+        if (pass == 0) {
+          uint32_t* mine = s_first[lane & (kSub - 1)];
 #pragma unroll
-          for (int j = 0; j < kLoads; ++j) {
-            const int i = i0 + j * kSelThreads;
-            x[j] = i < count ? __ldg(score + e0 + i) : 0.f;
-          }
+          for (int i = 0; i < KPT; ++i)
+            if (key[i] != 0) atomicAdd(mine + (key[i] >> 21), 1u);
+        } else {
+          const int above = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0;
+          const uint32_t mask = pass == 1 ? 2047u : 1023u;
 #pragma unroll
-          for (int j = 0; j < kLoads; ++j) {
-            const int i = i0 + j * kSelThreads;
-            const uint32_t key = score_key(x[j]);
-            if (i < count && i < key_cap) s_keys[i] = key;
-            if (i < count) atomicAdd(&hist[key >> 21], 1u);
-          }
-        }
-      } else {
-        const int above = pass == 1 ? 21 : 10;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < count; i += kSelThreads) {
-          const uint32_t key = key_at(i);
-          if (key >> above == prefix) atomicAdd(&hist[(key >> shift) & mask], 1u);
+          for (int i = 0; i < KPT; ++i)
+            if (key[i] >> above == prefix) atomicAdd(hist + ((key[i] >> shift) & mask), 1u);
         }
       }
-      if (cluster > 1) cluster_sync(); else __syncthreads();
-      uint32_t bin[kBinsPerThread] = {0, 0, 0, 0};
-      if (cluster == 1) {
-        const uint4 v = *reinterpret_cast<const uint4*>(&hist[kBinsPerThread * threadIdx.x]);
-        bin[0] = v.x;
-        bin[1] = v.y;
-        bin[2] = v.z;
-        bin[3] = v.w;
-      } else {
-        uint4 v[kMaxCluster];
+      __syncthreads();
+      const bool has = pass < 2 || threadIdx.x < kSelThreads / 2;  // the last has half the bins
+      uint4 sum = make_uint4(0u, 0u, 0u, 0u);
+      if (has) sum = *reinterpret_cast<const uint4*>(hist + kBinsPerThread * threadIdx.x);
+      if (pass == 0) {
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          if (c < cluster) v[c] = ld_cluster_u4(cluster_map(&hist[kBinsPerThread * threadIdx.x], c));
+        for (int c = 1; c < kSub; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(&s_first[c][kBinsPerThread * threadIdx.x]);
+          sum.x += v.x;
+          sum.y += v.y;
+          sum.z += v.z;
+          sum.w += v.w;
+        }
+      }
+      if (cluster > 1) {
+        if (pass == 0) *reinterpret_cast<uint4*>(hist + kBinsPerThread * threadIdx.x) = sum;
+        cluster_sync();
+        uint4 v[kMaxCluster - 1];
 #pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          if (c < cluster) {
-            bin[0] += v[c].x;
-            bin[1] += v[c].y;
-            bin[2] += v[c].z;
-            bin[3] += v[c].w;
+        for (int c = 1; c < kMaxCluster; ++c)
+          if (c < cluster && has)
+            v[c - 1] = ld_cluster_u4(
+                cluster_map(hist + kBinsPerThread * threadIdx.x, (rank + c) & (cluster - 1)));
+#pragma unroll
+        for (int c = 1; c < kMaxCluster; ++c)
+          if (c < cluster && has) {
+            sum.x += v[c - 1].x;
+            sum.y += v[c - 1].y;
+            sum.z += v[c - 1].z;
+            sum.w += v[c - 1].w;
           }
       }
       // how many keys lie in the bins of the threads after this one
+      const uint32_t bin[kBinsPerThread] = {sum.x, sum.y, sum.z, sum.w};
       const uint32_t mine = bin[0] + bin[1] + bin[2] + bin[3];
       uint32_t x = mine;
 #pragma unroll
@@ -180,85 +210,110 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Page
       if (lane == 0) s_warp[warp] = x;
       __syncthreads();
       uint32_t above = x - mine;
-      for (int w = warp + 1; w < kSelWarps; ++w) above += s_warp[w];
+      const uint32_t others = lane > warp && lane < kSelWarps ? s_warp[lane] : 0u;
+      above += __reduce_add_sync(0xFFFFFFFFu, others);
 #pragma unroll
       for (int j = kBinsPerThread - 1; j >= 0; --j) {
         if (above < need && need <= above + bin[j]) {
           s_found[0] = kBinsPerThread * threadIdx.x + j;
           s_found[1] = above;
+          s_found[2] = bin[j];
         }
         above += bin[j];
       }
       __syncthreads();
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       prefix = pass == 2 ? prefix << 10 | s_found[0] : prefix << 11 | s_found[0];
       need -= s_found[1];
+      if (s_found[2] == need) {  // every key of the digit stays
+        threshold = (prefix << shift) - 1;
+        need = 0;
+        break;
+      }
+      threshold = prefix;
     }
-    threshold = prefix;
   }
 
-  // positions of the kept keys: contiguous runs of the warps, in order
-  const int run = (count + 32 * kSelWarps - 1) / (32 * kSelWarps) * 32;
-  const int w0 = min(warp * run, count), w1 = min(w0 + run, count);
-  const bool all = k >= elig;
+  // positions of the kept keys
   uint32_t gt = 0, eq = 0;
-  if (!all) {
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const uint32_t key = key_at(i);
-      gt += key > threshold;
-      eq += key == threshold;
+  for (int round = 0; round < rounds; ++round) {
+    if (rounds > 1) load(round);
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      gt += key[i] > threshold;
+      eq += key[i] != 0 && key[i] == threshold;
     }
-    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
-    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-  } else {
-    gt = static_cast<uint32_t>(max(0, w1 - w0));
   }
+  gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
   if (lane == 0) {
     s_gt[warp] = gt;
     s_eq[warp] = eq;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t tg = 0, te = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      tg += s_gt[w];
-      te += s_eq[w];
+  const uint32_t lane_gt = lane < kSelWarps ? s_gt[lane] : 0u;
+  const uint32_t lane_eq = lane < kSelWarps ? s_eq[lane] : 0u;
+  uint32_t base_gt = 0, base_eq = 0;    // kept / at the threshold before this CTA's
+  if (cluster > 1) {
+    const uint32_t all_gt = __reduce_add_sync(0xFFFFFFFFu, lane_gt);
+    const uint32_t all_eq = __reduce_add_sync(0xFFFFFFFFu, lane_eq);
+    if (threadIdx.x == 0) {
+      s_count[0] = all_gt;
+      s_count[1] = all_eq;
     }
-    s_count[0] = tg;
-    s_count[1] = te;
+    cluster_sync();
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (lane < rank) v = ld_cluster_u4(cluster_map(s_count, lane));
+    base_gt = __reduce_add_sync(0xFFFFFFFFu, v.x);
+    base_eq = __reduce_add_sync(0xFFFFFFFFu, v.y);
   }
-  if (cluster > 1) cluster_sync(); else __syncthreads();
-  uint32_t base_gt = 0, base_eq = 0;
-  for (int c = 0; c < rank; ++c) {
-    const uint4 v = ld_cluster_u4(cluster_map(s_count, c));
-    base_gt += v.x;
-    base_eq += v.y;
-  }
-  for (int w = 0; w < warp; ++w) {
-    base_gt += s_gt[w];
-    base_eq += s_eq[w];
-  }
-  const uint32_t before = (1u << lane) - 1u;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const bool in = i < w1;
-    const uint32_t key = in && !all ? key_at(i) : 0u;
-    const bool is_gt = in && (all || key > threshold), is_eq = in && !all && key == threshold;
-    const uint32_t bg = __ballot_sync(0xFFFFFFFFu, is_gt);
-    const uint32_t be = __ballot_sync(0xFFFFFFFFu, is_eq);
-    const uint32_t eq_rank = base_eq + __popc(be & before);
-    if (is_gt || (is_eq && eq_rank < need)) {
-      const uint32_t at = base_gt + __popc(bg & before) + min(eq_rank, need);
-      if (at < static_cast<uint32_t>(k)) {  // else the scores changed meanwhile
-        kept[at] = e0 + i;
-        if (score_out != nullptr) {
-          // the key gives the score back, but for the values that share one
-          score_out[at] = all || key == kKeyZero || key == kKeyLowest ? __ldg(score + e0 + i)
-                                                                     : key_score(key);
-        }
+  const uint32_t lower = (1u << lane) - 1u;
+  for (int round = 0; round < rounds; ++round) {
+    uint32_t warp_gt, warp_eq;          // before this warp's
+    if (rounds > 1) {  // the round's own counts
+      load(round);
+      gt = eq = 0;
+#pragma unroll
+      for (int i = 0; i < KPT; ++i) {
+        gt += key[i] > threshold;
+        eq += key[i] != 0 && key[i] == threshold;
       }
+      gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+      eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+      __syncthreads();  // the last round's were read
+      if (lane == 0) {
+        s_gt[warp] = gt;
+        s_eq[warp] = eq;
+      }
+      __syncthreads();
+      const uint32_t x = lane < kSelWarps ? s_gt[lane] : 0u, y = lane < kSelWarps ? s_eq[lane] : 0u;
+      warp_gt = base_gt + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0u);
+      warp_eq = base_eq + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? y : 0u);
+      base_gt += __reduce_add_sync(0xFFFFFFFFu, x);
+      base_eq += __reduce_add_sync(0xFFFFFFFFu, y);
+    } else {
+      warp_gt = base_gt + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? lane_gt : 0u);
+      warp_eq = base_eq + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? lane_eq : 0u);
     }
-    base_gt += __popc(bg);
-    base_eq += __popc(be);
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      const bool is_gt = key[i] > threshold, is_eq = key[i] != 0 && key[i] == threshold;
+      const uint32_t bg = __ballot_sync(0xFFFFFFFFu, is_gt);
+      const uint32_t be = __ballot_sync(0xFFFFFFFFu, is_eq);
+      const uint32_t eq_rank = warp_eq + __popc(be & lower);
+      const uint32_t at = warp_gt + __popc(bg & lower) + min(eq_rank, need);
+      // (places run out only if the scores change meanwhile)
+      if ((is_gt || (is_eq && eq_rank < need)) && at < static_cast<uint32_t>(k)) {
+        const int pos = e0 + w0 + 32 * i + lane;
+        kept[at] = pos;
+        // the key gives the score back, but for the values that share one
+        if (score_out != nullptr)
+          score_out[at] =
+              key[i] == kKeyZero || key[i] == kKeyLowest ? __ldg(score + pos) : key_score(key[i]);
+      }
+      warp_gt += __popc(bg);
+      warp_eq += __popc(be);
+    }
   }
   if (cluster > 1) cluster_sync();  // no CTA leaves while others read its counts
 }
@@ -344,16 +399,11 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
   int cluster = 1;
   while (cluster < kMaxCluster &&
-         (a.max_len > kKeyCap * cluster ||
+         (a.max_len > static_cast<int64_t>(kSelThreads) * kMaxKeys * cluster ||
           (pairs * cluster * 2 <= num_sms && a.max_len > 2048 * cluster)))
     cluster *= 2;
-  int cap = (a.max_len + cluster - 1) / cluster;
-  if (cap > kKeyCap) cap = kKeyCap;
-  const size_t smem = static_cast<size_t>(cap < 4 ? 4 : cap) * 4;
-  static std::atomic<uint64_t> ready{0};
-  e = allow_smem(reinterpret_cast<const void*>(evict_select_kernel), kKeyCap * 4, ready);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
+  const int per = (a.max_len + cluster - 1) / cluster;
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = 1;
@@ -364,8 +414,9 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cluster, cap);
+  e = per <= 4 * kSelThreads    ? cudaLaunchKernelEx(&cfg, evict_select_kernel<4>, a, cluster)
+      : per <= 16 * kSelThreads ? cudaLaunchKernelEx(&cfg, evict_select_kernel<16>, a, cluster)
+                                : cudaLaunchKernelEx(&cfg, evict_select_kernel<kMaxKeys>, a, cluster);
   if (e != cudaSuccess) return e;
   const int chunks = static_cast<int>(
       (static_cast<int64_t>(a.budget) * a.hkv + kCopyThreads - 1) / kCopyThreads);
@@ -373,7 +424,6 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * chunks));
   cfg.blockDim = dim3(kCopyThreads);
-  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, evict_copy_kernel, a, chunks);
 }
 

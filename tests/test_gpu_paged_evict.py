@@ -120,6 +120,7 @@ def test_cases(name, kind, fp8):
 @pytest.mark.parametrize("lens,budget,recent,hkv", [
     ([70000], 3000, 64, 1),        # a cluster's CTAs share the keys
     ([170001, 20000], 9000, 100, 1),  # and do not hold all of them
+    ([400003, 3, 262144], 30000, 1000, 1),
     ([5000] * 40, 1000, 16, 4),    # one CTA each
     ([20481, 20480, 4097], 20480, 0, 2),
 ])
