@@ -386,7 +386,7 @@ quail_status quail_quantize_kv_fp8_with_scales(int32_t num_anchors,
  * sequence, and quail_get_device_error() reports QUAIL_ERR_DEVICE_BOUNDS.
  * Limits: page_size a power of two from 16 to 256; max_seq_len at most 2^30 and at most
  * max_pages_per_seq * page_size; d in {64, 128}; Hq/Hkv in {1, 2, 4, 8, 16};
- * num_seqs * Hq < 2^28.
+ * num_seqs * Hq < 2^28; num_seqs * max_pages_per_seq < 2^31.
  */
 typedef struct {
   int32_t num_seqs;              /* B >= 0 */
@@ -442,7 +442,7 @@ quail_status quail_paged_kv_append(const quail_paged_desc* desc, int64_t num_new
  *   score_in, score_out [B, Hkv, score_stride] fp32, score_stride >= max_seq_len;
  *            score_out NULL: no weights are formed; score_in NULL: zeros; both may be the
  *            same buffer. Entries at seq_lens[b] and beyond are left as they were. A head
- *            whose lse is NaN adds nothing.
+ *            whose lse is NaN or -inf adds nothing.
  *   workspace: at least quail_paged_decode_workspace_size(desc, score_out != NULL) bytes,
  *            16-byte aligned, overwritten; calls that share one must not overlap on the GPU.
  */
@@ -512,8 +512,8 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
  *            overlapping score: the kept tokens' scores, zeros behind them
  *   workspace: at least quail_paged_evict_workspace_size(desc, dst_num_pages) bytes,
  *            16-byte aligned, overwritten; calls that share one must not overlap on the GPU.
- * The scales of e4m3 pages stay those of the sequence. Limit: num_seqs * budget * Hkv <
- * 2^38.
+ * The scales of e4m3 pages stay those of the sequence. Limits: num_seqs * budget * Hkv <
+ * 2^38, num_seqs * dst_max_pages_per_seq < 2^31.
  */
 quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, int32_t recent,
                                   const void* k_pages, const void* v_pages,

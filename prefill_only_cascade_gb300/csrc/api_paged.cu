@@ -43,6 +43,7 @@ quail_status check_desc(const quail_paged_desc* desc) {
   if (d.max_seq_len > (1 << 30)) return QUAIL_ERR_UNSUPPORTED;
   if (d.max_seq_len > static_cast<int64_t>(d.max_pages_per_seq) * d.page_size)
     return QUAIL_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(d.num_seqs) * d.max_pages_per_seq > kInt32Max) return QUAIL_ERR_UNSUPPORTED;
   // work counted in 32 bits: 8 blocks per (sequence, query head)
   if (static_cast<int64_t>(d.num_seqs) * d.num_q_heads > kInt32Max / 8) return QUAIL_ERR_UNSUPPORTED;
   return QUAIL_OK;
@@ -63,7 +64,7 @@ float scale_log2_of(float softmax_scale, int head_dim) {
 }
 
 struct DecodeLayout {
-  size_t rec, part_ml, part_o, lse2, raw, total;
+  size_t rec, part_ml, part_o, lse2, begun, raw, total;
   int64_t raw_stride;
 };
 DecodeLayout decode_layout(const quail_paged_desc& d, bool with_scores) {
@@ -81,7 +82,8 @@ DecodeLayout decode_layout(const quail_paged_desc& d, bool with_scores) {
   l.part_o = up(l.part_ml + parts * group * sizeof(float2));
   l.lse2 = up(l.part_o + parts * group * d.head_dim * 4);
   const size_t rows = static_cast<size_t>(d.num_seqs) * d.num_q_heads;
-  l.raw = up(l.lse2 + (with_scores ? rows * 4 : 0));
+  l.begun = up(l.lse2 + (with_scores ? rows * 4 : 0));
+  l.raw = up(l.begun + (with_scores ? rows / group * 4 : 0));
   l.total = up(l.raw + (with_scores ? rows * l.raw_stride * 4 : 0));
   return l;
 }
@@ -213,6 +215,7 @@ quail_status quail_paged_decode_attn(const quail_paged_desc* desc, const void* q
   a.part_ml = reinterpret_cast<float2*>(w + l.part_ml);
   a.part_o = reinterpret_cast<float*>(w + l.part_o);
   a.lse2 = scored ? reinterpret_cast<float*>(w + l.lse2) : nullptr;
+  a.begun = scored ? reinterpret_cast<int32_t*>(w + l.begun) : nullptr;
   a.raw = scored ? reinterpret_cast<float*>(w + l.raw) : nullptr;
   a.raw_stride = l.raw_stride;
   a.err_word = info.err_word;
@@ -296,7 +299,7 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
 
 size_t quail_paged_evict_workspace_size(const quail_paged_desc* desc, int32_t dst_num_pages) {
   if (check_desc(desc) != QUAIL_OK || dst_num_pages < 0) return 0;
-  return (static_cast<size_t>(dst_num_pages) * 4 + 255) / 256 * 256 + 256;
+  return (static_cast<size_t>(dst_num_pages) * 12 + 255) / 256 * 256 + 256;
 }
 
 quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, int32_t recent,
@@ -318,6 +321,8 @@ quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, 
   if (most > static_cast<int64_t>(dst_max_pages_per_seq) * d.page_size) return QUAIL_ERR_INVALID_ARG;
   if (score_out != nullptr && score_out_stride < budget) return QUAIL_ERR_INVALID_ARG;
   const int64_t pairs = static_cast<int64_t>(d.num_seqs) * d.num_kv_heads;
+  if (static_cast<int64_t>(d.num_seqs) * dst_max_pages_per_seq > kInt32Max)
+    return QUAIL_ERR_UNSUPPORTED;
   // blocks of 256 kept rows
   if (d.num_seqs > 0 &&
       (static_cast<int64_t>(budget) * d.num_kv_heads + 255) / 256 > kInt32Max / d.num_seqs)
@@ -337,7 +342,7 @@ quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, 
         !aligned(score, 4) || !aligned(dst_table, 4) || !aligned(kept, 4) ||
         !aligned(new_lens, 4) || !aligned(score_out, 4))
       return QUAIL_ERR_INVALID_ARG;
-    // one pool for both (the marks tell its pages apart), or two that do not meet
+    // one pool for both (the kernels tell its pages apart), or two that do not meet
     if (same_pool ? (v_dst != v_pages || dst_num_pages != d.num_pages)
                   : (overlap(k_dst, dst_bytes, k_pages, src_bytes) ||
                      overlap(v_dst, dst_bytes, v_pages, src_bytes)))
@@ -385,7 +390,9 @@ quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, 
   a.new_lens = new_lens;
   a.score_out = score_out;
   a.score_out_stride = score_out_stride;
-  a.marks = static_cast<int32_t*>(workspace);
+  a.claim = static_cast<int32_t*>(workspace);
+  a.dup = a.claim + dst_num_pages;
+  a.hold = a.dup + dst_num_pages;
   a.err_word = info.err_word;
   const cudaError_t e =
       quail::launch_paged_evict(a, info.num_sms, reinterpret_cast<cudaStream_t>(stream));

@@ -8,7 +8,7 @@
 //    histograms of the cluster's CTAs added through distributed shared memory; it stops
 //    early where a digit settles it, which distinct scores mostly do after two) and writes
 //    the kept positions in order. The keys stay in registers between the passes: the scores
-//    are read once, up to 16,384 per CTA. It also marks the pages that are read and written.
+//    are read once, up to 16,384 per CTA. It also notes who writes and who holds each page.
 //    Bound by latency: about ten barriers and dependent steps of a microsecond or less.
 // 2. evict_copy_kernel    moves the kept rows: a block looks up the places of 256 (token,
 //    head) rows first, then moves them, 16 bytes a thread and eight in flight.
@@ -29,11 +29,30 @@ constexpr int kSub = 4;                              // copies of the first hist
 constexpr int kMaxCluster = 8;
 constexpr int kMaxKeys = 32;                         // keys a thread holds at most
 
-constexpr int kMarkRead = 1, kMarkWritten = 2;       // a page's uses: bit 0, and 2 per write
-
 __device__ __forceinline__ int evict_len(const PagedEvictArgs& a, int b) {
   const int n = __ldg(a.lens + b);
   return n >= 0 && n <= a.max_len ? n : -1;
+}
+
+__device__ __forceinline__ int pages_of(const PagedEvictArgs& a, int tokens) {
+  return (tokens + (1 << a.page_shift) - 1) >> a.page_shift;
+}
+
+// Notes about a destination page p, in a workspace that nobody clears: the notes name entries
+// of the tables, and one that its table does not confirm is what was there before.
+//   claim[p]  an entry of dst_table that names p (the last to claim it)
+//   dup[p]    -1 once claimed; the entry that found p claimed by another
+//   hold[p]   an entry of block_table that names p (same pool only; any of them)
+__device__ __forceinline__ bool is_claim(const PagedEvictArgs& a, int entry, int p) {
+  if (entry < 0 || entry >= a.num_seqs * a.dst_max_pages || __ldg(a.dst_table + entry) != p)
+    return false;
+  const int n = evict_len(a, entry / a.dst_max_pages);
+  return entry % a.dst_max_pages < pages_of(a, min(n, a.budget));
+}
+__device__ __forceinline__ bool is_held(const PagedEvictArgs& a, int p) {
+  const int entry = a.hold[p];
+  if (entry < 0 || entry >= a.num_seqs * a.max_pages || __ldg(a.table + entry) != p) return false;
+  return entry % a.max_pages < pages_of(a, evict_len(a, entry / a.max_pages));
 }
 
 // Orders like the scores; NaN counts as -inf and -0 as +0.
@@ -57,12 +76,14 @@ __device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
   return v;
 }
 
-// KPT: keys a thread holds. A CTA's part of the competing tokens is walked in rounds of
+// KPT: keys a thread holds, in registers, or (SHARED) in shared memory: 32 in registers leave
+// room for one CTA per SM, and then only 15 clusters of eight fit the GPU at once (36 with
+// two). A CTA's part of the competing tokens is walked in rounds of
 // kSelThreads * KPT (one, unless the part is longer: then the scores are read again in every
 // pass); in a round each warp has a contiguous run, lane by lane, so that the order of the
 // tokens is (round, warp, i, lane).
-template <int KPT>
-__global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1)
+template <int KPT, bool SHARED>
+__global__ void __launch_bounds__(kSelThreads, 2)
     evict_select_kernel(const PagedEvictArgs a, int cluster) {
   // Scores of one octave share few first digits, so lanes often add to the same bin: four
   // copies, by lane, keep those additions from queueing.
@@ -89,7 +110,11 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1)
   const int e0 = min(rank * per, elig), count = min(per, elig - e0);
   constexpr int kRound = kSelThreads * KPT;
   const int rounds = (per + kRound - 1) / kRound;
-  uint32_t key[KPT];                    // 0: none (every score's key is larger)
+  extern __shared__ uint32_t s_keys[];  // SHARED: [KPT][kSelThreads], each thread its own
+  [[maybe_unused]] uint32_t reg[SHARED ? 1 : KPT];
+  auto key = [&](int i) {               // 0: none (every score's key is larger)
+    return SHARED ? s_keys[i * kSelThreads + threadIdx.x] : reg[SHARED ? 0 : i];
+  };
   int w0 = 0;                           // the warp's first token of the round
   auto load = [&](int round) {
     const int left = max(0, min(kRound, count - round * kRound));
@@ -97,14 +122,24 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1)
     const int end = round * kRound + left;
     w0 = round * kRound + warp * run;
     const int w1 = min(w0 + run, end);
-    float x[KPT];
+    constexpr int kBatch = KPT < 16 ? KPT : 16;  // loads in flight
 #pragma unroll
-    for (int i = 0; i < KPT; ++i) {
-      const int at = w0 + 32 * i + lane;
-      x[i] = at < w1 ? __ldg(score + e0 + at) : 0.f;
+    for (int i0 = 0; i0 < KPT; i0 += kBatch) {
+      float x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int at = w0 + 32 * (i0 + i) + lane;
+        x[i] = at < w1 ? __ldg(score + e0 + at) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t u = w0 + 32 * (i0 + i) + lane < w1 ? score_key(x[i]) : 0u;
+        if (SHARED)
+          s_keys[(i0 + i) * kSelThreads + threadIdx.x] = u;
+        else
+          reg[SHARED ? 0 : i0 + i] = u;
+      }
     }
-#pragma unroll
-    for (int i = 0; i < KPT; ++i) key[i] = w0 + 32 * i + lane < w1 ? score_key(x[i]) : 0u;
   };
   if (k > 0) load(0);
 
@@ -117,15 +152,22 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1)
       a.new_lens[b] = n < 0 ? -1 : fresh;
       if (n < 0) atomicOr(a.err_word, kErrDeviceBounds);
     }
-    const int page = 1 << a.page_shift;
-    if (a.same_pool && n > 0)
-      for (int j = tid; j < (n + page - 1) >> a.page_shift; j += threads) {
-        const int p = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + j);
-        if (p >= 0 && p < a.num_pages) atomicOr(a.marks + p, kMarkRead);
+    if (a.same_pool)
+      for (int j = tid; j < pages_of(a, n); j += threads) {
+        const int p = __ldg(a.table + b * a.max_pages + j);
+        if (p >= 0 && p < a.num_pages) a.hold[p] = b * a.max_pages + j;
       }
-    for (int j = tid; j < (fresh + page - 1) >> a.page_shift; j += threads) {
-      const int p = __ldg(a.dst_table + static_cast<int64_t>(b) * a.dst_max_pages + j);
-      if (p >= 0 && p < a.dst_num_pages) atomicAdd(a.marks + p, kMarkWritten);
+    for (int j = tid; j < pages_of(a, fresh); j += threads) {
+      const int entry = b * a.dst_max_pages + j;
+      const int p = __ldg(a.dst_table + entry);
+      if (p < 0 || p >= a.dst_num_pages) continue;
+      // of several entries that claim p the last one to do so sees another's claim, and its
+      // note follows every clearing
+      a.dup[p] = -1;
+      __threadfence();
+      const int old = atomicExch(a.claim + p, entry);
+      __threadfence();
+      if (old != entry && is_claim(a, old, p)) a.dup[p] = entry;
     }
   }
   // the recent tokens, and what follows the last kept one
@@ -157,13 +199,13 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1)
           uint32_t* mine = s_first[lane & (kSub - 1)];
 #pragma unroll
           for (int i = 0; i < KPT; ++i)
-            if (key[i] != 0) atomicAdd(mine + (key[i] >> 21), 1u);
+            if (key(i) != 0) atomicAdd(mine + (key(i) >> 21), 1u);
         } else {
           const int above = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0;
           const uint32_t mask = pass == 1 ? 2047u : 1023u;
 #pragma unroll
           for (int i = 0; i < KPT; ++i)
-            if (key[i] >> above == prefix) atomicAdd(hist + ((key[i] >> shift) & mask), 1u);
+            if (key(i) >> above == prefix) atomicAdd(hist + ((key(i) >> shift) & mask), 1u);
         }
       }
       __syncthreads();
@@ -240,8 +282,8 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1)
     if (rounds > 1) load(round);
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-      gt += key[i] > threshold;
-      eq += key[i] != 0 && key[i] == threshold;
+      gt += key(i) > threshold;
+      eq += key(i) != 0 && key(i) == threshold;
     }
   }
   gt = __reduce_add_sync(0xFFFFFFFFu, gt);
@@ -275,8 +317,8 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1)
       gt = eq = 0;
 #pragma unroll
       for (int i = 0; i < KPT; ++i) {
-        gt += key[i] > threshold;
-        eq += key[i] != 0 && key[i] == threshold;
+        gt += key(i) > threshold;
+        eq += key(i) != 0 && key(i) == threshold;
       }
       gt = __reduce_add_sync(0xFFFFFFFFu, gt);
       eq = __reduce_add_sync(0xFFFFFFFFu, eq);
@@ -295,24 +337,36 @@ __global__ void __launch_bounds__(kSelThreads, KPT <= 16 ? 2 : 1)
       warp_gt = base_gt + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? lane_gt : 0u);
       warp_eq = base_eq + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? lane_eq : 0u);
     }
+    auto keep = [&](uint32_t u, int i, uint32_t at) {
+      if (at >= static_cast<uint32_t>(k)) return;  // only if the scores change meanwhile
+      const int pos = e0 + w0 + 32 * i + lane;
+      kept[at] = pos;
+      // the key gives the score back, but for the values that share one
+      if (score_out != nullptr)
+        score_out[at] = u == kKeyZero || u == kKeyLowest ? __ldg(score + pos) : key_score(u);
+    };
+    if (eq == 0) {                      // of the warp: no key at the threshold
+      warp_gt += min(warp_eq, need);
 #pragma unroll
-    for (int i = 0; i < KPT; ++i) {
-      const bool is_gt = key[i] > threshold, is_eq = key[i] != 0 && key[i] == threshold;
-      const uint32_t bg = __ballot_sync(0xFFFFFFFFu, is_gt);
-      const uint32_t be = __ballot_sync(0xFFFFFFFFu, is_eq);
-      const uint32_t eq_rank = warp_eq + __popc(be & lower);
-      const uint32_t at = warp_gt + __popc(bg & lower) + min(eq_rank, need);
-      // (places run out only if the scores change meanwhile)
-      if ((is_gt || (is_eq && eq_rank < need)) && at < static_cast<uint32_t>(k)) {
-        const int pos = e0 + w0 + 32 * i + lane;
-        kept[at] = pos;
-        // the key gives the score back, but for the values that share one
-        if (score_out != nullptr)
-          score_out[at] =
-              key[i] == kKeyZero || key[i] == kKeyLowest ? __ldg(score + pos) : key_score(key[i]);
+      for (int i = 0; i < KPT; ++i) {
+        const uint32_t u = key(i);
+        const uint32_t bg = __ballot_sync(0xFFFFFFFFu, u > threshold);
+        if (u > threshold) keep(u, i, warp_gt + __popc(bg & lower));
+        warp_gt += __popc(bg);
       }
-      warp_gt += __popc(bg);
-      warp_eq += __popc(be);
+    } else {
+#pragma unroll
+      for (int i = 0; i < KPT; ++i) {
+        const uint32_t u = key(i);
+        const bool is_eq = u != 0 && u == threshold;
+        const uint32_t bg = __ballot_sync(0xFFFFFFFFu, u > threshold);
+        const uint32_t be = __ballot_sync(0xFFFFFFFFu, is_eq);
+        const uint32_t eq_rank = warp_eq + __popc(be & lower);
+        if (u > threshold || (is_eq && eq_rank < need))
+          keep(u, i, warp_gt + __popc(bg & lower) + min(eq_rank, need));
+        warp_gt += __popc(bg);
+        warp_eq += __popc(be);
+      }
     }
   }
   if (cluster > 1) cluster_sync();  // no CTA leaves while others read its counts
@@ -340,8 +394,9 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const Paged
     const int pos = a.kept[(static_cast<int64_t>(b) * a.hkv + g) * a.budget + i];
     const int to = __ldg(a.dst_table + static_cast<int64_t>(b) * a.dst_max_pages +
                          (i >> a.page_shift));
-    // the destination page is written once, by this sequence, and read by none
-    bool ok = to >= 0 && to < a.dst_num_pages && a.marks[to] == kMarkWritten;
+    // the destination page is written once, by this sequence, and held by none
+    bool ok = to >= 0 && to < a.dst_num_pages && a.dup[to] == -1 &&
+              !(a.same_pool && is_held(a, to));
     int from = -1;
     if (pos >= 0 && pos < n) {
       from = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + (pos >> a.page_shift));
@@ -391,9 +446,7 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const Paged
 }  // namespace
 
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_t stream) {
-  cudaError_t e =
-      cudaMemsetAsync(a.marks, 0, static_cast<size_t>(a.dst_num_pages) * sizeof(int32_t), stream);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
   // CTAs per (sequence, head): enough to hold the keys, and more while SMs are idle and a
   // CTA has thousands of keys
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
@@ -414,9 +467,19 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
   cfg.blockDim = dim3(kSelThreads);
-  e = per <= 4 * kSelThreads    ? cudaLaunchKernelEx(&cfg, evict_select_kernel<4>, a, cluster)
-      : per <= 16 * kSelThreads ? cudaLaunchKernelEx(&cfg, evict_select_kernel<16>, a, cluster)
-                                : cudaLaunchKernelEx(&cfg, evict_select_kernel<kMaxKeys>, a, cluster);
+  if (per <= 4 * kSelThreads) {
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<4, false>, a, cluster);
+  } else if (per <= 16 * kSelThreads) {
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<16, false>, a, cluster);
+  } else {
+    constexpr int kBytes = kSelThreads * kMaxKeys * 4;
+    static std::atomic<uint64_t> ready{0};
+    e = allow_smem(reinterpret_cast<const void*>(evict_select_kernel<kMaxKeys, true>), kBytes, ready);
+    if (e != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = kBytes;
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<kMaxKeys, true>, a, cluster);
+    cfg.dynamicSmemBytes = 0;
+  }
   if (e != cudaSuccess) return e;
   const int chunks = static_cast<int>(
       (static_cast<int64_t>(a.budget) * a.hkv + kCopyThreads - 1) / kCopyThreads);

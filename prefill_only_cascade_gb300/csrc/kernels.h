@@ -217,7 +217,9 @@ struct PagedDecodeArgs {
   DecodeRec* rec;                   // [CTAs]
   float2* part_ml;                  // [2 CTAs][group] max (log2 units) and sum
   float* part_o;                    // [2 CTAs][group][d]
-  float* lse2;                      // [B, Hq], with scores only
+  float* lse2;                      // [B, Hq], with scores only: of what one CTA finished
+  int32_t* begun;                   // [B, Hkv], with scores only: the CTA in which a (sequence,
+                                    // head) of several CTAs begins, or -1
   float* raw;                       // [B, Hq, raw_stride] scores in log2 units, or NULL
   int64_t raw_stride;
   unsigned* err_word;
@@ -266,7 +268,9 @@ struct PagedEvictArgs {
   int32_t* new_lens;
   float* score_out;
   int64_t score_out_stride;
-  int32_t* marks;                    // workspace: [dst_num_pages]
+  int32_t* claim;                    // workspace: [dst_num_pages] each, not cleared
+  int32_t* dup;
+  int32_t* hold;
   unsigned* err_word;
 };
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_t stream);

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 // the order sequence, head, position, and each CTA takes an equal run of them, whatever
 // the lengths are: short sequences share a CTA, long ones spread over many. A sequence's
 // head that lies inside one CTA is finished there; the others leave (max, sum, O) partials
-// that paged_join_kernel rescales and adds.
+// that paged_finish_kernel rescales and adds.
 //
 // Each warp walks its own keys of its CTA's run with a running max and sum. Their K and V
 // rows come through a ring of its own in shared memory, filled by 16-byte asynchronous
@@ -733,6 +733,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
       }
       if (n == 0 && threadIdx.x == 0) {
         if (any_bad) atomicOr(a.err_word, kErrDeviceBounds);
+        if (a.begun != nullptr && cur.at == cur.piece0)
+          a.begun[static_cast<int64_t>(cur.b) * a.hkv + cur.g] = cur.whole ? -1 : cta;
         if (!cur.whole && cur.at == cur.piece0) {  // goes on in the next CTAs: the join's entry
           const int64_t end = cur.piece0 + (cur.len + C::kTile - 1) / C::kTile;
           // the last CTA of (b, g) is the one that holds tile end - 1
@@ -754,14 +756,12 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
 // a task for one warp, or for several where there are fewer tasks than warps. What counts is
 // latency: records of the candidates in one load, eight partials per warp in flight.
 constexpr int kJoinWarps = 8;
+constexpr int kFinishThreads = 32 * kJoinWarps;
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PagedDecodeArgs a,
-                                                                     int ctas, float l_shift) {
+__device__ __forceinline__ void join_parts(const PagedDecodeArgs& a, int ctas, float l_shift) {
   constexpr int V = D / 32;  // values of a lane
   __shared__ alignas(16) float s_acc[kJoinWarps][D];
   __shared__ float2 s_ml[kJoinWarps];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int G = a.group, block = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   DecodeRec rec{-1, 0, 0, 0};
@@ -878,48 +878,100 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
       if (lane == 0) {
         const float lse2 = top + (log2f(sum) - l_shift);
         if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
-        if (a.lse2 != nullptr) a.lse2[row] = lse2;
       }
     }
   }
 }
 
-// score_out[b, g, j] = score_in + sum over the group's heads of exp2(x - lse2), from the
-// scores that the attention left in the workspace (4 bytes per (head, token) against 4 d
-// or 2 d bytes of K and V per G of them, and mostly still in L2).
-constexpr int kWeightThreads = 256, kWeightPer = 4;
-__global__ void __launch_bounds__(kWeightThreads) paged_weights_kernel(const PagedDecodeArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = blockIdx.x / a.hkv, g = blockIdx.x % a.hkv;
+// score_out[b, g, j] = score_in + sum over the group's heads of exp2(x - lse2) for 1,024 keys,
+// from the scores that the attention left in the workspace (4 bytes per (head, token)
+// against 4 d or 2 d bytes of K and V per G of them, and mostly still in L2). lse2 is the
+// attention's own, or formed here from the (max, sum) of its parts.
+constexpr int kWeightPer = 4;
+constexpr int kWeightKeys = kFinishThreads * kWeightPer;
+__device__ __forceinline__ void add_weights(const PagedDecodeArgs& a, int ctas, float l_shift,
+                                            int pair, int chunk, int chunks) {
+  __shared__ float s_lse2[16];
+  const int b = pair / a.hkv;
   const int n = checked_len(a, b);
-  const int64_t row = static_cast<int64_t>(b) * a.hq + static_cast<int64_t>(g) * a.group;
-  const int64_t out_row = (static_cast<int64_t>(b) * a.hkv + g) * a.score_stride;
-  const int64_t chunk = static_cast<int64_t>(gridDim.y) * (kWeightThreads * kWeightPer);
-  for (int64_t j0 = static_cast<int64_t>(blockIdx.y) * (kWeightThreads * kWeightPer) + threadIdx.x;
-       j0 < n; j0 += chunk) {
-    float w[kWeightPer];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = static_cast<int64_t>(pair) * a.group;  // = b * Hq + g * G
+  const int64_t out_row = static_cast<int64_t>(pair) * a.score_stride;
+  const int64_t first = static_cast<int64_t>(chunk) * kWeightKeys;
+  if (first >= n) return;
+  // the inputs of the call and what does not depend on lse2 first
+  float base[kWeightPer];
 #pragma unroll
-    for (int k = 0; k < kWeightPer; ++k) {
-      const int64_t j = j0 + k * kWeightThreads;
-      w[k] = 0.f;
-      if (a.score_in != nullptr && j < n) w[k] = a.score_in[out_row + j];
+  for (int k = 0; k < kWeightPer; ++k) {
+    const int64_t j = first + k * kFinishThreads + threadIdx.x;
+    base[k] = a.score_in != nullptr && j < n ? a.score_in[out_row + j] : 0.f;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c0 = a.begun[pair];
+  if (c0 < 0) {
+    if (threadIdx.x < a.group) s_lse2[threadIdx.x] = a.lse2[row + threadIdx.x];
+  } else {
+    const DecodeRec rec = a.rec[c0];
+    for (int h = warp; h < a.group; h += kJoinWarps) {
+      float top = -INFINITY, sum = 0.f;
+      for (int c = c0 + lane; c <= rec.last; c += 32) {
+        if (rec.sparse != 0 &&
+            first_tile(c, rec.sparse, ctas) == first_tile(c + 1, rec.sparse, ctas))
+          continue;
+        const float2 ml = a.part_ml[(2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * a.group + h];
+        const float to = fmaxf(top, ml.x);
+        sum = sum * (top == -INFINITY ? 0.f : ex2(top - to)) +
+              ml.y * (ml.x == -INFINITY ? 0.f : ex2(ml.x - to));
+        top = to;
+      }
+      float all = top;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) all = fmaxf(all, __shfl_xor_sync(0xFFFFFFFFu, all, off));
+      sum *= top == -INFINITY ? 0.f : ex2(top - all);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+      if (lane == 0) s_lse2[h] = all + (log2f(sum) - l_shift);
     }
+  }
+  __syncthreads();
+  for (int64_t j0 = first; j0 < n; j0 += static_cast<int64_t>(chunks) * kWeightKeys) {
     float add[kWeightPer] = {0.f, 0.f, 0.f, 0.f};
+    if (j0 != first) {
+#pragma unroll
+      for (int k = 0; k < kWeightPer; ++k) {
+        const int64_t j = j0 + k * kFinishThreads + threadIdx.x;
+        base[k] = a.score_in != nullptr && j < n ? a.score_in[out_row + j] : 0.f;
+      }
+    }
 #pragma unroll 4
     for (int h = 0; h < a.group; ++h) {
-      const float lse2 = a.lse2[row + h];
+      const float lse2 = s_lse2[h];
       const float* raw = a.raw + (row + h) * a.raw_stride;
 #pragma unroll
       for (int k = 0; k < kWeightPer; ++k) {
-        const int64_t j = j0 + k * kWeightThreads;
-        if (j < n && lse2 == lse2) add[k] += ex2(raw[j] - lse2);
+        const int64_t j = j0 + k * kFinishThreads + threadIdx.x;
+        const float x = j < n ? raw[j] : -INFINITY;
+        add[k] += lse2 > -INFINITY ? ex2(x - lse2) : 0.f;  // (NaN: nothing either)
       }
     }
 #pragma unroll
     for (int k = 0; k < kWeightPer; ++k) {
-      const int64_t j = j0 + k * kWeightThreads;
-      if (j < n) a.score_out[out_row + j] = w[k] + add[k];
+      const int64_t j = j0 + k * kFinishThreads + threadIdx.x;
+      if (j < n) a.score_out[out_row + j] = base[k] + add[k];
     }
+  }
+}
+
+// What follows the attention: blocks 0 .. ctas - 1 join, the others form the weights.
+template <int D>
+__global__ void __launch_bounds__(kFinishThreads)
+    paged_finish_kernel(const PagedDecodeArgs a, int ctas, float l_shift, int chunks) {
+  if (static_cast<int>(blockIdx.x) < ctas) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    join_parts<D>(a, ctas, l_shift);
+  } else {
+    const int i = static_cast<int>(blockIdx.x) - ctas;
+    add_weights(a, ctas, l_shift, i / chunks, i % chunks, chunks);
   }
 }
 
@@ -940,19 +992,21 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  // the join is left out where no (sequence, head) can have more than one tile, unless the
-  // weights follow (which rely on it having waited for the attention)
-  if (e == cudaSuccess && (a.max_len > C::kTile || a.raw != nullptr)) {
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, ctas, FP8 ? 14.f : 0.f);
-  }
-  if (e == cudaSuccess && a.raw != nullptr && a.max_len > 0) {
-    constexpr int kPer = kWeightThreads * kWeightPer;
-    const int chunks = (a.max_len + kPer - 1) / kPer;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * a.hkv, chunks < 4096 ? chunks : 4096);
-    cfg.blockDim = dim3(kWeightThreads);
-    e = cudaLaunchKernelEx(&cfg, paged_weights_kernel, a);
+  // left out where no (sequence, head) can have more than one tile and no weights are wanted
+  if (e == cudaSuccess && (a.max_len > C::kTile || (a.raw != nullptr && a.max_len > 0))) {
+    int64_t blocks = ctas;
+    int chunks = 1;
+    if (a.raw != nullptr) {
+      const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
+      const int most = (a.max_len + kWeightKeys - 1) / kWeightKeys;
+      // few enough blocks for 32-bit numbers; each then takes several chunks
+      const int64_t room = (1ll << 30) / pairs;
+      chunks = static_cast<int>(most < room ? most : room < 1 ? 1 : room);
+      blocks += pairs * chunks;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kFinishThreads);
+    e = cudaLaunchKernelEx(&cfg, paged_finish_kernel<D>, a, ctas, FP8 ? 14.f : 0.f, chunks);
   }
   return e;
 }
