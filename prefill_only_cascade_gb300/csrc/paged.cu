@@ -907,6 +907,20 @@ __device__ __forceinline__ void add_weights(const PagedDecodeArgs& a, int ctas, 
     base[k] = a.score_in != nullptr && j < n ? a.score_in[out_row + j] : 0.f;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the first heads' scores are on their way while lse2 is worked out
+  float x[4][kWeightPer];
+  auto load_raw = [&](int h0, int64_t j0) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float* raw = a.raw + (row + h0 + u) * a.raw_stride;
+#pragma unroll
+      for (int k = 0; k < kWeightPer; ++k) {
+        const int64_t j = j0 + k * kFinishThreads + threadIdx.x;
+        x[u][k] = h0 + u < a.group && j < n ? raw[j] : -INFINITY;
+      }
+    }
+  };
+  load_raw(0, first);
   const int c0 = a.begun[pair];
   if (c0 < 0) {
     if (threadIdx.x < a.group) s_lse2[threadIdx.x] = a.lse2[row + threadIdx.x];
@@ -943,15 +957,14 @@ __device__ __forceinline__ void add_weights(const PagedDecodeArgs& a, int ctas, 
         base[k] = a.score_in != nullptr && j < n ? a.score_in[out_row + j] : 0.f;
       }
     }
-#pragma unroll 4
-    for (int h = 0; h < a.group; ++h) {
-      const float lse2 = s_lse2[h];
-      const float* raw = a.raw + (row + h) * a.raw_stride;
+    for (int h0 = 0; h0 < a.group; h0 += 4) {
+      if (h0 > 0 || j0 != first) load_raw(h0, j0);
 #pragma unroll
-      for (int k = 0; k < kWeightPer; ++k) {
-        const int64_t j = j0 + k * kFinishThreads + threadIdx.x;
-        const float x = j < n ? raw[j] : -INFINITY;
-        add[k] += lse2 > -INFINITY ? ex2(x - lse2) : 0.f;  // (NaN: nothing either)
+      for (int u = 0; u < 4; ++u) {
+        const float lse2 = h0 + u < a.group ? s_lse2[h0 + u] : -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kWeightPer; ++k)  // a head whose lse is -inf or NaN adds nothing
+          add[k] += lse2 > -INFINITY ? ex2(x[u][k] - lse2) : 0.f;
       }
     }
 #pragma unroll
@@ -964,7 +977,7 @@ __device__ __forceinline__ void add_weights(const PagedDecodeArgs& a, int ctas, 
 
 // What follows the attention: blocks 0 .. ctas - 1 join, the others form the weights.
 template <int D>
-__global__ void __launch_bounds__(kFinishThreads)
+__global__ void __launch_bounds__(kFinishThreads, 4)
     paged_finish_kernel(const PagedDecodeArgs a, int ctas, float l_shift, int chunks) {
   if (static_cast<int>(blockIdx.x) < ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
