@@ -425,7 +425,8 @@ def _need(what, t, dtype, shape, index):
 def _need_rows(what, t, shape, index):
     """bf16 rows [n, heads, d] any distance apart: their address and that distance."""
     st = t.stride()
-    if (t.dtype is not _BF16 or t.shape != shape or t.get_device() != index or len(st) != 3
+    if (t.dtype is not _BF16 or t.shape != shape or index < 0 or t.get_device() != index
+            or len(st) != 3
             or (st[2] != 1 and shape[0]) or (st[1] != shape[2] and shape[1] > 1 and shape[0])):
         _explain(what, t, (_BF16,), shape, index)
     return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
@@ -462,9 +463,7 @@ def _need_score(what, t, rows, heads, least, index):
     return t.data_ptr(), shape[2]
 
 
-def _need_workspace(t, index, size):
-    if t is None:
-        raise ValueError(f"workspace is required (size: {size})")
+def _need_workspace(t, index):
     if t.dtype is not torch.uint8 or t.dim() != 1 or t.get_device() != index or not t.is_contiguous():
         _explain("workspace", t, (torch.uint8,), (None,), index)
     return t.data_ptr(), t.numel()
@@ -520,10 +519,12 @@ def paged_decode_attn(desc: PagedDesc, q, k_pages, v_pages, block_table, seq_len
     """quail_paged_decode_attn: attention of one new token per sequence (q [B, Hq, d] bf16, any
     row stride) over its cached tokens; with score_out ([B, Hkv, n] fp32) also score_in plus
     the weight that each cached token receives (score_in may be score_out)."""
+    if workspace is None:
+        raise ValueError("workspace is required (size: paged_decode_workspace_size(...))")
     dev, B, hq, pages = q.get_device(), desc.num_seqs, desc.num_q_heads, desc.num_pages
-    ws, ws_bytes = _need_workspace(workspace, dev, "paged_decode_workspace_size(...)")
     shape = (B, hq, desc.head_dim)
     qp, q_stride = _need_rows("q", q, shape, dev)
+    ws, ws_bytes = _need_workspace(workspace, dev)
     ks, vs = _need_scales(desc, k_scale, v_scale, dev)
     si = so = None
     width = 0
@@ -577,9 +578,11 @@ def paged_kv_evict(desc: PagedDesc, budget, recent, k_pages, v_pages, block_tabl
     scored others, `budget` in all, copied in order into the pages that dst_table names (of
     the same pool or another); kept [B, Hkv, budget] and new_lens [B] int32 say which and how
     many, score_out [B, Hkv, n] takes their scores."""
+    if workspace is None:
+        raise ValueError("workspace is required (size: paged_evict_workspace_size(...))")
     budget, recent = int(budget), int(recent)
     dev, B, hkv, pages = k_pages.get_device(), desc.num_seqs, desc.num_kv_heads, desc.num_pages
-    ws, ws_bytes = _need_workspace(workspace, dev, "paged_evict_workspace_size(...)")
+    ws, ws_bytes = _need_workspace(workspace, dev)
     sp, width = _need_score("score", score, B, hkv, desc.max_seq_len, dev)
     so, out_width = None, 0
     if score_out is not None:

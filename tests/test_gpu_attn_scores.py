@@ -132,8 +132,8 @@ def test_strides_and_garbage_between():
     check(score[[0, 2]], qs, ks, lse, n, n, scale, True, 0)
 
 
-def test_after_prefill_and_cascade():
-    """With the lse that the prefill and the cascade write: each query's weights sum to 1."""
+def test_after_prefill():
+    """With the lse that the prefill writes: each query's weights sum to 1."""
     hq, hkv, d, S, L = 8, 2, 128, 3, 300
     x = lambda *s: torch.randn(*s, device=DEV).bfloat16()  # noqa: E731
     qs, ks, vs = x(S * L, hq, d), x(S * L, hkv, d), x(S * L, hkv, d)
@@ -150,6 +150,26 @@ def test_after_prefill_and_cascade():
     assert torch.allclose(score[:, :, L - 1].sum(), torch.exp(
         (qs[L - 1::L].float().view(S, hkv, hq // hkv, d) * ks[L - 1::L].float()[:, :, None]).sum(-1)
         / math.sqrt(d) - lse[L - 1::L].view(S, hkv, hq // hkv)).sum(), rtol=1e-4)
+
+
+def test_after_cascade():
+    """The weight that anchors receive from all tokens of their suffixes, whose lse (over the
+    anchor and the suffix itself) the cascade wrote."""
+    import workloads
+    from parity_util import run_cascade
+
+    lay = workloads.layout_from_lengths([300, 0, 77], [3, 1, 2], [90, 5, 40, 9, 120, 3])
+    hq, hkv, d = 8, 2, 128
+    cfg = workloads.AttnConfig("scores", 3, (0, 0), 0, (0, 0), hq, hkv, d, False, 3)
+    t = workloads.make_attention_inputs(cfg, lay, DEV)
+    _, lse = run_cascade((hq, hkv, d), lay, t)
+    q_off = t["suffix_offsets"][t["anchor_suffix_ptr"].long()].contiguous()
+    score = torch.full((3, hkv, 303), -3.0, device=DEV)
+    q.attn_scores(t["q_suf"], t["k_anc"], lse, q_off, t["anchor_offsets"], score, 135, 300,
+                  causal=False)
+    ok()
+    check(score, t["q_suf"], t["k_anc"], lse, np.diff(q_off.cpu().numpy()).tolist(), [300, 0, 77],
+          1 / math.sqrt(d), False, 0)
 
 
 def test_lse_of_minus_infinity_gives_no_weight():

@@ -237,6 +237,38 @@ def test_other_stream_and_captured_graph():
         check_decode(cache, qt, 8, out, lse, score)
 
 
+def test_binding_rejects_what_would_be_misread():
+    cache = Cache([40, 20], 2, 64, 16, False)
+    desc, qt = cache.desc(4), queries(2, 4, 64)
+    ws = torch.empty(q.paged_decode_workspace_size(desc, True), dtype=torch.uint8, device=DEV)
+    good = dict(q=qt, k_pages=cache.k, v_pages=cache.v, block_table=cache.table,
+                seq_lens=cache.seq_lens, out=torch.empty_like(qt), workspace=ws,
+                lse=torch.empty(2, 4, device=DEV), score_out=torch.empty(2, 2, 40, device=DEV))
+    q.paged_decode_attn(desc, **good)
+    ok()
+    for name, bad in [
+            ("q", qt.half()), ("q", qt[:, :2]), ("q", qt.transpose(0, 1)), ("q", qt.cpu()),
+            ("q", torch.empty(2, 4, 128, dtype=torch.bfloat16, device=DEV)[:, :, ::2]),
+            ("k_pages", cache.k[:, :8]), ("v_pages", cache.v.float()),
+            ("k_pages", cache.k.view(torch.uint8)[..., :64]), ("v_pages", cache.v.transpose(1, 2)),
+            ("block_table", cache.table.long()), ("block_table", cache.table[:, :-1]),
+            ("seq_lens", cache.seq_lens.long()), ("seq_lens", cache.seq_lens[:1]),
+            ("seq_lens", cache.seq_lens.cpu()), ("out", torch.empty(2, 4, 64, device=DEV)),
+            ("out", torch.empty(2, 64, 4, dtype=torch.bfloat16, device=DEV).transpose(1, 2)),
+            ("workspace", ws.float()), ("lse", torch.empty(4, 2, device=DEV)),
+            ("score_out", torch.empty(2, 2, 39, device=DEV)),
+            ("score_out", torch.empty(2, 2, 40, device=DEV, dtype=torch.bfloat16))]:
+        with pytest.raises(ValueError, match=name):
+            q.paged_decode_attn(desc, **{**good, name: bad})
+    with pytest.raises(ValueError, match="score_in"):
+        q.paged_decode_attn(desc, **{**good, "score_out": None}, score_in=good["score_out"])
+    with pytest.raises(q.QuailError, match="INVALID_ARG"):
+        q.paged_decode_attn(desc, **{**good, "workspace": ws[:64]})
+    with pytest.raises(ValueError, match="scale"):
+        q.paged_decode_attn(desc, **good, k_scale=torch.ones(2, 2, device=DEV))
+    ok()
+
+
 # ------------------------------------------------------------------ append
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("hkv,d,page", [(1, 64, 16), (8, 128, 64), (2, 128, 256), (3, 64, 32)])
