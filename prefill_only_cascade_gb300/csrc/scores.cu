@@ -227,7 +227,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int mine = left > rank ? (left - rank + cluster - 1) / cluster : 0;
   auto tile_at = [&](int i) { return t_first[0] + rank + i * cluster; };
 
-  if (threadIdx.x == 0) {
+  const uint64_t keep = l2_policy_evict_last();   // queries: read by every key tile
+  const uint64_t once = l2_policy_evict_first();
+  auto load_q = [&](int i) {
+    const int st = i % kQStages, t = static_cast<int>(sr.q0) + sr.f + tile_at(i) * tok;
+    mbar_arrive_expect_tx(&sh.q_full[st], C::kTileBytes);
+    for (int kb = 0; kb < C::kKB; ++kb)
+      tma_load_3d_hint(&q_map, &sh.q_full[st], s_q + st * C::kTileBytes + kb * kBlock, kb * 64,
+                       g * G, t, keep);
+  };
+  if (threadIdx.x == 32 * kWarpLoad) {
     mbar_init(&sh.k_full, 1);
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < kQStages; ++i) {
@@ -240,6 +249,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     sh.abort_flag = 0;
     fence_mbar_init();
+    if (mine > 0) {  // the first loads do not wait for the rest of the set-up
+      mbar_arrive_expect_tx(&sh.k_full, kKeyTiles * C::kTileBytes);
+      for (int kt = 0; kt < kKeyTiles; ++kt)  // keys past the tensor read as zeros
+        for (int kb = 0; kb < C::kKB; ++kb)
+          tma_load_3d_hint(&k_map, &sh.k_full, s_k + kt * C::kTileBytes + kb * kBlock, kb * 64, g,
+                           static_cast<int>(sr.k0) + j0 + kt * kBM, once);
+      for (int i = 0; i < min(mine, kQStages); ++i) load_q(i);
+    }
   }
   if (warp == kWarpMma) {
     tmem_alloc(&sh.tmem, 128 * kGroups);
@@ -255,30 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   float total = 0.f;
   if (warp == kWarpLoad) {
     if (mine > 0) {
-      const bool leader = elect_one();
-      const uint64_t keep = l2_policy_evict_last();  // queries: read by every key tile
-      const uint64_t once = l2_policy_evict_first();
-      if (leader) {
-        mbar_arrive_expect_tx(&sh.k_full, kKeyTiles * C::kTileBytes);
-        for (int kt = 0; kt < kKeyTiles; ++kt)  // keys past the tensor read as zeros
-          for (int kb = 0; kb < C::kKB; ++kb)
-            tma_load_3d_hint(&k_map, &sh.k_full, s_k + kt * C::kTileBytes + kb * kBlock, kb * 64,
-                             g, static_cast<int>(sr.k0) + j0 + kt * kBM, once);
-      }
-      __syncwarp();
       bool ok = true;
-      int armed = 0;
-      for (int i = 0; i < mine && ok; ++i) {
-        const int st = i % kQStages;
-        ok = wait_parity_warp(wc, &sh.q_empty[st], ((i / kQStages) & 1) ^ 1u);
+      int armed = min(mine, kQStages);
+      for (int i = armed; i < mine && ok; ++i) {
+        ok = wait_parity_warp(wc, &sh.q_empty[i % kQStages], ((i / kQStages) & 1) ^ 1u);
         if (!ok) break;
-        if (leader) {
-          mbar_arrive_expect_tx(&sh.q_full[st], C::kTileBytes);
-          const int t = static_cast<int>(sr.q0) + sr.f + tile_at(i) * tok;
-          for (int kb = 0; kb < C::kKB; ++kb)
-            tma_load_3d_hint(&q_map, &sh.q_full[st], s_q + st * C::kTileBytes + kb * kBlock,
-                             kb * 64, g * G, t, keep);
-        }
+        if ((threadIdx.x & 31) == 0) load_q(i);
         __syncwarp();
         ++armed;
       }
@@ -419,7 +418,15 @@ __global__ void __launch_bounds__(kWinThreads, 2)
     return;
   }
 
-  if (threadIdx.x == 0) {
+  const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+  auto load_k = [&](int i) {
+    const int st = i % kWinStages;
+    mbar_arrive_expect_tx(&sh.k_full[st], C::kTileBytes);
+    for (int kb = 0; kb < C::kKB; ++kb)
+      tma_load_3d_hint(&k_map, &sh.k_full[st], s_k + st * C::kTileBytes + kb * kBlock, kb * 64, g,
+                       static_cast<int>(sr.k0) + j0 + i * kBM, once);
+  };
+  if (threadIdx.x == 32 * kWinLoad) {
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < kWinStages; ++i) {
@@ -432,6 +439,12 @@ __global__ void __launch_bounds__(kWinThreads, 2)
     }
     sh.abort_flag = 0;
     fence_mbar_init();
+    // the first loads do not wait for the rest of the set-up
+    mbar_arrive_expect_tx(&sh.q_full, C::kTileBytes);
+    for (int kb = 0; kb < C::kKB; ++kb)
+      tma_load_3d_hint(&q_map, &sh.q_full, s_q + kb * kBlock, kb * 64, g * G,
+                       static_cast<int>(sr.q0) + sr.f, keep);
+    for (int i = 0; i < min(count, kWinStages); ++i) load_k(i);
   }
   if (warp == kWinMma) {
     tmem_alloc(&sh.tmem, 256);
@@ -449,31 +462,17 @@ __global__ void __launch_bounds__(kWinThreads, 2)
   const WaitCtl wc{a.timeout_ns, &sh.abort_flag, a.err_word};
 
   if (warp == kWinLoad) {
-    const bool leader = elect_one();
-    const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
     bool ok = true;
-    int armed = 0;
-    for (int i = 0; i < count && ok; ++i) {
-      const int st = i % kWinStages;
-      ok = wait_parity_warp(wc, &sh.k_empty[st], ((i / kWinStages) & 1) ^ 1u);
+    int armed = min(count, kWinStages);
+    for (int i = armed; i < count && ok; ++i) {
+      ok = wait_parity_warp(wc, &sh.k_empty[i % kWinStages], ((i / kWinStages) & 1) ^ 1u);
       if (!ok) break;
-      if (leader) {
-        mbar_arrive_expect_tx(&sh.k_full[st], C::kTileBytes);
-        for (int kb = 0; kb < C::kKB; ++kb)
-          tma_load_3d_hint(&k_map, &sh.k_full[st], s_k + st * C::kTileBytes + kb * kBlock, kb * 64,
-                           g, static_cast<int>(sr.k0) + j0 + i * kBM, once);
-        if (i == 0) {
-          mbar_arrive_expect_tx(&sh.q_full, C::kTileBytes);
-          for (int kb = 0; kb < C::kKB; ++kb)
-            tma_load_3d_hint(&q_map, &sh.q_full, s_q + kb * kBlock, kb * 64, g * G,
-                             static_cast<int>(sr.q0) + sr.f, keep);
-        }
-      }
+      if ((threadIdx.x & 31) == 0) load_k(i);
       __syncwarp();
       ++armed;
     }
     const uint64_t deadline = global_timer_ns() + 100000000ull;
-    if (armed > 0) drain(&sh.q_full, 0, deadline);
+    drain(&sh.q_full, 0, deadline);
     for (int i = armed > kWinStages ? armed - kWinStages : 0; i < armed; ++i)
       drain(&sh.k_full[i % kWinStages], (i / kWinStages) & 1u, deadline);
   } else if (warp == kWinMma) {
@@ -533,8 +532,8 @@ cudaError_t launch_t(const AttnScoresArgs& a, const CUtensorMap& q_map, const CU
   if (static_cast<int64_t>(most) * a.group <= kBN) {
     // runs of key tiles: long ones fill the ring's pipeline, short ones the GPU
     const int key_tiles = (a.max_k + kBM - 1) / kBM;
-    int run = 8;
-    while (run > 1 && pairs * ((key_tiles + run - 1) / run) < 8 * num_sms) run /= 2;
+    int run = 16;
+    while (run > 1 && pairs * ((key_tiles + run - 1) / run) < 2 * num_sms) run /= 2;
     static std::atomic<uint64_t> ready{0};
     e = allow_smem(reinterpret_cast<const void*>(attn_scores_window_kernel<D>), C::kWinSmem, ready);
     if (e != cudaSuccess) return e;
