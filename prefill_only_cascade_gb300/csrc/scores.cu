@@ -16,9 +16,10 @@
 //     parity of the query tile, each with its own S^T in TMEM) keep the MUFU fed while the
 //     tensor cores fill the other parity. 256 keys and not 128, so that a query tile is read
 //     from L2 once per two products (~9 TB/s at full rate instead of 18).
-//   attn_scores_window_kernel   where the queries of a (sequence, KV head) fit one tile (the
-//     last 32 tokens at G = 4), the tile stays and the keys stream past it: bound by reading
-//     K once from HBM.
+//   attn_scores_window_kernel   where the queries of a (sequence, KV head) fit four tiles (the
+//     last 128 tokens at G = 4), they stay in shared memory and the keys stream past them, a
+//     warpgroup per key tile: bound by reading K once from HBM with one query tile, by the
+//     exponentials with four.
 
 #include <cstddef>
 #include <cstdint>
@@ -45,14 +46,15 @@ constexpr int kQStages = 4;
 // attn_scores_window_kernel
 constexpr int kWinThreads = 2 * 128 + 64;   // two warpgroups take the key tiles in turn
 constexpr int kWinLoad = 8, kWinMma = 9;
-constexpr int kWinStages = 2;               // key tiles in flight; two CTAs share an SM
+constexpr int kWinStages = 2;               // key tiles in flight
+constexpr int kWinMaxQ = 4;                 // query tiles kept; with one, two CTAs share an SM
 
 template <int D>
 struct Cfg {
   static constexpr int kKB = D / 64;               // 64-column blocks
   static constexpr int kTileBytes = kKB * kBlock;  // 128 rows of K or Q
   static constexpr int kSmem = kTileBytes * (kKeyTiles + kQStages) + 1024;  // + alignment slack
-  static constexpr int kWinSmem = kTileBytes * (1 + kWinStages) + 1024;
+  static constexpr int win_smem(int q_tiles) { return kTileBytes * (q_tiles + kWinStages) + 1024; }
 };
 
 struct Shared {
@@ -66,10 +68,10 @@ struct Shared {
   int abort_flag;
 };
 struct WinShared {
-  alignas(16) float nlse[kBN];
+  alignas(16) float nlse[kWinMaxQ * kBN];
   uint64_t q_full, drain;
   uint64_t k_full[kWinStages], k_empty[kWinStages];
-  uint64_t s_full[2], s_empty[2];
+  uint64_t s_full[2][2], s_empty[2][2];     // [warpgroup][buffer]
   uint32_t tmem;
   int abort_flag;
 };
@@ -387,8 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWinThreads, 2)
+// QT: query tiles that fit (1, 2 or 4).
+template <int D, int QT>
+__global__ void __launch_bounds__(kWinThreads, QT == 1 ? 2 : 1)
     attn_scores_window_kernel(const AttnScoresArgs a, const __grid_constant__ CUtensorMap q_map,
                               const __grid_constant__ CUtensorMap k_map, int run) {
   using C = Cfg<D>;
@@ -396,7 +399,8 @@ __global__ void __launch_bounds__(kWinThreads, 2)
   __shared__ WinShared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~1023ull);
   uint8_t* s_q = smem;
-  uint8_t* s_k = smem + C::kTileBytes;
+  uint8_t* s_k = smem + QT * C::kTileBytes;
+  constexpr int kBufs = QT == 1 ? 1 : 2;  // S^T tiles of a warpgroup
   const int warp = threadIdx.x >> 5;
   int id = blockIdx.x;
   const int g = id % a.hkv;
@@ -418,6 +422,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
     return;
   }
 
+  const int tok = kBN / G, q_tiles = (sr.w + tok - 1) / tok;  // at most QT
   const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
   auto load_k = [&](int i) {
     const int st = i % kWinStages;
@@ -433,27 +438,28 @@ __global__ void __launch_bounds__(kWinThreads, 2)
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.k_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_empty[i], 128);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.s_full[i >> 1][i & 1], 1);
+      mbar_init(&sh.s_empty[i >> 1][i & 1], 128);
     }
     sh.abort_flag = 0;
     fence_mbar_init();
     // the first loads do not wait for the rest of the set-up
-    mbar_arrive_expect_tx(&sh.q_full, C::kTileBytes);
-    for (int kb = 0; kb < C::kKB; ++kb)
-      tma_load_3d_hint(&q_map, &sh.q_full, s_q + kb * kBlock, kb * 64, g * G,
-                       static_cast<int>(sr.q0) + sr.f, keep);
+    mbar_arrive_expect_tx(&sh.q_full, q_tiles * C::kTileBytes);
+    for (int qt = 0; qt < q_tiles; ++qt)
+      for (int kb = 0; kb < C::kKB; ++kb)
+        tma_load_3d_hint(&q_map, &sh.q_full, s_q + qt * C::kTileBytes + kb * kBlock, kb * 64, g * G,
+                         static_cast<int>(sr.q0) + sr.f + qt * tok, keep);
     for (int i = 0; i < min(count, kWinStages); ++i) load_k(i);
   }
   if (warp == kWinMma) {
-    tmem_alloc(&sh.tmem, 256);
+    tmem_alloc(&sh.tmem, 256 * kBufs);
     tmem_relinquish();
   }
-  if (threadIdx.x < kBN) {
-    const int t = sr.f + threadIdx.x / G;
-    const float l = t < sr.nq ? __ldg(a.lse + (sr.q0 + t) * a.hq + g * G + threadIdx.x % G) : 0.f;
-    sh.nlse[threadIdx.x] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+  for (int r = threadIdx.x; r < q_tiles * kBN; r += kWinThreads) {
+    const int t = sr.f + r / G;
+    const float l = t < sr.nq ? __ldg(a.lse + (sr.q0 + t) * a.hq + g * G + r % G) : 0.f;
+    sh.nlse[r] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
   }
   tc_fence_before();
   __syncthreads();
@@ -480,46 +486,82 @@ __global__ void __launch_bounds__(kWinThreads, 2)
     const uint32_t k_lo = sw128_desc_lo(smem_u32(s_k), 16);
     const uint32_t q_lo = sw128_desc_lo(smem_u32(s_q), 16);
     bool ok = wait_parity_warp(wc, &sh.q_full, 0);
-    for (int i = 0; i < count && ok; ++i) {
-      const int st = i % kWinStages, buf = i & 1;
-      ok = wait_parity_warp(wc, &sh.k_full[st], (i / kWinStages) & 1u) &&
-           wait_parity_warp(wc, &sh.s_empty[buf], ((i >> 1) & 1) ^ 1u);
-      if (!ok) break;
-      tc_fence_after();
-      if (leader) {
-        mma_tile<D>(tmem + 128u * buf, k_lo + st * (C::kTileBytes >> 4), q_lo);
-        mma_commit(&sh.k_empty[st]);
-        mma_commit(&sh.s_full[buf]);
+    // the warpgroups' key tiles side by side, query tile by query tile
+    for (int i0 = 0, n = 0; i0 < count && ok; i0 += 2) {
+      for (int qt = 0; qt < q_tiles && ok; ++qt, ++n) {
+        const int buf = n % kBufs;
+        const uint32_t parity = ((n / kBufs) & 1u) ^ 1u;
+        for (int grp = 0; grp < 2 && i0 + grp < count && ok; ++grp) {
+          const int st = (i0 + grp) % kWinStages;
+          ok = (qt > 0 || wait_parity_warp(wc, &sh.k_full[st], ((i0 + grp) / kWinStages) & 1u)) &&
+               wait_parity_warp(wc, &sh.s_empty[grp][buf], parity);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            mma_tile<D>(tmem + 128u * (grp * kBufs + buf), k_lo + st * (C::kTileBytes >> 4),
+                        q_lo + qt * (C::kTileBytes >> 4));
+            if (qt == q_tiles - 1) mma_commit(&sh.k_empty[st]);
+            mma_commit(&sh.s_full[grp][buf]);
+          }
+          __syncwarp();
+        }
       }
-      __syncwarp();
     }
     if (leader) mma_commit(&sh.drain);
     __syncwarp();
     drain(&sh.drain, 0, global_timer_ns() + 100000000ull);
   } else {
     const int grp = warp >> 2, row = threadIdx.x & 127;
-    const uint32_t t_tile = tmem + 128u * grp + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t_lane =
+        tmem + 128u * grp * kBufs + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
-    const int rows = sr.w * G;
-    for (int i = grp; i < count; i += 2) {
+    int n = 0;                          // S^T tiles so far
+    bool ok = true;
+    for (int i = grp; i < count && ok; i += 2) {
       const int key = j0 + i * kBM + row;
       const bool real = key < sr.nk;
       const float base = real && a.score_in != nullptr ? a.score_in[out0 + key] : 0.f;
-      if (!__all_sync(0xFFFFFFFFu, wait_parity(wc, &sh.s_full[grp], (i >> 1) & 1u))) break;
-      tc_fence_after();
-      const bool whole =
-          rows == kBN && !(a.causal && j0 + (i + 1) * kBM - 1 > sr.f + sr.off);
-      const int lo = a.causal && !whole ? first_row(key, sr.off, sr.f, G) : 0;
-      const float w = tile_weight(t_tile, sh.nlse, c2, whole, lo, rows, &sh.s_empty[grp]);
-      if (real) a.score_out[out0 + key] = base + w;
+      float w = 0.f;
+      for (int qt = 0; qt < q_tiles; ++qt, ++n) {
+        const int buf = n % kBufs;
+        ok = __all_sync(0xFFFFFFFFu, wait_parity(wc, &sh.s_full[grp][buf], (n / kBufs) & 1u));
+        if (!ok) break;
+        tc_fence_after();
+        const int t0 = sr.f + qt * tok, rows = min(kBN, (sr.w - qt * tok) * G);
+        const bool whole = rows == kBN && !(a.causal && j0 + (i + 1) * kBM - 1 > t0 + sr.off);
+        const int lo = a.causal && !whole ? first_row(key, sr.off, t0, G) : 0;
+        w += tile_weight(t_lane + 128u * buf, sh.nlse + qt * kBN, c2, whole, lo, rows,
+                         &sh.s_empty[grp][buf]);
+      }
+      if (real && ok) a.score_out[out0 + key] = base + w;
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kWinMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 256 * kBufs);
   }
+}
+
+template <int D, int QT>
+cudaError_t launch_window(const AttnScoresArgs& a, const CUtensorMap& q_map,
+                          const CUtensorMap& k_map, int num_sms, cudaStream_t stream) {
+  constexpr int kBytes = Cfg<D>::win_smem(QT);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(
+      reinterpret_cast<const void*>(attn_scores_window_kernel<D, QT>), kBytes, ready);
+  if (e != cudaSuccess) return e;
+  // Runs of key tiles, as long as there are two blocks per SM: a block costs 4-5 us besides
+  // its tiles. Runs of 2, 4, 8 and 16 tiles measured 47, 37, 32 and 32 us (64 prompts of
+  // 128-2,048 tokens, the last 32 tokens of each).
+  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
+  const int key_tiles = (a.max_k + kBM - 1) / kBM;
+  int run = 16;
+  while (run > 1 && pairs * ((key_tiles + run - 1) / run) < 2 * num_sms) run /= 2;
+  const unsigned blocks = static_cast<unsigned>(pairs * ((key_tiles + run - 1) / run));
+  attn_scores_window_kernel<D, QT><<<blocks, kWinThreads, kBytes, stream>>>(a, q_map, k_map, run);
+  return cudaGetLastError();
 }
 
 template <int D>
@@ -528,20 +570,11 @@ cudaError_t launch_t(const AttnScoresArgs& a, const CUtensorMap& q_map, const CU
   using C = Cfg<D>;
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
   const int most = a.window > 0 && a.window < a.max_q ? a.window : a.max_q;
+  const int64_t tiles = (static_cast<int64_t>(most) * a.group + kBN - 1) / kBN;
+  if (tiles <= 1) return launch_window<D, 1>(a, q_map, k_map, num_sms, stream);
+  if (tiles <= 2) return launch_window<D, 2>(a, q_map, k_map, num_sms, stream);
+  if (tiles <= kWinMaxQ) return launch_window<D, kWinMaxQ>(a, q_map, k_map, num_sms, stream);
   cudaError_t e;
-  if (static_cast<int64_t>(most) * a.group <= kBN) {
-    // runs of key tiles: long ones fill the ring's pipeline, short ones the GPU
-    const int key_tiles = (a.max_k + kBM - 1) / kBM;
-    int run = 16;
-    while (run > 1 && pairs * ((key_tiles + run - 1) / run) < 2 * num_sms) run /= 2;
-    static std::atomic<uint64_t> ready{0};
-    e = allow_smem(reinterpret_cast<const void*>(attn_scores_window_kernel<D>), C::kWinSmem, ready);
-    if (e != cudaSuccess) return e;
-    const unsigned blocks = static_cast<unsigned>(pairs * ((key_tiles + run - 1) / run));
-    attn_scores_window_kernel<D><<<blocks, kWinThreads, C::kWinSmem, stream>>>(a, q_map, k_map,
-                                                                               run);
-    return cudaGetLastError();
-  }
   static std::atomic<uint64_t> ready{0};
   e = allow_smem(reinterpret_cast<const void*>(attn_scores_kernel<D>), C::kSmem, ready);
   if (e != cudaSuccess) return e;
@@ -550,7 +583,6 @@ cudaError_t launch_t(const AttnScoresArgs& a, const CUtensorMap& q_map, const CU
   // are two blocks per SM, at least eight tiles apiece. A block costs about 5 us besides its
   // tiles (~1 us each): four per SM measured 260 us against 242 (4 x 4,096 tokens, all
   // queries) and 199 against 178 (8 anchors of 1,024 tokens, ~3,000 queries each).
-  const int64_t tiles = (static_cast<int64_t>(most) * a.group + kBN - 1) / kBN;
   int cluster = 1;
   while (cluster < kMaxCluster && blocks * cluster < 2 * num_sms && tiles >= 16 * cluster)
     cluster *= 2;
