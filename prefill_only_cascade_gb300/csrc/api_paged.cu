@@ -256,6 +256,9 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
   if (total_k_tokens > 0 && (k == nullptr || score_out == nullptr || !aligned(k, 16)))
     return QUAIL_ERR_INVALID_ARG;
   if (!aligned(score_in, 4) || !aligned(score_out, 4)) return QUAIL_ERR_INVALID_ARG;
+  // TMA coordinates run up to two tiles past the last token
+  if (total_q_tokens > kInt32Max - 1024 || total_k_tokens > kInt32Max - 1024)
+    return QUAIL_ERR_UNSUPPORTED;
   // 8 blocks at most per (sequence, KV head, 128 keys)
   if ((static_cast<int64_t>(max_k_len) + 127) / 128 * num_seqs > kInt32Max / 8 / num_kv_heads)
     return QUAIL_ERR_UNSUPPORTED;

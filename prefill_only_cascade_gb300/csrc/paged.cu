@@ -1012,8 +1012,9 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
     if (a.raw != nullptr) {
       const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
       const int most = (a.max_len + kWeightKeys - 1) / kWeightKeys;
-      // few enough blocks for 32-bit numbers; each then takes several chunks
-      const int64_t room = (1ll << 30) / pairs;
+      // Blocks of 1,024 keys as long as there are not many thousands of them (the lengths may
+      // be far below max_seq_len); beyond that a block takes several chunks.
+      const int64_t room = 8192 / pairs;
       chunks = static_cast<int>(most < room ? most : room < 1 ? 1 : room);
       blocks += pairs * chunks;
     }

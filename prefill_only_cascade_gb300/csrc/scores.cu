@@ -44,17 +44,28 @@ constexpr int kWarpLoad = 4 * kGroups, kWarpMma = 4 * kGroups + 1;
 constexpr int kQStages = 4;
 
 // attn_scores_window_kernel
-constexpr int kWinThreads = 2 * 128 + 64;   // two warpgroups take the key tiles in turn
-constexpr int kWinLoad = 8, kWinMma = 9;
-constexpr int kWinStages = 2;               // key tiles in flight
-constexpr int kWinMaxQ = 4;                 // query tiles kept; with one, two CTAs share an SM
+constexpr int kWinMaxQ = 4;                 // query tiles kept at most
+// QT query tiles kept: the warpgroups that take the key tiles in turn, key tiles in flight,
+// and S^T tiles of a warpgroup. One: two CTAs share an SM. Two: four warpgroups keep the MUFU
+// busier than two. Four: shared memory has no room for more than two key tiles.
+template <int QT>
+struct Win {
+  static constexpr int kGroups = QT == 2 ? 4 : 2;
+  static constexpr int kStages = kGroups;
+  static constexpr int kBufs = QT == 4 ? 2 : 1;
+  static constexpr int kTmem = 128 * kGroups * kBufs;
+  static constexpr int kThreads = 128 * kGroups + 64;  // + the TMA warp and the MMA warp
+  static constexpr int kLoad = 4 * kGroups, kMma = 4 * kGroups + 1;
+};
 
 template <int D>
 struct Cfg {
   static constexpr int kKB = D / 64;               // 64-column blocks
   static constexpr int kTileBytes = kKB * kBlock;  // 128 rows of K or Q
   static constexpr int kSmem = kTileBytes * (kKeyTiles + kQStages) + 1024;  // + alignment slack
-  static constexpr int win_smem(int q_tiles) { return kTileBytes * (q_tiles + kWinStages) + 1024; }
+  static constexpr int win_smem(int q_tiles, int stages) {
+    return kTileBytes * (q_tiles + stages) + 1024;
+  }
 };
 
 struct Shared {
@@ -70,8 +81,8 @@ struct Shared {
 struct WinShared {
   alignas(16) float nlse[kWinMaxQ * kBN];
   uint64_t q_full, drain;
-  uint64_t k_full[kWinStages], k_empty[kWinStages];
-  uint64_t s_full[2][2], s_empty[2][2];     // [warpgroup][buffer]
+  uint64_t k_full[4], k_empty[4];
+  uint64_t s_full[4][2], s_empty[4][2];     // [warpgroup][buffer]
   uint32_t tmem;
   int abort_flag;
 };
@@ -145,24 +156,41 @@ __device__ __forceinline__ bool seq_range(const AttnScoresArgs& a, int s, SeqRan
 }
 
 // Adds the weights of one S^T tile (in TMEM at t_tile, this thread's lane) that this thread's
-// key receives. Query rows [lo, hi) see it; `whole`: all rows see all keys of the tile.
-// Releases the TMEM tile as soon as it is in registers.
-__device__ __forceinline__ float tile_weight(uint32_t t_tile, const float* nlse, uint64_t c2,
-                                             bool whole, int lo, int hi, uint64_t* s_empty) {
+// key receives: those of the query rows [lo, hi). lo_first and lo_last are the warp's first
+// and last lanes' lo: 32 columns that no lane sees are skipped, those that all see take no
+// mask. Releases the TMEM tile as soon as it is in registers.
+__device__ __forceinline__ float tile_weight(uint32_t t_tile, const float* nlse, uint64_t c2, int lo,
+                                             int lo_first, int lo_last, int hi, uint64_t* s_empty) {
   uint64_t acc[4] = {0, 0, 0, 0};
+  if (lo_last == 0 && hi == kBN) {  // most tiles
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t v[32];
-    tmem_ld32(t_tile + 32 * q, v);
-    tmem_wait_ld_dep(v);
-    if (q == 3) {
-      tc_fence_before();
-      mbar_arrive(s_empty);
-    }
-    if (whole)
+    for (int q = 0; q < 4; ++q) {
+      uint32_t v[32];
+      tmem_ld32(t_tile + 32 * q, v);
+      tmem_wait_ld_dep(v);
+      if (q == 3) {
+        tc_fence_before();
+        mbar_arrive(s_empty);
+      }
       add_columns<false>(v, nlse + 32 * q, c2, 0, 0, acc);
-    else
-      add_columns<true>(v, nlse + 32 * q, c2, lo - 32 * q, hi - 32 * q, acc);
+    }
+  } else {
+    const int q0 = lo_first >> 5, q1 = (hi + 31) >> 5;
+    if (q0 >= q1) mbar_arrive(s_empty);
+#pragma unroll 1
+    for (int q = q0; q < q1; ++q) {
+      uint32_t v[32];
+      tmem_ld32(t_tile + 32 * q, v);
+      tmem_wait_ld_dep(v);
+      if (q == q1 - 1) {
+        tc_fence_before();
+        mbar_arrive(s_empty);
+      }
+      if (lo_last <= 32 * q && 32 * q + 32 <= hi)
+        add_columns<false>(v, nlse + 32 * q, c2, 0, 0, acc);
+      else
+        add_columns<true>(v, nlse + 32 * q, c2, lo - 32 * q, hi - 32 * q, acc);
+    }
   }
   float x0, x1, y0, y1;
   f2_split(f2_add(acc[0], acc[1]), x0, x1);
@@ -355,12 +383,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) continue;
       tc_fence_after();
       const int t0 = sr.f + tile_at(i) * tok;
-      const bool whole =
-          t0 + tok <= sr.nq && !(a.causal && j0 + (kt + 1) * kBM - 1 > t0 + sr.off);
       const int hi = sr.nq - t0 >= tok ? kBN : (sr.nq - t0) * G;
-      const int lo = a.causal && !whole ? first_row(key, sr.off, t0, G) : 0;
+      int lo = 0, lo_first = 0, lo_last = 0;
+      if (a.causal && j0 + (kt + 1) * kBM - 1 > t0 + sr.off) {
+        lo = first_row(key, sr.off, t0, G);
+        lo_first = __shfl_sync(0xFFFFFFFFu, lo, 0);
+        lo_last = __shfl_sync(0xFFFFFFFFu, lo, 31);
+      }
       // compensated: thousands of tiles may add up (Kahan)
-      const float y = tile_weight(t_tile, nlse, c2, whole, lo, hi, &sh.s_empty[grp]) - lost;
+      const float y = tile_weight(t_tile, nlse, c2, lo, lo_first, lo_last, hi, &sh.s_empty[grp]) - lost;
       const float sum = total + y;
       lost = fabsf(sum) < INFINITY ? (sum - total) - y : 0.f;
       total = sum;
@@ -391,16 +422,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // QT: query tiles that fit (1, 2 or 4).
 template <int D, int QT>
-__global__ void __launch_bounds__(kWinThreads, QT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(Win<QT>::kThreads, QT == 1 ? 2 : 1)
     attn_scores_window_kernel(const AttnScoresArgs a, const __grid_constant__ CUtensorMap q_map,
                               const __grid_constant__ CUtensorMap k_map, int run) {
   using C = Cfg<D>;
+  using W = Win<QT>;
   extern __shared__ uint8_t dyn[];
   __shared__ WinShared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~1023ull);
   uint8_t* s_q = smem;
   uint8_t* s_k = smem + QT * C::kTileBytes;
-  constexpr int kBufs = QT == 1 ? 1 : 2;  // S^T tiles of a warpgroup
   const int warp = threadIdx.x >> 5;
   int id = blockIdx.x;
   const int g = id % a.hkv;
@@ -417,7 +448,7 @@ __global__ void __launch_bounds__(kWinThreads, QT == 1 ? 2 : 1)
   const int count = min(run, (sr.nk - j0 + kBM - 1) / kBM);  // key tiles of this CTA
   const int64_t out0 = (static_cast<int64_t>(s) * a.hkv + g) * a.score_stride;
   if (sr.w == 0) {  // no queries
-    for (int j = j0 + threadIdx.x; j < min(sr.nk, j0 + count * kBM); j += kWinThreads)
+    for (int j = j0 + threadIdx.x; j < min(sr.nk, j0 + count * kBM); j += W::kThreads)
       a.score_out[out0 + j] = a.score_in != nullptr ? a.score_in[out0 + j] : 0.f;
     return;
   }
@@ -425,20 +456,20 @@ __global__ void __launch_bounds__(kWinThreads, QT == 1 ? 2 : 1)
   const int tok = kBN / G, q_tiles = (sr.w + tok - 1) / tok;  // at most QT
   const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
   auto load_k = [&](int i) {
-    const int st = i % kWinStages;
+    const int st = i % W::kStages;
     mbar_arrive_expect_tx(&sh.k_full[st], C::kTileBytes);
     for (int kb = 0; kb < C::kKB; ++kb)
       tma_load_3d_hint(&k_map, &sh.k_full[st], s_k + st * C::kTileBytes + kb * kBlock, kb * 64, g,
                        static_cast<int>(sr.k0) + j0 + i * kBM, once);
   };
-  if (threadIdx.x == 32 * kWinLoad) {
+  if (threadIdx.x == 32 * W::kLoad) {
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.drain, 1);
-    for (int i = 0; i < kWinStages; ++i) {
+    for (int i = 0; i < W::kStages; ++i) {
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.k_empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * W::kGroups; ++i) {
       mbar_init(&sh.s_full[i >> 1][i & 1], 1);
       mbar_init(&sh.s_empty[i >> 1][i & 1], 128);
     }
@@ -450,13 +481,13 @@ __global__ void __launch_bounds__(kWinThreads, QT == 1 ? 2 : 1)
       for (int kb = 0; kb < C::kKB; ++kb)
         tma_load_3d_hint(&q_map, &sh.q_full, s_q + qt * C::kTileBytes + kb * kBlock, kb * 64, g * G,
                          static_cast<int>(sr.q0) + sr.f + qt * tok, keep);
-    for (int i = 0; i < min(count, kWinStages); ++i) load_k(i);
+    for (int i = 0; i < min(count, W::kStages); ++i) load_k(i);
   }
-  if (warp == kWinMma) {
-    tmem_alloc(&sh.tmem, 256 * kBufs);
+  if (warp == W::kMma) {
+    tmem_alloc(&sh.tmem, W::kTmem);
     tmem_relinquish();
   }
-  for (int r = threadIdx.x; r < q_tiles * kBN; r += kWinThreads) {
+  for (int r = threadIdx.x; r < q_tiles * kBN; r += W::kThreads) {
     const int t = sr.f + r / G;
     const float l = t < sr.nq ? __ldg(a.lse + (sr.q0 + t) * a.hq + g * G + r % G) : 0.f;
     sh.nlse[r] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
@@ -467,11 +498,11 @@ __global__ void __launch_bounds__(kWinThreads, QT == 1 ? 2 : 1)
   const uint32_t tmem = sh.tmem;
   const WaitCtl wc{a.timeout_ns, &sh.abort_flag, a.err_word};
 
-  if (warp == kWinLoad) {
+  if (warp == W::kLoad) {
     bool ok = true;
-    int armed = min(count, kWinStages);
+    int armed = min(count, W::kStages);
     for (int i = armed; i < count && ok; ++i) {
-      ok = wait_parity_warp(wc, &sh.k_empty[i % kWinStages], ((i / kWinStages) & 1) ^ 1u);
+      ok = wait_parity_warp(wc, &sh.k_empty[i % W::kStages], ((i / W::kStages) & 1) ^ 1u);
       if (!ok) break;
       if ((threadIdx.x & 31) == 0) load_k(i);
       __syncwarp();
@@ -479,26 +510,26 @@ __global__ void __launch_bounds__(kWinThreads, QT == 1 ? 2 : 1)
     }
     const uint64_t deadline = global_timer_ns() + 100000000ull;
     drain(&sh.q_full, 0, deadline);
-    for (int i = armed > kWinStages ? armed - kWinStages : 0; i < armed; ++i)
-      drain(&sh.k_full[i % kWinStages], (i / kWinStages) & 1u, deadline);
-  } else if (warp == kWinMma) {
+    for (int i = armed > W::kStages ? armed - W::kStages : 0; i < armed; ++i)
+      drain(&sh.k_full[i % W::kStages], (i / W::kStages) & 1u, deadline);
+  } else if (warp == W::kMma) {
     const bool leader = elect_one();
     const uint32_t k_lo = sw128_desc_lo(smem_u32(s_k), 16);
     const uint32_t q_lo = sw128_desc_lo(smem_u32(s_q), 16);
     bool ok = wait_parity_warp(wc, &sh.q_full, 0);
     // the warpgroups' key tiles side by side, query tile by query tile
-    for (int i0 = 0, n = 0; i0 < count && ok; i0 += 2) {
+    for (int i0 = 0, n = 0; i0 < count && ok; i0 += W::kGroups) {
       for (int qt = 0; qt < q_tiles && ok; ++qt, ++n) {
-        const int buf = n % kBufs;
-        const uint32_t parity = ((n / kBufs) & 1u) ^ 1u;
-        for (int grp = 0; grp < 2 && i0 + grp < count && ok; ++grp) {
-          const int st = (i0 + grp) % kWinStages;
-          ok = (qt > 0 || wait_parity_warp(wc, &sh.k_full[st], ((i0 + grp) / kWinStages) & 1u)) &&
+        const int buf = n % W::kBufs;
+        const uint32_t parity = ((n / W::kBufs) & 1u) ^ 1u;
+        for (int grp = 0; grp < W::kGroups && i0 + grp < count && ok; ++grp) {
+          const int st = (i0 + grp) % W::kStages;
+          ok = (qt > 0 || wait_parity_warp(wc, &sh.k_full[st], ((i0 + grp) / W::kStages) & 1u)) &&
                wait_parity_warp(wc, &sh.s_empty[grp][buf], parity);
           if (!ok) break;
           tc_fence_after();
           if (leader) {
-            mma_tile<D>(tmem + 128u * (grp * kBufs + buf), k_lo + st * (C::kTileBytes >> 4),
+            mma_tile<D>(tmem + 128u * (grp * W::kBufs + buf), k_lo + st * (C::kTileBytes >> 4),
                         q_lo + qt * (C::kTileBytes >> 4));
             if (qt == q_tiles - 1) mma_commit(&sh.k_empty[st]);
             mma_commit(&sh.s_full[grp][buf]);
@@ -513,24 +544,28 @@ __global__ void __launch_bounds__(kWinThreads, QT == 1 ? 2 : 1)
   } else {
     const int grp = warp >> 2, row = threadIdx.x & 127;
     const uint32_t t_lane =
-        tmem + 128u * grp * kBufs + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        tmem + 128u * grp * W::kBufs + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
     int n = 0;                          // S^T tiles so far
     bool ok = true;
-    for (int i = grp; i < count && ok; i += 2) {
+    for (int i = grp; i < count && ok; i += W::kGroups) {
       const int key = j0 + i * kBM + row;
       const bool real = key < sr.nk;
       const float base = real && a.score_in != nullptr ? a.score_in[out0 + key] : 0.f;
       float w = 0.f;
       for (int qt = 0; qt < q_tiles; ++qt, ++n) {
-        const int buf = n % kBufs;
-        ok = __all_sync(0xFFFFFFFFu, wait_parity(wc, &sh.s_full[grp][buf], (n / kBufs) & 1u));
+        const int buf = n % W::kBufs;
+        ok = __all_sync(0xFFFFFFFFu, wait_parity(wc, &sh.s_full[grp][buf], (n / W::kBufs) & 1u));
         if (!ok) break;
         tc_fence_after();
         const int t0 = sr.f + qt * tok, rows = min(kBN, (sr.w - qt * tok) * G);
-        const bool whole = rows == kBN && !(a.causal && j0 + (i + 1) * kBM - 1 > t0 + sr.off);
-        const int lo = a.causal && !whole ? first_row(key, sr.off, t0, G) : 0;
-        w += tile_weight(t_lane + 128u * buf, sh.nlse + qt * kBN, c2, whole, lo, rows,
+        int lo = 0, lo_first = 0, lo_last = 0;
+        if (a.causal && j0 + (i + 1) * kBM - 1 > t0 + sr.off) {
+          lo = first_row(key, sr.off, t0, G);
+          lo_first = __shfl_sync(0xFFFFFFFFu, lo, 0);
+          lo_last = __shfl_sync(0xFFFFFFFFu, lo, 31);
+        }
+        w += tile_weight(t_lane + 128u * buf, sh.nlse + qt * kBN, c2, lo, lo_first, lo_last, rows,
                          &sh.s_empty[grp][buf]);
       }
       if (real && ok) a.score_out[out0 + key] = base + w;
@@ -538,16 +573,16 @@ __global__ void __launch_bounds__(kWinThreads, QT == 1 ? 2 : 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kWinMma) {
+  if (warp == W::kMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256 * kBufs);
+    tmem_dealloc(tmem, W::kTmem);
   }
 }
 
 template <int D, int QT>
 cudaError_t launch_window(const AttnScoresArgs& a, const CUtensorMap& q_map,
                           const CUtensorMap& k_map, int num_sms, cudaStream_t stream) {
-  constexpr int kBytes = Cfg<D>::win_smem(QT);
+  constexpr int kBytes = Cfg<D>::win_smem(QT, Win<QT>::kStages);
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(
       reinterpret_cast<const void*>(attn_scores_window_kernel<D, QT>), kBytes, ready);
@@ -560,7 +595,7 @@ cudaError_t launch_window(const AttnScoresArgs& a, const CUtensorMap& q_map,
   int run = 16;
   while (run > 1 && pairs * ((key_tiles + run - 1) / run) < 2 * num_sms) run /= 2;
   const unsigned blocks = static_cast<unsigned>(pairs * ((key_tiles + run - 1) / run));
-  attn_scores_window_kernel<D, QT><<<blocks, kWinThreads, kBytes, stream>>>(a, q_map, k_map, run);
+  attn_scores_window_kernel<D, QT><<<blocks, Win<QT>::kThreads, kBytes, stream>>>(a, q_map, k_map, run);
   return cudaGetLastError();
 }
 

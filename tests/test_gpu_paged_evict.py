@@ -221,6 +221,85 @@ def test_captured_graph_on_another_stream():
         check(cache, fresh, 64, 8, (kept, new, out, k, v, table))
 
 
+def test_nothing_to_do():
+    """No sequences at all, and sequences without tokens."""
+    i32 = dict(dtype=torch.int32, device=DEV)
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    pages = torch.zeros(3, 16, 2, 64, **bf)
+    desc = q.make_paged_desc(0, 40, 3, 16, 3, 4, 2, 64)
+    none = torch.zeros(0, **i32)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device=DEV)
+    q.paged_kv_append(desc, torch.zeros(0, 2, 64, **bf), torch.zeros(0, 2, 64, **bf), none,
+                      torch.zeros(0, 3, **i32), pages, pages.clone())
+    q.paged_decode_attn(desc, torch.zeros(0, 4, 64, **bf), pages, pages, torch.zeros(0, 3, **i32), none,
+                        torch.zeros(0, 4, 64, **bf), ws, lse=torch.zeros(0, 4, device=DEV),
+                        score_out=torch.zeros(0, 2, 40, device=DEV))
+    q.attn_scores(torch.zeros(0, 4, 64, **bf), torch.zeros(0, 2, 64, **bf), torch.zeros(0, 4, device=DEV),
+                  torch.zeros(1, **i32), torch.zeros(1, **i32), torch.zeros(0, 2, 40, device=DEV), 0, 0)
+    q.paged_kv_evict(desc, 8, 2, pages, pages, torch.zeros(0, 3, **i32), none,
+                     torch.zeros(0, 2, 40, device=DEV), torch.zeros(0, 1, **i32), pages.clone(),
+                     pages.clone(), torch.zeros(0, 2, 8, **i32), torch.zeros(0, **i32), ws)
+    # prompts of no new tokens, and positions that nothing is written to
+    desc = q.make_paged_desc(2, 40, 3, 16, 3, 4, 2, 64)
+    q.paged_kv_append(desc, torch.zeros(0, 2, 64, **bf), torch.zeros(0, 2, 64, **bf),
+                      torch.zeros(2, **i32), torch.zeros(2, 3, **i32), pages, pages.clone(),
+                      new_offsets=torch.zeros(3, **i32))
+    ok()
+    assert (pages == 0).all()
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import torch, prefill_only_cascade_gb300 as q
+dev = "cuda"
+bf, i32 = torch.bfloat16, torch.int32
+k, v = (torch.randn(8, 16, 2, 128, device=dev).to(bf) for _ in range(2))
+table = torch.arange(8, dtype=i32, device=dev)[None]
+n = torch.tensor([100], dtype=i32, device=dev)
+x = torch.randn(1, 8, 128, device=dev).to(bf)
+desc = q.make_paged_desc(1, 128, 8, 16, 8, 8, 2, 128)
+out, lse = torch.zeros(1, 8, 128, dtype=bf, device=dev), torch.zeros(1, 8, device=dev)
+score = torch.zeros(1, 2, 128, device=dev)
+ws = torch.empty(q.paged_decode_workspace_size(desc, True), dtype=torch.uint8, device=dev)
+flat, off = k.view(128, 2, 128), torch.tensor([0, 100], dtype=i32, device=dev)
+q_all, l_all = torch.randn(100, 8, 128, device=dev).to(bf), torch.full((100, 8), 6.0, device=dev)
+votes = torch.zeros(1, 2, 128, device=dev)
+kd, vd = torch.zeros(2, 16, 2, 128, dtype=bf, device=dev), torch.zeros(2, 16, 2, 128, dtype=bf, device=dev)
+kept, new = torch.zeros(1, 2, 20, dtype=i32, device=dev), torch.zeros(1, dtype=i32, device=dev)
+to = torch.arange(2, dtype=i32, device=dev)[None]
+ews = torch.empty(q.paged_evict_workspace_size(desc, 2), dtype=torch.uint8, device=dev)
+torch.cuda.synchronize()
+def step():
+    q.paged_kv_append(desc, x[:, :2], x[:, 2:4], n - 1, table, k, v)
+    q.paged_decode_attn(desc, x, k, v, table, n, out, ws, lse=lse, score_out=score)
+    q.attn_scores(q_all, flat[:100], l_all, off, off, votes, 100, 100, window=16)
+    q.paged_kv_evict(desc, 20, 4, k, v, table, n, votes, to, kd, vd, kept, new, ews)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+assert q.get_device_error() == 0
+got = [t.clone() for t in (out, lse, score, votes, kept, new, kd, vd)]
+step()
+torch.cuda.synchronize()
+assert q.get_device_error() == 0
+assert all(torch.equal(a, b) for a, b in zip(got, (out, lse, score, votes, kept, new, kd, vd)))
+assert new.item() == 20 and float(out.abs().sum()) > 0
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE], cwd=root, timeout=240,
+                         capture_output=True, text=True)
+    assert run.returncode == 0 and "same" in run.stdout, run.stdout + run.stderr
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("fp8", [False, True])
 def test_prompt_then_evict_then_tokens(fp8):
