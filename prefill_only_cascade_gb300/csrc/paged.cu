@@ -134,7 +134,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 // the order sequence, head, position, and each CTA takes an equal run of them, whatever
 // the lengths are: short sequences share a CTA, long ones spread over many. A sequence's
 // head that lies inside one CTA is finished there; the others leave (max, sum, O) partials
-// that paged_finish_kernel rescales and adds.
+// that paged_finish_kernel rescales and adds. Small calls (ONE) do all of it in one launch:
+// a thread-block cluster per (sequence, head) divides its tiles, joins through distributed
+// shared memory and forms the weights.
 //
 // Each warp walks its own keys of its CTA's run with a running max and sum. Their K and V
 // rows come through a ring of its own in shared memory, filled by 16-byte asynchronous
@@ -157,6 +159,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 
+constexpr int kOneCluster = 8;                       // CTAs that share a small call's head
 constexpr int kStages = 3;                           // steps in a warp's ring
 constexpr int kStepBytes = 4096;                     // of K, and of V, in one step
 
@@ -350,45 +353,74 @@ __device__ __forceinline__ bool next_piece(const PagedDecodeArgs& a, int64_t end
   return true;
 }
 
-template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const PagedDecodeArgs a) {
+__device__ __forceinline__ void write_empty(const PagedDecodeArgs& a, int b, int n, int h0, int h1,
+                                            int D) {
+  const float nan = __int_as_float(0x7FFFFFFF);
+  if (n < 0 && threadIdx.x == 0) atomicOr(a.err_word, kErrDeviceBounds);
+  const int64_t row = static_cast<int64_t>(b) * a.hq;
+  for (int i = h0 * D + threadIdx.x; i < h1 * D; i += kDecThreads)
+    a.out[row * D + i] = __float2bfloat16(n < 0 ? nan : 0.f);
+  if (a.lse != nullptr)
+    for (int i = h0 + threadIdx.x; i < h1; i += kDecThreads) a.lse[row + i] = n < 0 ? nan : -INFINITY;
+}
+
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int D, bool FP8, int NT, bool ONE>
+__global__ void __launch_bounds__(kDecThreads, 2)
+    paged_decode_kernel(const PagedDecodeArgs a, int cluster) {
   using C = DecCfg<D, FP8>;
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ float s_m[kDecWarps][8 * NT], s_l[kDecWarps][8 * NT];
   __shared__ int s_bad[kDecWarps];
   float(*s_o)[8][D] = reinterpret_cast<float(*)[8][D]>(dyn + C::kRing);  // [warp][head][d]
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  float* s_part = reinterpret_cast<float*>(dyn);  // ONE, at the end: [head][d]
+  __shared__ float2 s_pml[ONE ? 8 * NT : 1];
+  __shared__ float s_lse2[ONE ? 8 * NT : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, q4 = lane & 3;
-  const int cta = blockIdx.x, ctas = gridDim.x;
   const int G = a.group;
-
-  // sequences without tokens (0 and -inf) and with lengths out of range (NaN)
-  for (int b = cta; b < a.num_seqs; b += ctas) {
-    const int n = checked_len(a, b);
-    if (n > 0) continue;
-    const float nan = __int_as_float(0x7FFFFFFF);
-    if (n < 0 && threadIdx.x == 0) atomicOr(a.err_word, kErrDeviceBounds);
-    for (int i = threadIdx.x; i < a.hq * D; i += kDecThreads)
-      a.out[static_cast<int64_t>(b) * a.hq * D + i] = __float2bfloat16(n < 0 ? nan : 0.f);
-    if (a.lse != nullptr)
-      for (int i = threadIdx.x; i < a.hq; i += kDecThreads)
-        a.lse[static_cast<int64_t>(b) * a.hq + i] = n < 0 ? nan : -INFINITY;
-  }
-
-  const RunStart run = find_run(a, C::kTile, cta, ctas);
-  if (threadIdx.x == 0) a.rec[cta] = DecodeRec{-1, 0, 0, 0};
-  if (run.begin >= run.end) return;
+  const int cta = ONE ? static_cast<int>(blockIdx.x) % cluster : blockIdx.x;  // ONE: the rank
+  const int ctas = gridDim.x;
   Piece cur;
-  cur.b = run.seq;
-  cur.len = checked_len(a, cur.b);
-  {
+  int64_t run_end, run_total = 0;
+  if constexpr (ONE) {
+    const int pair = static_cast<int>(blockIdx.x) / cluster;
+    cur.b = pair / a.hkv;
+    cur.g = pair % a.hkv;
+    cur.len = checked_len(a, cur.b);
+    if (cur.len <= 0) {  // the same for every CTA of the cluster
+      if (cta == 0) write_empty(a, cur.b, cur.len, cur.g * G, (cur.g + 1) * G, D);
+      return;
+    }
+    const int tiles = (cur.len + C::kTile - 1) / C::kTile;
+    cur.piece0 = 0;
+    cur.at = first_tile(cta, tiles, cluster);
+    run_end = first_tile(cta + 1, tiles, cluster);
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // sequences without tokens (0 and -inf) and with lengths out of range (NaN)
+    for (int b = cta; b < a.num_seqs; b += ctas) {
+      const int n = checked_len(a, b);
+      if (n <= 0) write_empty(a, b, n, 0, a.hq, D);
+    }
+    const RunStart run = find_run(a, C::kTile, cta, ctas);
+    if (threadIdx.x == 0) a.rec[cta] = DecodeRec{-1, 0, 0, 0};
+    if (run.begin >= run.end) return;
+    cur.b = run.seq;
+    cur.len = checked_len(a, cur.b);
     const int tiles = (cur.len + C::kTile - 1) / C::kTile;
     cur.g = static_cast<int>((run.begin - run.seq_tile0) / tiles);
     cur.piece0 = run.seq_tile0 + static_cast<int64_t>(cur.g) * tiles;
+    cur.at = run.begin;
+    run_end = run.end;
+    run_total = run.total;
   }
-  cur.at = run.begin;
-  set_piece<C::kTile>(a, run.end, cur);
+  set_piece<C::kTile>(a, run_end, cur);
 
   // ------------------------------------------------------ loads: a cursor of their own
   const int64_t row_stride = static_cast<int64_t>(a.hkv) * C::kRB;
@@ -400,7 +432,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
   uint32_t bad_steps = 0;                // bit s: a page of the step in stage s is no page
   auto seek = [&]() {                    // on to a piece that has a step for this warp
     while (ld_more && ld_key >= ld.ke) {
-      ld_more = next_piece<C::kTile>(a, run.end, ld);
+      ld_more = next_piece<C::kTile>(a, run_end, ld);
       ld_key = ld.kb + warp * C::kKeys;
     }
     if (ld_more) {
@@ -680,7 +712,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
 
     // the next piece's queries are on their way while this one is put together
     Piece nxt = cur;
-    const bool more = next_piece<C::kTile>(a, run.end, nxt);
+    const bool more = !ONE && next_piece<C::kTile>(a, run_end, nxt);
     if (more) load_q(nxt.b, nxt.g);
 
     // ---------------------------------------------------- the four warps' parts together
@@ -719,7 +751,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
         }
         if (any_bad) sum = __int_as_float(0x7FFFFFFF);
         const int64_t row = static_cast<int64_t>(cur.b) * a.hq + cur.g * G + hh;
-        if (cur.whole) {
+        if constexpr (ONE) {  // over the ring: every warp has used its last step
+          s_part[hh * D + d] = acc;
+          if (d == 0) s_pml[hh] = make_float2(top, sum);
+        } else if (cur.whole) {
           a.out[row * D + d] = __float2bfloat16(acc / sum * vs);
           if (d == 0) {
             const float lse2 = top + (log2f(sum) - (FP8 ? 14.f : 0.f));
@@ -733,19 +768,78 @@ __global__ void __launch_bounds__(kDecThreads, 2) paged_decode_kernel(const Page
       }
       if (n == 0 && threadIdx.x == 0) {
         if (any_bad) atomicOr(a.err_word, kErrDeviceBounds);
-        if (a.begun != nullptr && cur.at == cur.piece0)
+        if (!ONE && a.begun != nullptr && cur.at == cur.piece0)
           a.begun[static_cast<int64_t>(cur.b) * a.hkv + cur.g] = cur.whole ? -1 : cta;
-        if (!cur.whole && cur.at == cur.piece0) {  // goes on in the next CTAs: the join's entry
+        if (!ONE && !cur.whole && cur.at == cur.piece0) {  // goes on in the next CTAs: the join's entry
           const int64_t end = cur.piece0 + (cur.len + C::kTile - 1) / C::kTile;
           // the last CTA of (b, g) is the one that holds tile end - 1
-          a.rec[cta] = DecodeRec{cur.b, cur.g, static_cast<int>((end * ctas - 1) / run.total),
-                                 run.total < ctas ? static_cast<int>(run.total) : 0};
+          a.rec[cta] = DecodeRec{cur.b, cur.g, static_cast<int>((end * ctas - 1) / run_total),
+                                 run_total < ctas ? static_cast<int>(run_total) : 0};
         }
       }
       __syncthreads();  // the shared parts may be overwritten
     }
+    if constexpr (ONE) break;
     if (!more) break;
     cur = nxt;
+  }
+
+  if constexpr (ONE) {
+    // ---------------------------------------------------- the cluster's parts together
+    constexpr float kShift = FP8 ? 14.f : 0.f;
+    if (cluster > 1) cluster_sync(); else __syncthreads();
+    const float vs = FP8 ? __ldg(a.v_scale + static_cast<int64_t>(cur.b) * a.hkv + cur.g) : 1.f;
+    const int64_t row0 = static_cast<int64_t>(cur.b) * a.hq + cur.g * G;
+    for (int h = cta; h < G; h += cluster) {
+      float2 ml[kOneCluster];
+      float x[kOneCluster];
+      const int d = threadIdx.x;
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kOneCluster; ++c) {
+        ml[c] = make_float2(-INFINITY, 0.f);
+        x[c] = 0.f;
+        if (c < cluster) {
+          ml[c] = ld_cluster_f32x2(cluster_map(&s_pml[h], c));
+          if (d < D) x[c] = ld_cluster_f32(cluster_map(&s_part[h * D + d], c));
+          top = fmaxf(top, ml[c].x);
+        }
+      }
+      float sum = 0.f, acc = 0.f;
+#pragma unroll
+      for (int c = 0; c < kOneCluster; ++c) {
+        const float f = ml[c].x == -INFINITY ? 0.f : ex2(ml[c].x - top);
+        sum = fmaf(ml[c].y, f, sum);
+        acc = fmaf(x[c], f, acc);
+      }
+      if (d < D) a.out[(row0 + h) * D + d] = __float2bfloat16(acc / sum * vs);
+      if (d == 0 && a.lse != nullptr)
+        a.lse[row0 + h] = (top + (log2f(sum) - kShift)) * 0.6931471805599453f;
+    }
+    if (a.raw != nullptr) {
+      if (threadIdx.x < G) {
+        float top = -INFINITY, sum = 0.f;
+        for (int c = 0; c < cluster; ++c)
+          top = fmaxf(top, ld_cluster_f32x2(cluster_map(&s_pml[threadIdx.x], c)).x);
+        for (int c = 0; c < cluster; ++c) {
+          const float2 ml = ld_cluster_f32x2(cluster_map(&s_pml[threadIdx.x], c));
+          sum = fmaf(ml.y, ml.x == -INFINITY ? 0.f : ex2(ml.x - top), sum);
+        }
+        s_lse2[threadIdx.x] = top + (log2f(sum) - kShift);
+      }
+      __syncthreads();
+      const int64_t out_row = (static_cast<int64_t>(cur.b) * a.hkv + cur.g) * a.score_stride;
+      for (int j = cur.kb + threadIdx.x; j < cur.ke; j += kDecThreads) {  // this CTA's own keys
+        float w = 0.f;
+        for (int h = 0; h < G; ++h) {
+          const float lse2 = s_lse2[h];
+          const float x = a.raw[(row0 + h) * a.raw_stride + j];
+          if (lse2 > -INFINITY) w += ex2(x - lse2);
+        }
+        a.score_out[out_row + j] = (a.score_in != nullptr ? a.score_in[out_row + j] : 0.f) + w;
+      }
+    }
+    if (cluster > 1) cluster_sync();  // no CTA leaves while others read its part
   }
 }
 
@@ -991,12 +1085,40 @@ __global__ void __launch_bounds__(kFinishThreads, 4)
 template <int D, bool FP8, int NT>
 cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
   using C = DecCfg<D, FP8>;
+  cudaError_t e;
+  // One launch where clusters of up to eight CTAs, four tiles each at most, all fit the GPU
+  // at once: a launch less is worth more there than an even division. Measured against the
+  // two launches: 5.9 us and 7.4 (one sequence of 777 tokens, 8 KV heads), 6.9 and 7.9 (four
+  // of 64-600 tokens, d = 64, with weights).
+  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
+  const int tiles = (a.max_len + C::kTile - 1) / C::kTile;
+  int cluster = 1;
+  while (cluster < kOneCluster && cluster < tiles) cluster *= 2;
+  if (tiles <= 4 * cluster && pairs * cluster <= 2 * num_sms) {
+    static std::atomic<uint64_t> one_ready{0};
+    e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT, true>), C::kSmem,
+                   one_ready);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute dims;
+    dims.id = cudaLaunchAttributeClusterDimension;
+    dims.val.clusterDim.x = cluster;
+    dims.val.clusterDim.y = 1;
+    dims.val.clusterDim.z = 1;
+    cudaLaunchConfig_t one{};
+    one.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
+    one.blockDim = dim3(kDecThreads);
+    one.dynamicSmemBytes = C::kSmem;
+    one.stream = stream;
+    one.attrs = &dims;
+    one.numAttrs = 1;
+    return cudaLaunchKernelEx(&one, paged_decode_kernel<D, FP8, NT, true>, a, cluster);
+  }
   const int ctas = decode_ctas(num_sms, a.num_seqs, a.hkv, a.max_len, C::kTile);
   static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT>),
-                             C::kSmem, ready);
+  e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT, false>), C::kSmem,
+                 ready);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D, FP8, NT><<<ctas, kDecThreads, C::kSmem, stream>>>(a);
+  paged_decode_kernel<D, FP8, NT, false><<<ctas, kDecThreads, C::kSmem, stream>>>(a, 1);
   e = cudaGetLastError();
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
