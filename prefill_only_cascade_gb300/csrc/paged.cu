@@ -1086,15 +1086,16 @@ template <int D, bool FP8, int NT>
 cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
   using C = DecCfg<D, FP8>;
   cudaError_t e;
-  // One launch where clusters of up to eight CTAs, four tiles each at most, all fit the GPU
-  // at once: a launch less is worth more there than an even division. Measured against the
-  // two launches: 5.9 us and 7.4 (one sequence of 777 tokens, 8 KV heads), 6.9 and 7.9 (four
-  // of 64-600 tokens, d = 64, with weights).
+  // One launch where clusters of up to eight CTAs, eight tiles each at most, all fit the GPU
+  // at once: there a launch less is worth more than an even division. Measured against the
+  // divided runs (8 KV heads, d = 128): one sequence of 777 tokens 5.9 us and 7.4, four of
+  // 2,000 8.9 and 12.8, four of 4,000 15.5 and 20.0, four of 1,000-4,000 with weights 15.2 and
+  // 13.9; past the rule, one of 8,000 14.9 and 12.4, sixteen of 2,000 38 and 30.
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
   const int tiles = (a.max_len + C::kTile - 1) / C::kTile;
   int cluster = 1;
   while (cluster < kOneCluster && cluster < tiles) cluster *= 2;
-  if (tiles <= 4 * cluster && pairs * cluster <= 2 * num_sms) {
+  if (tiles <= 8 * cluster && pairs * cluster <= 2 * num_sms) {
     static std::atomic<uint64_t> one_ready{0};
     e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT, true>), C::kSmem,
                    one_ready);
