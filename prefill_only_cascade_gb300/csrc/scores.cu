@@ -12,9 +12,11 @@
 //   attn_scores_kernel   a CTA keeps 256 keys of a (sequence, KV head) in shared memory and
 //     streams 128-row query tiles (128 / G tokens x G heads, as one TMA box) past them. Per
 //     tile and SM the MMA (2 x ~512 clk) and the exponentials (2 x 512 clk of the MUFU) are
-//     about equal, and both bound it: 16 softmax warps (four warpgroups, one per key tile and
-//     parity of the query tile, each with its own S^T in TMEM) keep the MUFU fed while the
-//     tensor cores fill the other parity. 256 keys and not 128, so that a query tile is read
+//     about equal: 16 softmax warps (four warpgroups, one per key tile and parity of the query
+//     tile, each with its own S^T in TMEM) exponentiate while the tensor cores fill the other
+//     parity. What bounds it is the hand-over MMA -> softmax -> MMA of each S^T tile, whose
+//     latency four tiles in TMEM do not hide (about 1,700 clk per two products instead of
+//     1,030): hence an MMA warp per key tile and a warp of its own for the lse. 256 keys and not 128, so that a query tile is read
 //     from L2 once per two products (~9 TB/s at full rate instead of 18).
 //   attn_scores_window_kernel   where the queries of a (sequence, KV head) fit four tiles (the
 //     last 128 tokens at G = 4), they stay in shared memory and the keys stream past them, a
@@ -39,8 +41,8 @@ constexpr int kMaxCluster = 8;
 // attn_scores_kernel
 constexpr int kKeyTiles = 2;        // key tiles of a CTA
 constexpr int kGroups = 2 * kKeyTiles;  // softmax warpgroups: (key tile, query tile parity)
-constexpr int kThreads = 128 * kGroups + 64;  // + the TMA warp and the MMA warp
-constexpr int kWarpLoad = 4 * kGroups, kWarpMma = 4 * kGroups + 1;
+constexpr int kThreads = 128 * kGroups + 128;  // + TMA, an MMA warp per key tile, lse
+constexpr int kWarpLoad = 4 * kGroups, kWarpMma = 4 * kGroups + 1, kWarpLse = 4 * kGroups + 3;
 constexpr int kQStages = 4;
 
 // attn_scores_window_kernel
@@ -69,11 +71,11 @@ struct Cfg {
 };
 
 struct Shared {
-  alignas(16) float nlse[kGroups][2][kBN];  // -lse * log2(e) of a tile's query rows
+  alignas(16) float nlse[kQStages][kBN];    // -lse * log2(e) of a tile's query rows
   alignas(16) float part[kMaxCluster][kKeyTiles * kBM];  // others' sums: rank 0's own odd
                                             // tiles in row 0, the cluster's CTAs behind
-  uint64_t k_full, drain;
-  uint64_t q_full[kQStages], q_empty[kQStages];
+  uint64_t k_full, drain[kKeyTiles];
+  uint64_t q_full[kQStages], q_empty[kQStages], l_full[kQStages], l_empty[kQStages];
   uint64_t s_full[kGroups], s_empty[kGroups];
   uint32_t tmem;
   int abort_flag;
@@ -268,10 +270,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (threadIdx.x == 32 * kWarpLoad) {
     mbar_init(&sh.k_full, 1);
-    mbar_init(&sh.drain, 1);
+    for (int i = 0; i < kKeyTiles; ++i) mbar_init(&sh.drain[i], 1);
     for (int i = 0; i < kQStages; ++i) {
       mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.q_empty[i], kKeyTiles);  // both MMA warps
+      mbar_init(&sh.l_full[i], 32);
+      mbar_init(&sh.l_empty[i], 4 * kKeyTiles);  // the warps that read it
     }
     for (int i = 0; i < kGroups; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -316,25 +320,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = armed > kQStages ? armed - kQStages : 0; i < armed; ++i)
         drain(&sh.q_full[i % kQStages], (i / kQStages) & 1u, deadline);
     }
-  } else if (warp == kWarpMma) {
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
     if (mine > 0) {
+      const int kt = warp - kWarpMma;  // each issues the products of one key tile
       const bool leader = elect_one();
       const uint32_t k_lo = sw128_desc_lo(smem_u32(s_k), 16);
       const uint32_t q_lo = sw128_desc_lo(smem_u32(s_q), 16);
-      uint32_t used[kGroups] = {0, 0, 0, 0};
+      const int from = kt == 0 ? t_first[0] : t_first[1];
+      uint32_t used[2] = {0, 0};
       bool ok = wait_parity_warp(wc, &sh.k_full, 0);
       for (int i = 0; i < mine && ok; ++i) {
         const int st = i % kQStages;
         ok = wait_parity_warp(wc, &sh.q_full[st], (i / kQStages) & 1u);
-#pragma unroll
-        for (int kt = 0; kt < kKeyTiles; ++kt) {
-          if (!ok || tile_at(i) < t_first[kt]) continue;
+        if (!ok) break;
+        if (tile_at(i) >= from) {
           const int grp = 2 * kt + (i & 1);
-          // the group's last tile is in its registers
-          const uint32_t parity = (kt == 0 ? ((i & 1) ? used[1] : used[0])
-                                           : ((i & 1) ? used[3] : used[2])) & 1u;
+          const uint32_t parity = ((i & 1) ? used[1] : used[0]) & 1u;
           ok = wait_parity_warp(wc, &sh.s_empty[grp], parity ^ 1u);
-          if (!ok) continue;
+          if (!ok) break;
           tc_fence_after();
           if (leader) {
             mma_tile<D>(tmem + 128u * grp, k_lo + kt * (C::kTileBytes >> 4),
@@ -342,19 +345,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&sh.s_full[grp]);
           }
           __syncwarp();
-          if (kt == 0) {
-            if (i & 1) ++used[1]; else ++used[0];
-          } else {
-            if (i & 1) ++used[3]; else ++used[2];
-          }
+          if (i & 1) ++used[1]; else ++used[0];
         }
-        if (!ok) break;
         if (leader) mma_commit(&sh.q_empty[st]);
         __syncwarp();
       }
-      if (leader) mma_commit(&sh.drain);
+      if (leader) mma_commit(&sh.drain[kt]);
       __syncwarp();
-      drain(&sh.drain, 0, global_timer_ns() + 100000000ull);
+      drain(&sh.drain[kt], 0, global_timer_ns() + 100000000ull);
+    }
+  } else if (warp == kWarpLse) {
+    // -lse log2(e) of every tile's query rows, four tiles ahead. G divides 128, so the rows
+    // lane + 32 j of a tile are tokens and heads at fixed places of it.
+    const int lane = threadIdx.x & 31;
+    int dt[4];
+    const float* at[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      dt[j] = (lane + 32 * j) / G;
+      at[j] = a.lse + (sr.q0 + sr.f + dt[j]) * a.hq + g * G + (lane + 32 * j) % G;
+    }
+    const int64_t per_token = a.hq;
+    float l[4][4];
+    auto load = [&](int i, float (&x)[4]) {
+      const int t = tile_at(i) * tok, left = i < mine ? sr.w - t : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = dt[j] < left ? __ldg(at[j] + t * per_token) : 0.f;
+    };
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load(k, l[k]);
+    bool ok = true;
+    for (int i0 = 0; i0 < mine && ok; i0 += 4) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k, st = i % kQStages;
+        if (i >= mine || !ok) break;
+        ok = wait_parity_warp(wc, &sh.l_empty[st], ((i / kQStages) & 1) ^ 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // a row that saw nothing (-inf) gives no weight
+          sh.nlse[st][lane + 32 * j] =
+              l[k][j] == -INFINITY ? -INFINITY : l[k][j] * -1.4426950408889634f;
+        mbar_arrive(&sh.l_full[st]);
+        load(i + 4, l[k]);
+      }
     }
   } else {
     const int grp = warp >> 2, kt = grp >> 1;
@@ -362,39 +396,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key = j0 + kt * kBM + row;
     const uint32_t t_tile = tmem + 128u * grp + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
+    const int from = kt == 0 ? t_first[0] : t_first[1];
     float lost = 0.f;                   // what the running sum has rounded away
-    bool ok = true;
-    // lse of this thread's query row of the i-th tile, loaded a tile ahead
-    auto row_lse = [&](int i) {
-      const int t = sr.f + tile_at(i) * tok + row / G;
-      return i < mine && t < sr.nq ? __ldg(a.lse + (sr.q0 + t) * a.hq + g * G + row % G) : 0.f;
-    };
-    int i = grp & 1;
-    while (i < mine && tile_at(i) < t_first[kt]) i += 2;
-    float l = row_lse(i);
-    for (uint32_t n = 0; i < mine; i += 2, ++n) {
-      float* nlse = sh.nlse[grp][n & 1];
-      // a row that saw nothing (-inf) gives no weight
-      nlse[row] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
-      asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
-      l = row_lse(i + 2);
-      // after a wait that ran out every warp still takes part in the barriers
-      ok = ok && __all_sync(0xFFFFFFFFu, wait_parity(wc, &sh.s_full[grp], n & 1u));
-      if (!ok) continue;
-      tc_fence_after();
-      const int t0 = sr.f + tile_at(i) * tok;
-      const int hi = sr.nq - t0 >= tok ? kBN : (sr.nq - t0) * G;
-      int lo = 0, lo_first = 0, lo_last = 0;
-      if (a.causal && j0 + (kt + 1) * kBM - 1 > t0 + sr.off) {
-        lo = first_row(key, sr.off, t0, G);
-        lo_first = __shfl_sync(0xFFFFFFFFu, lo, 0);
-        lo_last = __shfl_sync(0xFFFFFFFFu, lo, 31);
+    uint32_t n = 0;                     // S^T tiles of this group so far
+    for (int i = grp & 1; i < mine; i += 2) {
+      const int st = i % kQStages;
+      // also where it sees no key: one release of a stage per tile, in the tiles' order
+      bool ok = wait_parity_warp(wc, &sh.l_full[st], (i / kQStages) & 1u);
+      if (!ok) break;
+      if (tile_at(i) >= from) {
+        ok = wait_parity_warp(wc, &sh.s_full[grp], n & 1u);
+        if (!ok) break;
+        ++n;
+        tc_fence_after();
+        const int t0 = sr.f + tile_at(i) * tok;
+        const int hi = sr.nq - t0 >= tok ? kBN : (sr.nq - t0) * G;
+        int lo = 0, lo_first = 0, lo_last = 0;
+        if (a.causal && j0 + (kt + 1) * kBM - 1 > t0 + sr.off) {
+          lo = first_row(key, sr.off, t0, G);
+          lo_first = __shfl_sync(0xFFFFFFFFu, lo, 0);
+          lo_last = __shfl_sync(0xFFFFFFFFu, lo, 31);
+        }
+        // compensated: thousands of tiles may add up (Kahan)
+        const float y =
+            tile_weight(t_tile, sh.nlse[st], c2, lo, lo_first, lo_last, hi, &sh.s_empty[grp]) - lost;
+        const float sum = total + y;
+        lost = fabsf(sum) < INFINITY ? (sum - total) - y : 0.f;
+        total = sum;
       }
-      // compensated: thousands of tiles may add up (Kahan)
-      const float y = tile_weight(t_tile, nlse, c2, lo, lo_first, lo_last, hi, &sh.s_empty[grp]) - lost;
-      const float sum = total + y;
-      lost = fabsf(sum) < INFINITY ? (sum - total) - y : 0.f;
-      total = sum;
+      __syncwarp();  // the warp has read nlse
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.l_empty[st]);
     }
     if (grp & 1) sh.part[0][kt * kBM + row] = total;
   }

@@ -96,6 +96,22 @@ def test_causal_with_other_lengths(nq, nk):
     check(score, qs, ks, lse, nq, nk, scale, True, 0)
 
 
+@pytest.mark.parametrize("window", [20, 40, 100])
+def test_long_runs_of_key_tiles(window):
+    """Many sequences: a CTA takes up to 16 key tiles of one, with one, two or four query tiles."""
+    nk = [2100, 1] + [2049 + 3 * i for i in range(38)]
+    scale = 1 / math.sqrt(64)
+    gen = torch.Generator().manual_seed(12)
+    qs = torch.randn(sum(nk), 16, 64, generator=gen).bfloat16()
+    ks = torch.randn(sum(nk), 4, 64, generator=gen).bfloat16()
+    lse = 7 + torch.rand(sum(nk), 16, generator=gen)     # as good as any
+    score = torch.full((len(nk), 4, max(nk) + 3), -3.0, device=DEV)
+    q.attn_scores(qs.to(DEV), ks.to(DEV), lse.to(DEV), offsets(nk), offsets(nk), score, max(nk),
+                  max(nk), window=window)
+    ok()
+    check(score, qs, ks, lse, nk, nk, scale, True, window)
+
+
 def test_few_keys_many_queries():
     """Query tiles split over a cluster; the same bits every time."""
     nq, nk, scale = [5000, 1], [100, 40], 1 / math.sqrt(128)
