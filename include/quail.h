@@ -504,8 +504,8 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
  *            page count) or one that does not overlap it. Each destination page belongs to
  *            one sequence and is none that a sequence of the call holds; rows for pages
  *            that break this are not written and new_lens[b] becomes -1, as it does for a
- *            source page outside the pool and for a length out of range (all with
- *            QUAIL_ERR_DEVICE_BOUNDS).
+ *            length out of range and for a source page outside the pool (at least where a
+ *            kept token lies in it); all with QUAIL_ERR_DEVICE_BOUNDS.
  *   kept [B, Hkv, budget] int32 out: the kept positions in increasing order, then -1
  *   new_lens [B] int32 out, not overlapping seq_lens
  *   score_out [B, Hkv, score_out_stride] fp32 out or NULL, score_out_stride >= budget, not

@@ -12,6 +12,8 @@
 //    Bound by latency: about ten barriers and dependent steps of a microsecond or less.
 // 2. evict_copy_kernel    moves the kept rows: a block looks up the places of 256 (token,
 //    head) rows first, then moves them, 16 bytes a thread and eight in flight.
+// Small calls do both in one launch (FUSED): a CTA per (sequence, KV head) that compares its
+// destination pages with every other page of the call itself, and moves what it keeps.
 #include <cstdint>
 
 #include "kernels.h"
@@ -82,7 +84,10 @@ __device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
 // kSelThreads * KPT (one, unless the part is longer: then the scores are read again in every
 // pass); in a round each warp has a contiguous run, lane by lane, so that the order of the
 // tokens is (round, warp, i, lane).
-template <int KPT, bool SHARED>
+constexpr int kSmallKeys = 4 * kSelThreads;   // FUSED: tokens of a sequence at most
+constexpr int kSmallKept = 512;               // kept ones at most
+constexpr int kSmallPages = kSmallKept / 16;  // their pages at most
+template <int KPT, bool SHARED, bool FUSED>
 __global__ void __launch_bounds__(kSelThreads, 2)
     evict_select_kernel(const PagedEvictArgs a, int cluster) {
   // Scores of one octave share few first digits, so lanes often add to the same bin: four
@@ -93,7 +98,9 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   __shared__ uint32_t s_found[3];       // digit, how many are above it, how many have it
   __shared__ __align__(16) uint32_t s_count[4];  // this CTA's keys above / at the threshold
   __shared__ uint32_t s_gt[kSelWarps], s_eq[kSelWarps];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int s_kept[FUSED ? kSmallKept : 1];
+  __shared__ int s_to[FUSED ? kSmallPages : 1], s_bad[FUSED ? kSmallPages + 1 : 1];
+  if (!FUSED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int pair = blockIdx.x / cluster;
   const int b = pair / a.hkv, g = pair % a.hkv;
@@ -111,7 +118,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   constexpr int kRound = kSelThreads * KPT;
   const int rounds = (per + kRound - 1) / kRound;
   extern __shared__ uint32_t s_keys[];  // SHARED: [KPT][kSelThreads], each thread its own
-  [[maybe_unused]] uint32_t reg[SHARED ? 1 : KPT];
+  uint32_t reg[SHARED ? 1 : KPT] = {};
   auto key = [&](int i) {               // 0: none (every score's key is larger)
     return SHARED ? s_keys[i * kSelThreads + threadIdx.x] : reg[SHARED ? 0 : i];
   };
@@ -147,7 +154,37 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   float* score_out =
       a.score_out != nullptr ? a.score_out + static_cast<int64_t>(pair) * a.score_out_stride : nullptr;
   const int tid = rank * kSelThreads + threadIdx.x, threads = cluster * kSelThreads;
-  if (g == 0) {  // the sequence's pages and its new length, once
+  if constexpr (FUSED) {
+    const int mine = pages_of(a, fresh);
+    for (int j = threadIdx.x; j <= mine; j += kSelThreads) {
+      const int p = j < mine ? __ldg(a.dst_table + b * a.dst_max_pages + j) : 0;
+      if (j < mine) s_to[j] = p;
+      s_bad[j] = j < mine && (p < 0 || p >= a.dst_num_pages);  // the last: the source pages
+    }
+    __syncthreads();
+    auto meet = [&](int p, int entry) {  // page p is claimed (entry of dst_table) or held (-1)
+      for (int j = 0; j < mine; ++j)
+        if (s_to[j] == p && b * a.dst_max_pages + j != entry) s_bad[j] = 1;
+    };
+    const int claims = pages_of(a, min(a.budget, a.max_len));
+    for (int e = threadIdx.x; e < a.num_seqs * claims; e += kSelThreads) {
+      const int seq = e / claims, j = e % claims, len = evict_len(a, seq);
+      if (j < pages_of(a, min(len, a.budget)))
+        meet(__ldg(a.dst_table + seq * a.dst_max_pages + j), seq * a.dst_max_pages + j);
+    }
+    if (a.same_pool) {
+      const int held = pages_of(a, a.max_len);
+      for (int e = threadIdx.x; e < a.num_seqs * held; e += kSelThreads) {
+        const int seq = e / held, j = e % held;
+        if (j < pages_of(a, evict_len(a, seq))) meet(__ldg(a.table + seq * a.max_pages + j), -1);
+      }
+    }
+    if (g == 0)
+      for (int j = threadIdx.x; j < pages_of(a, n); j += kSelThreads) {
+        const int p = __ldg(a.table + b * a.max_pages + j);
+        if (p < 0 || p >= a.num_pages) s_bad[mine] = 1;
+      }
+  } else if (g == 0) {  // the sequence's pages and its new length, once
     if (tid == 0) {
       a.new_lens[b] = n < 0 ? -1 : fresh;
       if (n < 0) atomicOr(a.err_word, kErrDeviceBounds);
@@ -173,12 +210,14 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   // the recent tokens, and what follows the last kept one
   for (int i = tid; i < recent; i += threads) {
     kept[k + i] = elig + i;
+    if (FUSED) s_kept[k + i] = elig + i;
     if (score_out != nullptr) score_out[k + i] = __ldg(score + elig + i);
   }
   for (int i = fresh + tid; i < a.budget; i += threads) kept[i] = -1;
   if (score_out != nullptr)
     for (int64_t i = fresh + tid; i < a.score_out_stride; i += threads) score_out[i] = 0.f;
-  if (k == 0) return;  // the same for every CTA of the cluster
+  if (!FUSED && k == 0) return;  // the same for every CTA of the cluster
+  if (k > 0) {
 
   // keys above the threshold stay, and `need` of those at it; k >= elig: every key
   uint32_t threshold = 0, need = 0;
@@ -341,6 +380,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       if (at >= static_cast<uint32_t>(k)) return;  // only if the scores change meanwhile
       const int pos = e0 + w0 + 32 * i + lane;
       kept[at] = pos;
+      if (FUSED) s_kept[at] = pos;
       // the key gives the score back, but for the values that share one
       if (score_out != nullptr)
         score_out[at] = u == kKeyZero || u == kKeyLowest ? __ldg(score + pos) : key_score(u);
@@ -370,6 +410,39 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     }
   }
   if (cluster > 1) cluster_sync();  // no CTA leaves while others read its counts
+  }
+
+  if constexpr (FUSED) {
+    __syncthreads();
+    const int mine = pages_of(a, fresh);
+    if (g == 0 && threadIdx.x < 32) {
+      bool bad = n < 0;
+      for (int j = lane; j <= mine; j += 32) bad |= s_bad[j] != 0;
+      bad = __any_sync(0xFFFFFFFFu, bad);
+      if (lane == 0) {
+        a.new_lens[b] = bad ? -1 : fresh;
+        if (bad) atomicOr(a.err_word, kErrDeviceBounds);
+      }
+    }
+    const int shift = a.row_bytes == 256 ? 4 : a.row_bytes == 128 ? 3 : 2;  // 16-byte pieces a row
+    const int mask = (1 << a.page_shift) - 1;
+#pragma unroll 4
+    for (int u = threadIdx.x; u < fresh << shift; u += kSelThreads) {
+      const int i = u >> shift, c = u & ((1 << shift) - 1), pos = s_kept[i];
+      if (pos < 0 || pos >= n) continue;  // only if the scores changed meanwhile
+      const int from = __ldg(a.table + b * a.max_pages + (pos >> a.page_shift));
+      if (s_bad[i >> a.page_shift] || from < 0 || from >= a.num_pages) continue;
+      const int64_t src =
+          (((static_cast<int64_t>(from) << a.page_shift) + (pos & mask)) * a.hkv + g) * a.row_bytes +
+          16 * c;
+      const int64_t dst = (((static_cast<int64_t>(s_to[i >> a.page_shift]) << a.page_shift) +
+                            (i & mask)) * a.hkv + g) * a.row_bytes + 16 * c;
+      const uint4 x = *reinterpret_cast<const uint4*>(a.k_pages + src);
+      const uint4 y = *reinterpret_cast<const uint4*>(a.v_pages + src);
+      *reinterpret_cast<uint4*>(a.k_dst + dst) = x;
+      *reinterpret_cast<uint4*>(a.v_dst + dst) = y;
+    }
+  }
 }
 
 constexpr int kCopyThreads = 256;
@@ -446,10 +519,18 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const Paged
 }  // namespace
 
 cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_t stream) {
+  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
+  const int page = 1 << a.page_shift;
+  const int most = a.budget < a.max_len ? a.budget : a.max_len;
+  const int64_t own = (most + page - 1) / page;
+  const int64_t others = a.num_seqs * (own + (a.same_pool ? (a.max_len + page - 1) / page : 0));
+  if (a.max_len <= kSmallKeys && most <= kSmallKept && own * others <= 65536) {
+    evict_select_kernel<4, false, true><<<static_cast<unsigned>(pairs), kSelThreads, 0, stream>>>(a, 1);
+    return cudaGetLastError();
+  }
   cudaError_t e = cudaSuccess;
   // CTAs per (sequence, head): enough to hold the keys, and more while SMs are idle and a
   // CTA has thousands of keys
-  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
   int cluster = 1;
   while (cluster < kMaxCluster &&
          (a.max_len > static_cast<int64_t>(kSelThreads) * kMaxKeys * cluster ||
@@ -468,16 +549,16 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
   cfg.blockDim = dim3(kSelThreads);
   if (per <= 4 * kSelThreads) {
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<4, false>, a, cluster);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<4, false, false>, a, cluster);
   } else if (per <= 16 * kSelThreads) {
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<16, false>, a, cluster);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<16, false, false>, a, cluster);
   } else {
     constexpr int kBytes = kSelThreads * kMaxKeys * 4;
     static std::atomic<uint64_t> ready{0};
-    e = allow_smem(reinterpret_cast<const void*>(evict_select_kernel<kMaxKeys, true>), kBytes, ready);
+    e = allow_smem(reinterpret_cast<const void*>(evict_select_kernel<kMaxKeys, true, false>), kBytes, ready);
     if (e != cudaSuccess) return e;
     cfg.dynamicSmemBytes = kBytes;
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<kMaxKeys, true>, a, cluster);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<kMaxKeys, true, false>, a, cluster);
     cfg.dynamicSmemBytes = 0;
   }
   if (e != cudaSuccess) return e;

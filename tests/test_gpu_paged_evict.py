@@ -20,6 +20,8 @@ CASES = {
     "one_recent": ([1, 2, 700], 1, 1),
     "under_budget": ([5, 60, 64], 64, 3),
     "empty": ([0, 0], 16, 4),
+    "larger": ([512, 511, 513, 2048, 2000], 512, 100),
+    "past_one_launch": ([600, 2048], 513, 100),
 }
 
 
@@ -105,14 +107,16 @@ def check(cache, score, budget, recent, got, only=None):
                 np.testing.assert_array_equal(y[z, g], x[a, g])
 
 
+@pytest.mark.parametrize("most", [0, 3000])    # (0: the longest; see below)
 @pytest.mark.parametrize("name", list(CASES))
 @pytest.mark.parametrize("kind", ["heavy", "ties", "equal", "special"])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_cases(name, kind, fp8):
+def test_cases(name, kind, fp8, most):
     lens, budget, recent = CASES[name]
-    cache = Cache(lens, 2, 64 if fp8 else 128, 16, fp8, seed=3)
-    score = scores_for(lens, 2, max(max(lens), 1) + 2, kind)
-    got = run(cache, score, budget, recent, score_stride=budget + 7)
+    most = most or max(lens)
+    cache = Cache(lens, 2, 64 if fp8 else 128, 16, fp8, seed=3, width=max(1, -(-most // 16)))
+    score = scores_for(lens, 2, max(most, 1) + 2, kind)
+    got = run(cache, score, budget, recent, score_stride=budget + 7, max_len=most)
     ok()
     check(cache, score, budget, recent, got)
 
@@ -133,27 +137,32 @@ def test_long(lens, budget, recent, hkv, kind):
     check(cache, score, budget, recent, got)
 
 
-def test_same_pool_and_shared_source_pages():
-    cache = Cache([200, 200, 90], 2, 128, 16, False)
+# max_seq_len 200: one launch; 3,000: select and copy are two
+@pytest.mark.parametrize("most", [200, 3000])
+def test_same_pool_and_shared_source_pages(most):
+    cache = Cache([200, 200, 90], 2, 128, 16, False, width=-(-most // 16))
     cache.table_np[1, :6] = cache.table_np[0, :6]       # a shared prefix
     cache.table.copy_(torch.from_numpy(cache.table_np))
-    score = scores_for(cache.lens, 2, 200, "normal")
-    got = run(cache, score, 64, 8, dst="same")
+    score = scores_for(cache.lens, 2, most, "normal")
+    got = run(cache, score, 64, 8, dst="same", max_len=most)
     ok()
     check(cache, score, 64, 8, got)
 
 
-@pytest.mark.parametrize("where", ["twice", "held", "outside"])
-def test_destination_pages_that_break_the_rules(where):
+@pytest.mark.parametrize("most", [200, 3000])
+@pytest.mark.parametrize("where", ["twice", "itself", "held", "outside"])
+def test_destination_pages_that_break_the_rules(where, most):
     """The sequences concerned end with -1 and nothing written there; the others are right."""
-    cache = Cache([200, 150, 90], 2, 128, 16, False)
-    score = scores_for(cache.lens, 2, 200, "normal")
+    cache = Cache([200, 150, 90], 2, 128, 16, False, width=-(-most // 16))
+    score = scores_for(cache.lens, 2, most, "normal")
     held = int(cache.table_np[2, 1])
 
     def spoil(table):
         table = table.copy()
         if where == "twice":
             table[0, 2] = table[1, 3]
+        elif where == "itself":
+            table[1, 0] = table[1, 2]
         elif where == "held":
             table[1, 3] = held
         else:
@@ -161,7 +170,7 @@ def test_destination_pages_that_break_the_rules(where):
         return table
 
     before = cache.k.clone()
-    got = run(cache, score, 64, 8, dst="same", dst_table=spoil)
+    got = run(cache, score, 64, 8, dst="same", dst_table=spoil, max_len=most)
     torch.cuda.synchronize()
     assert q.get_device_error() == q.QUAIL_ERR_DEVICE_BOUNDS
     assert q.get_device_error() == q.QUAIL_OK
@@ -172,14 +181,16 @@ def test_destination_pages_that_break_the_rules(where):
     assert torch.equal(cache.k[:before.shape[0]].view(torch.int16), before.view(torch.int16))
 
 
-def test_bad_sources_and_lengths():
-    cache = Cache([200, 150, 90, 60], 2, 128, 16, False)
-    score = scores_for(cache.lens, 2, 200, "normal")
+@pytest.mark.parametrize("most", [200, 3000])
+def test_bad_sources_and_lengths(most):
+    cache = Cache([200, 150, 90, 60], 2, 128, 16, False, width=-(-most // 16))
+    score = scores_for(cache.lens, 2, most, "normal")
     table = cache.table_np.copy()
     table[1, :] = -1
     cache.table = torch.from_numpy(table).to(DEV)
-    cache.seq_lens = torch.tensor([200, 150, 201, -4], dtype=torch.int32, device=DEV)
-    got = run(cache, score, 64, 8)
+    cache.seq_lens = torch.tensor([200, 150, most + 1, -4], dtype=torch.int32,
+                                  device=DEV)
+    got = run(cache, score, 64, 8, max_len=most)
     torch.cuda.synchronize()
     assert q.get_device_error() == q.QUAIL_ERR_DEVICE_BOUNDS
     assert got[1].tolist() == [64, -1, -1, -1]
