@@ -432,18 +432,24 @@ def _need_rows(what, t, shape, index):
     return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _need_pages(what, t, desc, pages, index):
-    """A pool of `pages` pages; its address."""
+def _need_pool(k_name, k, v_name, v, desc, pages, index):
+    """K and V of a pool of `pages` pages; their addresses."""
     shape = (pages, desc.page_size, desc.num_kv_heads, desc.head_dim)
-    fp8 = desc.kv_dtype == QUAIL_FP8_E4M3
-    if ((t.dtype not in _CODES if fp8 else t.dtype is not _BF16) or t.shape != shape
-            or t.get_device() != index or not t.is_contiguous()):
-        _explain(what, t, _CODES if fp8 else (_BF16,), shape, index)
-    return t.data_ptr()
+    dtype = k.dtype
+    if ((dtype not in _CODES if desc.kv_dtype else dtype is not _BF16) or k.shape != shape
+            or k.get_device() != index or not k.is_contiguous() or v.dtype is not dtype
+            or v.shape != shape or v.get_device() != index or not v.is_contiguous()):
+        dtypes = _CODES if desc.kv_dtype == QUAIL_FP8_E4M3 else (_BF16,)
+        for name, t in ((k_name, k), (v_name, v)):
+            if (t.dtype not in dtypes or t.shape != shape or t.get_device() != index
+                    or not t.is_contiguous()):
+                _explain(name, t, dtypes, shape, index)
+        raise ValueError(f"{k_name} and {v_name}: dtypes {k.dtype} and {v.dtype} differ")
+    return k.data_ptr(), v.data_ptr()
 
 
 def _need_scales(desc, k_scale, v_scale, index):
-    if desc.kv_dtype != QUAIL_FP8_E4M3 and k_scale is None and v_scale is None:
+    if k_scale is None and v_scale is None and not desc.kv_dtype:
         return None, None
     if k_scale is None or v_scale is None:
         raise ValueError("e4m3 pages need k_scale and v_scale, bf16 pages neither")
@@ -505,8 +511,7 @@ def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pag
                ctypes.byref(desc), shape[0], k, v, k_stride, v_stride, off,
                _need("start_pos", start_pos, _I32, (B,), dev),
                _need("block_table", block_table, _I32, (B, desc.max_pages_per_seq), dev), ks, vs,
-               _need_pages("k_pages", k_pages, desc, pages, dev),
-               _need_pages("v_pages", v_pages, desc, pages, dev))
+               *_need_pool("k_pages", k_pages, "v_pages", v_pages, desc, pages, dev))
 
 
 def paged_decode_workspace_size(desc: PagedDesc, with_scores=False) -> int:
@@ -536,8 +541,7 @@ def paged_decode_attn(desc: PagedDesc, q, k_pages, v_pages, block_table, seq_len
         raise ValueError("score_in without score_out")
     _on_device(lib.quail_paged_decode_attn, "quail_paged_decode_attn", dev, stream,
                ctypes.byref(desc), qp, q_stride,
-               _need_pages("k_pages", k_pages, desc, pages, dev),
-               _need_pages("v_pages", v_pages, desc, pages, dev),
+               *_need_pool("k_pages", k_pages, "v_pages", v_pages, desc, pages, dev),
                _need("block_table", block_table, _I32, (B, desc.max_pages_per_seq), dev),
                _need("seq_lens", seq_lens, _I32, (B,), dev), ks, vs,
                _need("out", out, _BF16, shape, dev),
@@ -591,13 +595,12 @@ def paged_kv_evict(desc: PagedDesc, budget, recent, k_pages, v_pages, block_tabl
     if len(dst_shape) != 2:
         _explain("dst_table", dst_table, (_I32,), (B, None), dev)
     _on_device(lib.quail_paged_kv_evict, "quail_paged_kv_evict", dev, stream, ctypes.byref(desc),
-               budget, recent, _need_pages("k_pages", k_pages, desc, pages, dev),
-               _need_pages("v_pages", v_pages, desc, pages, dev),
+               budget, recent,
+               *_need_pool("k_pages", k_pages, "v_pages", v_pages, desc, pages, dev),
                _need("block_table", block_table, _I32, (B, desc.max_pages_per_seq), dev),
                _need("seq_lens", seq_lens, _I32, (B,), dev), sp, width,
                _need("dst_table", dst_table, _I32, (B, dst_shape[1]), dev), dst_shape[1],
-               dst_pages, _need_pages("k_dst", k_dst, desc, dst_pages, dev),
-               _need_pages("v_dst", v_dst, desc, dst_pages, dev),
+               dst_pages, *_need_pool("k_dst", k_dst, "v_dst", v_dst, desc, dst_pages, dev),
                _need("kept", kept, _I32, (B, hkv, budget), dev),
                _need("new_lens", new_lens, _I32, (B,), dev), so, out_width, ws, ws_bytes)
 
