@@ -105,12 +105,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 32 columns of S^T: adds exp2(s c + nlse[n]) over the columns n in [lo, hi) (MASK), or all.
+// 16 columns of S^T: adds exp2(s c + nlse[n]) over the columns n in [lo, hi) (MASK), or all.
 template <bool MASK>
-__device__ __forceinline__ void add_columns(const uint32_t (&s)[32], const float* nlse, uint64_t c2,
+__device__ __forceinline__ void add_columns(const uint32_t (&s)[16], const float* nlse, uint64_t c2,
                                             int lo, int hi, uint64_t (&acc)[4]) {
 #pragma unroll
-  for (int n = 0; n < 32; n += 4) {
+  for (int n = 0; n < 16; n += 4) {
     const uint4 l = *reinterpret_cast<const uint4*>(nlse + n);
     const uint64_t x0 = f2_fma(f2(__uint_as_float(s[n]), __uint_as_float(s[n + 1])), c2,
                                f2(__uint_as_float(l.x), __uint_as_float(l.y)));
@@ -159,39 +159,43 @@ __device__ __forceinline__ bool seq_range(const AttnScoresArgs& a, int s, SeqRan
 
 // Adds the weights of one S^T tile (in TMEM at t_tile, this thread's lane) that this thread's
 // key receives: those of the query rows [lo, hi). lo_first and lo_last are the warp's first
-// and last lanes' lo: 32 columns that no lane sees are skipped, those that all see take no
-// mask. Releases the TMEM tile as soon as it is in registers.
+// and last lanes' lo: 16 columns that no lane sees are skipped, those that all see take no
+// mask. Pieces of 16 columns, the next one loading while one is worked on (32 at a time
+// without that measured 222 us instead of 217, 4 x 4,096 tokens). Releases the TMEM tile as
+// soon as it is in registers.
 __device__ __forceinline__ float tile_weight(uint32_t t_tile, const float* nlse, uint64_t c2, int lo,
                                              int lo_first, int lo_last, int hi, uint64_t* s_empty) {
   uint64_t acc[4] = {0, 0, 0, 0};
   if (lo_last == 0 && hi == kBN) {  // most tiles
+    uint32_t v[2][16];
+    tmem_ld16(t_tile, v[0]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t v[32];
-      tmem_ld32(t_tile + 32 * q, v);
-      tmem_wait_ld_dep(v);
-      if (q == 3) {
+    for (int q = 0; q < kBN / 16; ++q) {
+      tmem_wait_ld16_dep(v[q & 1]);
+      if (q < kBN / 16 - 1) {
+        tmem_ld16(t_tile + 16 * (q + 1), v[(q + 1) & 1]);
+      } else {
         tc_fence_before();
         mbar_arrive(s_empty);
       }
-      add_columns<false>(v, nlse + 32 * q, c2, 0, 0, acc);
+      add_columns<false>(v[q & 1], nlse + 16 * q, c2, 0, 0, acc);
     }
   } else {
-    const int q0 = lo_first >> 5, q1 = (hi + 31) >> 5;
+    const int q0 = lo_first >> 4, q1 = (hi + 15) >> 4;
     if (q0 >= q1) mbar_arrive(s_empty);
 #pragma unroll 1
     for (int q = q0; q < q1; ++q) {
-      uint32_t v[32];
-      tmem_ld32(t_tile + 32 * q, v);
-      tmem_wait_ld_dep(v);
+      uint32_t v[16];
+      tmem_ld16(t_tile + 16 * q, v);
+      tmem_wait_ld16_dep(v);
       if (q == q1 - 1) {
         tc_fence_before();
         mbar_arrive(s_empty);
       }
-      if (lo_last <= 32 * q && 32 * q + 32 <= hi)
-        add_columns<false>(v, nlse + 32 * q, c2, 0, 0, acc);
+      if (lo_last <= 16 * q && 16 * q + 16 <= hi)
+        add_columns<false>(v, nlse + 16 * q, c2, 0, 0, acc);
       else
-        add_columns<true>(v, nlse + 32 * q, c2, lo - 32 * q, hi - 32 * q, acc);
+        add_columns<true>(v, nlse + 16 * q, c2, lo - 16 * q, hi - 16 * q, acc);
     }
   }
   float x0, x1, y0, y1;
