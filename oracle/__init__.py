@@ -36,6 +36,10 @@ longest-processing-time-first, the exhaustive optimum); pins in tests/test_oracl
 join.py: the join's verdicts from the head's argmax (verdict per suffix, the passing
 suffixes in order, a count per anchor); pins in tests/test_oracle_join.py.
 
+paged.py: the paged cache (rows written into pages, attention of one new token, the weight
+that keys receive, eviction by it); pins in tests/test_oracle_paged.py (causal attention's
+last row, softmax column sums, a selection loop, hand-placed slots).
+
 Pins (tests/test_oracle.py): brute-force loops, the cascade-merge = monolithic identity,
 closed forms, a library SDPA with an explicit mask, RMSNorm closed forms, all 256 E4M3
 codes against the OCP formula and against torch's float8_e4m3fn. No function here is
