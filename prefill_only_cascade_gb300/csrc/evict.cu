@@ -524,7 +524,8 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   const int most = a.budget < a.max_len ? a.budget : a.max_len;
   const int64_t own = (most + page - 1) / page;
   const int64_t others = a.num_seqs * (own + (a.same_pool ? (a.max_len + page - 1) / page : 0));
-  if (a.max_len <= kSmallKeys && most <= kSmallKept && own * others <= 65536) {
+  // (every CTA compares its `own` pages with all the `others`)
+  if (a.max_len <= kSmallKeys && most <= kSmallKept && others <= 1024 && own * others <= 65536) {
     evict_select_kernel<4, false, true><<<static_cast<unsigned>(pairs), kSelThreads, 0, stream>>>(a, 1);
     return cudaGetLastError();
   }
