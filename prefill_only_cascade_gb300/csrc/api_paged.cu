@@ -256,8 +256,9 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
   if (total_k_tokens > 0 && (k == nullptr || score_out == nullptr || !aligned(k, 16)))
     return QUAIL_ERR_INVALID_ARG;
   if (!aligned(score_in, 4) || !aligned(score_out, 4)) return QUAIL_ERR_INVALID_ARG;
-  // TMA coordinates run up to two tiles past the last token
-  if (total_q_tokens > kInt32Max - 1024 || total_k_tokens > kInt32Max - 1024)
+  // TMA coordinates and key numbers run up to two tiles past the last token
+  if (total_q_tokens > kInt32Max - 1024 || total_k_tokens > kInt32Max - 1024 ||
+      max_k_len > kInt32Max - 1024)
     return QUAIL_ERR_UNSUPPORTED;
   // 8 blocks at most per (sequence, KV head, 128 keys)
   if ((static_cast<int64_t>(max_k_len) + 127) / 128 * num_seqs > kInt32Max / 8 / num_kv_heads)
@@ -320,6 +321,7 @@ quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, 
   if (budget < 1 || recent < 0 || recent > budget || dst_max_pages_per_seq < 0 ||
       dst_num_pages < 0 || score_stride < d.max_seq_len)
     return QUAIL_ERR_INVALID_ARG;
+  if (budget > (1 << 30)) return QUAIL_ERR_UNSUPPORTED;
   const int64_t most = budget < d.max_seq_len ? budget : d.max_seq_len;
   if (most > static_cast<int64_t>(dst_max_pages_per_seq) * d.page_size) return QUAIL_ERR_INVALID_ARG;
   if (score_out != nullptr && score_out_stride < budget) return QUAIL_ERR_INVALID_ARG;

@@ -130,6 +130,7 @@ def test_decode_workspace():
     (dict(lse=None), INVALID), (dict(lse=P + 2), INVALID), (dict(qo=None), INVALID),
     (dict(ko=P + 1), INVALID), (dict(so=None), INVALID), (dict(so=P + 2), INVALID),
     (dict(si=P + 2), INVALID), (dict(seqs=1 << 20, mk=1 << 20, stride=1 << 20), UNSUPPORTED),
+    (dict(mk=(1 << 31) - 1000, stride=1 << 31), UNSUPPORTED),
 ])
 def test_scores_rejects(change, expect):
     assert scores(**change) == expect
@@ -157,6 +158,7 @@ def test_evict_limits():
     d = desc(num_seqs=1 << 10, num_kv_heads=32)
     assert evict(d, budget=(1 << 31) - 1, dst_max=1 << 10, kd=1 << 60, vd=1 << 61, new=1 << 59) == UNSUPPORTED
     assert evict(desc(num_seqs=1 << 12), dst_max=1 << 20, new=1 << 59) == UNSUPPORTED
+    assert evict(desc(), budget=(1 << 30) + 1) == UNSUPPORTED
 
 
 # ------------------------------------------------------------------ the binding
