@@ -415,8 +415,9 @@ typedef struct {
  *               sequence (then T = B)
  *   start_pos   [B] int32: tokens that the sequence holds already
  * A row whose position or page is out of range, or that no sequence holds, is skipped and
- * reported (see above), and so are offsets that do not increase from 0 to T. A page that is written must belong to one sequence: of two rows
- * that name the same slot an unspecified mixture remains.
+ * reported (see above), and so are offsets that do not increase from 0 to T. A page that is
+ * written must belong to one sequence: of two rows that name the same slot an unspecified
+ * mixture remains. The slots written must not overlap k_new and v_new.
  */
 quail_status quail_paged_kv_append(const quail_paged_desc* desc, int64_t num_new,
                                    const void* k_new, const void* v_new, int64_t k_row_stride,
@@ -438,7 +439,8 @@ quail_status quail_paged_kv_append(const quail_paged_desc* desc, int64_t num_new
  *            of range or a page outside the pool: out and lse NaN for that sequence (for
  *            its KV heads), and its score_out as below with w = 0, or untouched where the
  *            length is out of range.
- *   out [B, Hq, d] bf16, 16-byte aligned; lse [B, Hq] fp32 (natural log), may be NULL
+ *   out [B, Hq, d] bf16, 16-byte aligned, not overlapping q; lse [B, Hq] fp32 (natural
+ *            log), may be NULL
  *   score_in, score_out [B, Hkv, score_stride] fp32, score_stride >= max_seq_len;
  *            score_out NULL: no weights are formed; score_in NULL: zeros; both may be the
  *            same buffer. Entries at seq_lens[b] and beyond are left as they were. A head
@@ -471,7 +473,8 @@ size_t quail_paged_decode_workspace_size(const quail_paged_desc* desc, int32_t w
  * q_offsets[a] = suffix_offsets[anchor_suffix_ptr[a]], lse from quail_cascade_attn).
  *   q [Tq, Hq, d], k [Tk, Hkv, d] bf16, rows q_row_stride / k_row_stride elements apart
  *            (at least the row, a multiple of 8), 16-byte aligned
- *   lse [Tq, Hq] fp32 natural log; a query whose lse is -inf gives no weight
+ *   lse [Tq, Hq] fp32 natural log; a query whose lse is -inf gives no weight, whatever
+ *            its row holds; NaN carries over
  *   q_offsets, k_offsets [num_seqs+1] int32 token prefix sums (checked on the device: a
  *            sequence whose ranges lie outside the totals or exceed max_q_len / max_k_len
  *            is left out and QUAIL_ERR_DEVICE_BOUNDS reported)
@@ -497,7 +500,7 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
  * -inf). Their K and V rows are copied in order to positions 0 .. new_lens[b]-1 of the pages
  * that dst_table names; heads keep their own positions (keys are already rotated). The
  * source is not changed, so shared pages may be cut; the caller frees it.
- *   budget >= 1, 0 <= recent <= budget
+ *   1 <= budget <= 2^30, 0 <= recent <= budget
  *   score [B, Hkv, score_stride] fp32, score_stride >= max_seq_len
  *   dst_table [B, dst_max_pages_per_seq] int32 into the destination pool k_dst / v_dst
  *            [dst_num_pages, page_size, Hkv, d]: either the same pool (same pointers and

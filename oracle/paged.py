@@ -66,7 +66,7 @@ def scores(q, k, lse, scale, causal, window=0):
     for i in range(nq - min(window, nq) if window else 0, nq):
         seen = min(nk, max(0, i + nk - nq + 1)) if causal else nk
         for h in range(hq):
-            if lse[i, h] > -np.inf:
+            if lse[i, h] != -np.inf:
                 g = h // (hq // hkv)
                 total[g, :seen] += np.exp(scale * (k[:seen, g] @ q[i, h]) - lse[i, h])
     return total

@@ -16,8 +16,9 @@
 //     tile, each with its own S^T in TMEM) exponentiate while the tensor cores fill the other
 //     parity. What bounds it is the hand-over MMA -> softmax -> MMA of each S^T tile, whose
 //     latency four tiles in TMEM do not hide (about 1,700 clk per two products instead of
-//     1,030): hence an MMA warp per key tile and a warp of its own for the lse. 256 keys and not 128, so that a query tile is read
-//     from L2 once per two products (~9 TB/s at full rate instead of 18).
+//     1,030): hence an MMA warp per key tile and a warp of its own for the lse. 256 keys and
+//     not 128, so that a query tile is read from L2 once per two products (~9 TB/s at full rate
+//     instead of 18).
 //   attn_scores_window_kernel   where the queries of a (sequence, KV head) fit four tiles (the
 //     last 128 tokens at G = 4), they stay in shared memory and the keys stream past them, a
 //     warpgroup per key tile: bound by reading K once from HBM with one query tile, by the
@@ -79,6 +80,7 @@ struct Shared {
   uint64_t s_full[kGroups], s_empty[kGroups];
   uint32_t tmem;
   int abort_flag;
+  int dead[kQStages];                       // the tile has rows whose lse is -inf
 };
 struct WinShared {
   alignas(16) float nlse[kWinMaxQ * kBN];
@@ -105,8 +107,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 16 columns of S^T: adds exp2(s c + nlse[n]) over the columns n in [lo, hi) (MASK), or all.
-template <bool MASK>
+// 16 columns of S^T: adds exp2(s c + nlse[n]) over the columns n in [lo, hi) (MASK), of them
+// those whose nlse is not -inf (DEAD), or all.
+template <bool MASK, bool DEAD>
 __device__ __forceinline__ void add_columns(const uint32_t (&s)[16], const float* nlse, uint64_t c2,
                                             int lo, int hi, uint64_t (&acc)[4]) {
 #pragma unroll
@@ -123,11 +126,12 @@ __device__ __forceinline__ void add_columns(const uint32_t (&s)[16], const float
     b = ex2(b);
     c = ex2(c);
     d = ex2(d);
-    if (MASK) {  // select, not multiply: rows past the end may hold anything
-      a = n >= lo && n < hi ? a : 0.f;
-      b = n + 1 >= lo && n + 1 < hi ? b : 0.f;
-      c = n + 2 >= lo && n + 2 < hi ? c : 0.f;
-      d = n + 3 >= lo && n + 3 < hi ? d : 0.f;
+    // select, not multiply: rows past the end, or of no weight, may hold anything
+    if (MASK) {
+      a = n >= lo && n < hi && (!DEAD || __uint_as_float(l.x) != -INFINITY) ? a : 0.f;
+      b = n + 1 >= lo && n + 1 < hi && (!DEAD || __uint_as_float(l.y) != -INFINITY) ? b : 0.f;
+      c = n + 2 >= lo && n + 2 < hi && (!DEAD || __uint_as_float(l.z) != -INFINITY) ? c : 0.f;
+      d = n + 3 >= lo && n + 3 < hi && (!DEAD || __uint_as_float(l.w) != -INFINITY) ? d : 0.f;
     }
     acc[(n >> 1) & 3] = f2_add(acc[(n >> 1) & 3], f2(a, b));
     acc[((n >> 1) + 1) & 3] = f2_add(acc[((n >> 1) + 1) & 3], f2(c, d));
@@ -160,13 +164,16 @@ __device__ __forceinline__ bool seq_range(const AttnScoresArgs& a, int s, SeqRan
 // Adds the weights of one S^T tile (in TMEM at t_tile, this thread's lane) that this thread's
 // key receives: those of the query rows [lo, hi). lo_first and lo_last are the warp's first
 // and last lanes' lo: 16 columns that no lane sees are skipped, those that all see take no
-// mask. Pieces of 16 columns, the next one loading while one is worked on (32 at a time
-// without that measured 222 us instead of 217, 4 x 4,096 tokens). Releases the TMEM tile as
-// soon as it is in registers.
+// mask unless the tile has dead rows (lse -inf; telling them apart from the others costs 0.6 %
+// of 4 x 4,096 tokens, 1.5 % where every tile would otherwise be without a mask). Pieces of 16
+// columns, the next one loading while one is worked on (32 at a time without that measured
+// 222 us instead of 217, 4 x 4,096 tokens). Releases the TMEM tile as soon as it is in
+// registers.
 __device__ __forceinline__ float tile_weight(uint32_t t_tile, const float* nlse, uint64_t c2, int lo,
-                                             int lo_first, int lo_last, int hi, uint64_t* s_empty) {
+                                             int lo_first, int lo_last, int hi, bool dead,
+                                             uint64_t* s_empty) {
   uint64_t acc[4] = {0, 0, 0, 0};
-  if (lo_last == 0 && hi == kBN) {  // most tiles
+  if (lo_last == 0 && hi == kBN && !dead) {  // most tiles
     uint32_t v[2][16];
     tmem_ld16(t_tile, v[0]);
 #pragma unroll
@@ -178,7 +185,7 @@ __device__ __forceinline__ float tile_weight(uint32_t t_tile, const float* nlse,
         tc_fence_before();
         mbar_arrive(s_empty);
       }
-      add_columns<false>(v[q & 1], nlse + 16 * q, c2, 0, 0, acc);
+      add_columns<false, false>(v[q & 1], nlse + 16 * q, c2, 0, 0, acc);
     }
   } else {
     const int q0 = lo_first >> 4, q1 = (hi + 15) >> 4;
@@ -192,10 +199,12 @@ __device__ __forceinline__ float tile_weight(uint32_t t_tile, const float* nlse,
         tc_fence_before();
         mbar_arrive(s_empty);
       }
-      if (lo_last <= 16 * q && 16 * q + 16 <= hi)
-        add_columns<false>(v, nlse + 16 * q, c2, 0, 0, acc);
+      if (lo_last <= 16 * q && 16 * q + 16 <= hi && !dead)
+        add_columns<false, false>(v, nlse + 16 * q, c2, 0, 0, acc);
+      else if (!dead)
+        add_columns<true, false>(v, nlse + 16 * q, c2, lo - 16 * q, hi - 16 * q, acc);
       else
-        add_columns<true>(v, nlse + 16 * q, c2, lo - 16 * q, hi - 16 * q, acc);
+        add_columns<true, true>(v, nlse + 16 * q, c2, lo - 16 * q, hi - 16 * q, acc);
     }
   }
   float x0, x1, y0, y1;
@@ -387,9 +396,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_parity_warp(wc, &sh.l_empty[st], ((i / kQStages) & 1) ^ 1u);
         if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)  // a row that saw nothing (-inf) gives no weight
+        for (int j = 0; j < 4; ++j)
           sh.nlse[st][lane + 32 * j] =
               l[k][j] == -INFINITY ? -INFINITY : l[k][j] * -1.4426950408889634f;
+        const bool dead = __any_sync(0xFFFFFFFFu, l[k][0] == -INFINITY || l[k][1] == -INFINITY ||
+                                                      l[k][2] == -INFINITY || l[k][3] == -INFINITY);
+        if (lane == 0) sh.dead[st] = dead;
         mbar_arrive(&sh.l_full[st]);
         load(i + 4, l[k]);
       }
@@ -408,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // also where it sees no key: one release of a stage per tile, in the tiles' order
       bool ok = wait_parity_warp(wc, &sh.l_full[st], (i / kQStages) & 1u);
       if (!ok) break;
+      const bool dead = sh.dead[st] != 0;
       if (tile_at(i) >= from) {
         ok = wait_parity_warp(wc, &sh.s_full[grp], n & 1u);
         if (!ok) break;
@@ -423,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // compensated: thousands of tiles may add up (Kahan)
         const float y =
-            tile_weight(t_tile, sh.nlse[st], c2, lo, lo_first, lo_last, hi, &sh.s_empty[grp]) - lost;
+            tile_weight(t_tile, sh.nlse[st], c2, lo, lo_first, lo_last, hi, dead,
+                        &sh.s_empty[grp]) - lost;
         const float sum = total + y;
         lost = fabsf(sum) < INFINITY ? (sum - total) - y : 0.f;
         total = sum;
@@ -522,13 +536,15 @@ __global__ void __launch_bounds__(Win<QT>::kThreads, QT == 1 ? 2 : 1)
     tmem_alloc(&sh.tmem, W::kTmem);
     tmem_relinquish();
   }
+  bool mine = false;  // of this thread's rows one has an lse of -inf
   for (int r = threadIdx.x; r < q_tiles * kBN; r += W::kThreads) {
     const int t = sr.f + r / G;
     const float l = t < sr.nq ? __ldg(a.lse + (sr.q0 + t) * a.hq + g * G + r % G) : 0.f;
     sh.nlse[r] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+    mine |= l == -INFINITY;
   }
   tc_fence_before();
-  __syncthreads();
+  const bool dead = __syncthreads_or(mine);
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const WaitCtl wc{a.timeout_ns, &sh.abort_flag, a.err_word};
@@ -600,7 +616,7 @@ __global__ void __launch_bounds__(Win<QT>::kThreads, QT == 1 ? 2 : 1)
           lo_first = __shfl_sync(0xFFFFFFFFu, lo, 0);
           lo_last = __shfl_sync(0xFFFFFFFFu, lo, 31);
         }
-        w += tile_weight(t_lane + 128u * buf, sh.nlse + qt * kBN, c2, lo, lo_first, lo_last, rows,
+        w += tile_weight(t_lane + 128u * buf, sh.nlse + qt * kBN, c2, lo, lo_first, lo_last, rows, dead,
                          &sh.s_empty[grp][buf]);
       }
       if (real && ok) a.score_out[out0 + key] = base + w;

@@ -198,6 +198,22 @@ def test_lse_of_minus_infinity_gives_no_weight():
     check(score, qs, ks, lse, n, n, scale, True, 0)
 
 
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 60), (True, 130), (True, 250), (False, 0)])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_queries_without_weight_may_hold_anything(causal, window, what):
+    """Rows whose lse is -inf (padding, say) are left out although they hold NaN or infinities."""
+    n, scale = [1200, 300], 1 / 8
+    qs, ks, lse = make(n, n, 2, 1, 64, 11, causal, scale)
+    for rows in (slice(0, 3), slice(700, 900), slice(1100, 1101), slice(1190, 1210), slice(1499, 1500)):
+        qs[rows, 1], lse[rows, 1] = what, -math.inf
+    score = torch.full((2, 1, 1203), -3.0, device=DEV)
+    q.attn_scores(qs.to(DEV), ks.to(DEV), lse.to(DEV), offsets(n), offsets(n), score, 1200, 1200,
+                  causal=causal, window=window)
+    ok()
+    qs[lse == -math.inf] = 0    # for the bound's magnitudes
+    check(score, qs, ks, lse, n, n, scale, causal, window)
+
+
 def test_bad_offsets_are_left_out_and_reported():
     n, scale = [50, 60, 70], 1 / 8
     qs, ks, lse = make(n, n, 2, 1, 64, 9, True, scale)
