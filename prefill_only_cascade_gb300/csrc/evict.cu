@@ -85,6 +85,40 @@ __device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void st_cluster_u4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster_u2(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+
+// The notes about the pages of all sequences, a warp for 32 places of a sequence's table.
+__device__ void write_notes(const PagedEvictArgs& a, int warp, int warps, int chunks) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t item = warp; item < static_cast<int64_t>(a.num_seqs) * chunks; item += warps) {
+    const int b = static_cast<int>(item / chunks), j = static_cast<int>(item % chunks) * 32 + lane;
+    const int n = evict_len(a, b);
+    if (a.same_pool && j < pages_of(a, n)) {
+      const int p = __ldg(a.table + b * a.max_pages + j);
+      if (p >= 0 && p < a.num_pages) a.hold[p] = b * a.max_pages + j;
+    }
+    if (j < pages_of(a, min(n, a.budget))) {
+      const int entry = b * a.dst_max_pages + j;
+      const int p = __ldg(a.dst_table + entry);
+      if (p < 0 || p >= a.dst_num_pages) continue;
+      // of several entries that claim p the last one to do so sees another's claim, and its
+      // note follows every clearing
+      a.dup[p] = -1;
+      __threadfence();
+      const int old = atomicExch(a.claim + p, entry);
+      __threadfence();
+      if (old != entry && is_claim(a, old, p)) a.dup[p] = entry;
+    }
+  }
+}
+
 // KPT: keys a thread holds, in registers, or (SHARED) in shared memory: 32 in registers leave
 // room for one CTA per SM, and then only 15 clusters of eight fit the GPU at once (36 with
 // two). A CTA's part of the competing tokens is walked in rounds of
@@ -96,20 +130,24 @@ constexpr int kSmallKept = 512;               // kept ones at most
 constexpr int kSmallPages = kSmallKept / 16;  // their pages at most
 template <int KPT, bool SHARED, bool FUSED>
 __global__ void __launch_bounds__(kSelThreads, 2)
-    evict_select_kernel(const PagedEvictArgs a, int cluster) {
+    evict_select_kernel(const PagedEvictArgs a, int cluster, int note_blocks, int note_chunks) {
   // Scores of one octave share few first digits, so lanes often add to the same bin: four
   // copies, by lane, keep those additions from queueing.
   __shared__ __align__(16) uint32_t s_first[kSub][kBins];
   __shared__ __align__(16) uint32_t s_second[kBins], s_third[kBins / 2];
   __shared__ uint32_t s_warp[kSelWarps];
   __shared__ uint32_t s_found[3];       // digit, how many are above it, how many have it
-  __shared__ __align__(16) uint32_t s_count[4];  // this CTA's keys above / at the threshold
+  __shared__ __align__(16) uint32_t s_count[kMaxCluster][2];  // the CTAs' keys above / at the threshold
   __shared__ uint32_t s_gt[kSelWarps], s_eq[kSelWarps];
   __shared__ int s_kept[FUSED ? kSmallKept : 1];
   __shared__ int s_to[FUSED ? kSmallPages : 1], s_bad[FUSED ? kSmallPages + 1 : 1];
   if (!FUSED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!FUSED && static_cast<int>(blockIdx.x) < note_blocks) {
+    write_notes(a, blockIdx.x * kSelWarps + (threadIdx.x >> 5), note_blocks * kSelWarps, note_chunks);
+    return;
+  }
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int pair = blockIdx.x / cluster;
+  const int pair = (blockIdx.x - note_blocks) / cluster;
   const int b = pair / a.hkv, g = pair % a.hkv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = evict_len(a, b);
@@ -191,28 +229,9 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         const int p = __ldg(a.table + b * a.max_pages + j);
         if (p < 0 || p >= a.num_pages) s_bad[mine] = 1;
       }
-  } else if (g == 0) {  // the sequence's pages and its new length, once
-    if (tid == 0) {
-      a.new_lens[b] = n < 0 ? -1 : fresh;
-      if (n < 0) atomicOr(a.err_word, kErrDeviceBounds);
-    }
-    if (a.same_pool)
-      for (int j = tid; j < pages_of(a, n); j += threads) {
-        const int p = __ldg(a.table + b * a.max_pages + j);
-        if (p >= 0 && p < a.num_pages) a.hold[p] = b * a.max_pages + j;
-      }
-    for (int j = tid; j < pages_of(a, fresh); j += threads) {
-      const int entry = b * a.dst_max_pages + j;
-      const int p = __ldg(a.dst_table + entry);
-      if (p < 0 || p >= a.dst_num_pages) continue;
-      // of several entries that claim p the last one to do so sees another's claim, and its
-      // note follows every clearing
-      a.dup[p] = -1;
-      __threadfence();
-      const int old = atomicExch(a.claim + p, entry);
-      __threadfence();
-      if (old != entry && is_claim(a, old, p)) a.dup[p] = entry;
-    }
+  } else if (g == 0 && tid == 0) {  // the new length, once
+    a.new_lens[b] = n < 0 ? -1 : fresh;
+    if (n < 0) atomicOr(a.err_word, kErrDeviceBounds);
   }
   // the recent tokens, and what follows the last kept one
   for (int i = tid; i < recent; i += threads) {
@@ -269,22 +288,31 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         }
       }
       if (cluster > 1) {
+        // Each CTA adds up its share of the bins and hands the sums to all. (All bins read
+        // by all, 57 KB through distributed shared memory per CTA, took 3-4 us a pass.)
         if (pass == 0) *reinterpret_cast<uint4*>(hist + kBinsPerThread * threadIdx.x) = sum;
         cluster_sync();
-        uint4 v[kMaxCluster - 1];
+        const int share = (pass < 2 ? kBins : kBins / 2) / cluster;
+        if (threadIdx.x < share / 4) {
+          uint32_t* at = hist + rank * share + 4 * threadIdx.x;
+          uint4 v[kMaxCluster];
 #pragma unroll
-        for (int c = 1; c < kMaxCluster; ++c)
-          if (c < cluster && has)
-            v[c - 1] = ld_cluster_u4(
-                cluster_map(hist + kBinsPerThread * threadIdx.x, (rank + c) & (cluster - 1)));
+          for (int c = 0; c < kMaxCluster; ++c)
+            if (c < cluster) v[c] = ld_cluster_u4(cluster_map(at, (rank + c) & (cluster - 1)));
 #pragma unroll
-        for (int c = 1; c < kMaxCluster; ++c)
-          if (c < cluster && has) {
-            sum.x += v[c - 1].x;
-            sum.y += v[c - 1].y;
-            sum.z += v[c - 1].z;
-            sum.w += v[c - 1].w;
-          }
+          for (int c = 1; c < kMaxCluster; ++c)
+            if (c < cluster) {
+              v[0].x += v[c].x;
+              v[0].y += v[c].y;
+              v[0].z += v[c].z;
+              v[0].w += v[c].w;
+            }
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; ++c)  // nobody else reads this share
+            if (c < cluster) st_cluster_u4(cluster_map(at, (rank + c) & (cluster - 1)), v[0]);
+        }
+        cluster_sync();
+        if (has) sum = *reinterpret_cast<const uint4*>(hist + kBinsPerThread * threadIdx.x);
       }
       // how many keys lie in the bins of the threads after this one
       const uint32_t bin[kBinsPerThread] = {sum.x, sum.y, sum.z, sum.w};
@@ -352,18 +380,16 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   const uint32_t lane_gt = lane < kSelWarps ? s_gt[lane] : 0u;
   const uint32_t lane_eq = lane < kSelWarps ? s_eq[lane] : 0u;
   uint32_t base_gt = 0, base_eq = 0;    // kept / at the threshold before this CTA's
-  if (cluster > 1) {
+  if (k >= elig) {
+    base_gt = e0;
+  } else if (cluster > 1) {
     const uint32_t all_gt = __reduce_add_sync(0xFFFFFFFFu, lane_gt);
     const uint32_t all_eq = __reduce_add_sync(0xFFFFFFFFu, lane_eq);
-    if (threadIdx.x == 0) {
-      s_count[0] = all_gt;
-      s_count[1] = all_eq;
-    }
+    // to all of them (which run: the passes had a barrier), so that none has to stay for reads
+    if (threadIdx.x < cluster) st_cluster_u2(cluster_map(s_count[rank], threadIdx.x), all_gt, all_eq);
     cluster_sync();
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (lane < rank) v = ld_cluster_u4(cluster_map(s_count, lane));
-    base_gt = __reduce_add_sync(0xFFFFFFFFu, v.x);
-    base_eq = __reduce_add_sync(0xFFFFFFFFu, v.y);
+    base_gt = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? s_count[lane][0] : 0u);
+    base_eq = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? s_count[lane][1] : 0u);
   }
   for (int round = 0; round < rounds; ++round) {
     uint32_t warp_gt, warp_eq;          // before this warp's
@@ -430,7 +456,6 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       }
     }
   }
-  if (cluster > 1) cluster_sync();  // no CTA leaves while others read its counts
   }
 
   if constexpr (FUSED) {
@@ -547,7 +572,7 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   const int64_t others = a.num_seqs * (own + (a.same_pool ? (a.max_len + page - 1) / page : 0));
   // (every CTA compares its `own` pages with all the `others`)
   if (a.max_len <= kSmallKeys && most <= kSmallKept && others <= 1024 && own * others <= 65536) {
-    evict_select_kernel<4, false, true><<<static_cast<unsigned>(pairs), kSelThreads, 0, stream>>>(a, 1);
+    evict_select_kernel<4, false, true><<<static_cast<unsigned>(pairs), kSelThreads, 0, stream>>>(a, 1, 0, 0);
     return cudaGetLastError();
   }
   cudaError_t e = cudaSuccess;
@@ -568,19 +593,29 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
+  // The notes have blocks of their own in front, up to 32 (the claims' fences and exchanges
+  // would keep one head's selection, and so its cluster, 2 us longer).
+  const int64_t places = a.same_pool ? (a.max_len + page - 1) / page : own;
+  const int note_chunks = static_cast<int>((places + 31) / 32);
+  int note_blocks = 0;
+  while (note_blocks < 32 && note_blocks * kSelWarps < a.num_seqs * static_cast<int64_t>(note_chunks))
+    note_blocks += cluster;
+  cfg.gridDim = dim3(static_cast<unsigned>(note_blocks + pairs * cluster));
   cfg.blockDim = dim3(kSelThreads);
   if (per <= 4 * kSelThreads) {
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<4, false, false>, a, cluster);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<4, false, false>, a, cluster, note_blocks,
+                           note_chunks);
   } else if (per <= 16 * kSelThreads) {
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<16, false, false>, a, cluster);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<16, false, false>, a, cluster, note_blocks,
+                           note_chunks);
   } else {
     constexpr int kBytes = kSelThreads * kMaxKeys * 4;
     static std::atomic<uint64_t> ready{0};
     e = allow_smem(reinterpret_cast<const void*>(evict_select_kernel<kMaxKeys, true, false>), kBytes, ready);
     if (e != cudaSuccess) return e;
     cfg.dynamicSmemBytes = kBytes;
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<kMaxKeys, true, false>, a, cluster);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel<kMaxKeys, true, false>, a, cluster, note_blocks,
+                           note_chunks);
     cfg.dynamicSmemBytes = 0;
   }
   if (e != cudaSuccess) return e;
