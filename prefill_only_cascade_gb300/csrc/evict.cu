@@ -51,8 +51,7 @@ __device__ __forceinline__ bool is_claim(const PagedEvictArgs& a, int entry, int
   const int n = evict_len(a, entry / a.dst_max_pages);
   return entry % a.dst_max_pages < pages_of(a, min(n, a.budget));
 }
-__device__ __forceinline__ bool is_held(const PagedEvictArgs& a, int p) {
-  const int entry = a.hold[p];
+__device__ __forceinline__ bool is_held(const PagedEvictArgs& a, int entry, int p) {
   if (entry < 0 || entry >= a.num_seqs * a.max_pages || __ldg(a.table + entry) != p) return false;
   return entry % a.max_pages < pages_of(a, evict_len(a, entry / a.max_pages));
 }
@@ -498,31 +497,37 @@ constexpr int kCopyUnroll = 4;   // rows' pieces in flight per thread, K and V e
 __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const PagedEvictArgs a,
                                                                      int chunks) {
   __shared__ int64_t s_src[kCopyThreads], s_dst[kCopyThreads];  // byte offsets; < 0: none
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x / chunks;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x % chunks) * kCopyThreads;
   const int n = evict_len(a, b);
   const int fresh = min(n, a.budget);
   const int64_t rows = static_cast<int64_t>(fresh) * a.hkv;
-  if (r0 >= rows) return;
+  if (r0 >= rows) {
+    // also where nothing is to be moved: the call ends with its selection
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int count = static_cast<int>(min(static_cast<int64_t>(kCopyThreads), rows - r0));
-  if (threadIdx.x < count) {
-    const int64_t r = r0 + threadIdx.x;
-    const int i = static_cast<int>(r / a.hkv), g = static_cast<int>(r % a.hkv);
+  const bool has = threadIdx.x < count;
+  const int64_t r = r0 + threadIdx.x;
+  const int i = static_cast<int>(r / a.hkv), g = static_cast<int>(r % a.hkv);
+  // what the selection does not write is read before its end
+  const int to = has ? __ldg(a.dst_table + static_cast<int64_t>(b) * a.dst_max_pages +
+                             (i >> a.page_shift)) : -1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (has) {
     const int mask = (1 << a.page_shift) - 1;
+    const bool to_ok = to >= 0 && to < a.dst_num_pages;
+    // (three loads side by side, then two: not one after the other)
     const int pos = a.kept[(static_cast<int64_t>(b) * a.hkv + g) * a.budget + i];
-    const int to = __ldg(a.dst_table + static_cast<int64_t>(b) * a.dst_max_pages +
-                         (i >> a.page_shift));
+    const int dup = to_ok ? a.dup[to] : 0;
+    const int hold = to_ok && a.same_pool ? a.hold[to] : -1;
+    const bool pos_ok = pos >= 0 && pos < n;
+    const int from = pos_ok ? __ldg(a.table + static_cast<int64_t>(b) * a.max_pages +
+                                    (pos >> a.page_shift)) : -1;
     // the destination page is written once, by this sequence, and held by none
-    bool ok = to >= 0 && to < a.dst_num_pages && a.dup[to] == -1 &&
-              !(a.same_pool && is_held(a, to));
-    int from = -1;
-    if (pos >= 0 && pos < n) {
-      from = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + (pos >> a.page_shift));
-      ok = ok && from >= 0 && from < a.num_pages;
-    } else {
-      ok = false;
-    }
+    const bool ok = to_ok && dup == -1 && pos_ok && from >= 0 && from < a.num_pages &&
+                    !is_held(a, hold, to);
     if (!ok) {
       atomicOr(a.err_word, kErrDeviceBounds);
       a.new_lens[b] = -1;
