@@ -12,8 +12,8 @@
 //    Bound by latency: about ten barriers and dependent steps of a microsecond or less.
 // 2. evict_copy_kernel    moves the kept rows: a block looks up the places of 256 (token,
 //    head) rows first, then moves them, 16 bytes a thread and eight in flight.
-// Small calls do both in one launch (FUSED): a CTA per (sequence, KV head) that compares its
-// destination pages with every other page of the call itself, and moves what it keeps.
+// Small calls do both in one launch (FUSED): each CTA compares its sequence's destination pages
+// with every other page of the call itself, and moves the tokens of its own part that stay.
 #include <cstdint>
 
 #include "kernels.h"
@@ -124,9 +124,9 @@ __device__ void write_notes(const PagedEvictArgs& a, int warp, int warps, int ch
 // kSelThreads * KPT (one, unless the part is longer: then the scores are read again in every
 // pass); in a round each warp has a contiguous run, lane by lane, so that the order of the
 // tokens is (round, warp, i, lane).
-constexpr int kSmallKeys = 4 * kSelThreads;   // FUSED: tokens of a sequence at most
-constexpr int kSmallKept = 512;               // kept ones at most
-constexpr int kSmallPages = kSmallKept / 16;  // their pages at most
+constexpr int kSmallKeys = 4 * kSelThreads;   // FUSED: tokens per CTA at most
+constexpr int kSmallKept = 512;               // kept ones per CTA of the cluster at most
+constexpr int kSmallPages = kMaxCluster * kSmallKept / 16;  // their pages at most
 template <int KPT, bool SHARED, bool FUSED>
 __global__ void __launch_bounds__(kSelThreads, 2)
     evict_select_kernel(const PagedEvictArgs a, int cluster, int note_blocks, int note_chunks) {
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   __shared__ uint32_t s_found[3];       // digit, how many are above it, how many have it
   __shared__ __align__(16) uint32_t s_count[kMaxCluster][2];  // the CTAs' keys above / at the threshold
   __shared__ uint32_t s_gt[kSelWarps], s_eq[kSelWarps];
-  __shared__ int s_kept[FUSED ? kSmallKept : 1];
+  int* s_kept = reinterpret_cast<int*>(s_first);  // FUSED, after the passes: this CTA's kept ones
   __shared__ int s_to[FUSED ? kSmallPages : 1], s_bad[FUSED ? kSmallPages + 1 : 1];
   if (!FUSED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!FUSED && static_cast<int>(blockIdx.x) < note_blocks) {
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         if (j < pages_of(a, evict_len(a, seq))) meet(__ldg(a.table + seq * a.max_pages + j), -1);
       }
     }
-    if (g == 0)
+    if (g == 0 && rank == 0)
       for (int j = threadIdx.x; j < pages_of(a, n); j += kSelThreads) {
         const int p = __ldg(a.table + b * a.max_pages + j);
         if (p < 0 || p >= a.num_pages) s_bad[mine] = 1;
@@ -235,13 +235,13 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   // the recent tokens, and what follows the last kept one
   for (int i = tid; i < recent; i += threads) {
     kept[k + i] = elig + i;
-    if (FUSED) s_kept[k + i] = elig + i;
     if (score_out != nullptr) score_out[k + i] = __ldg(score + elig + i);
   }
   for (int i = fresh + tid; i < a.budget; i += threads) kept[i] = -1;
   if (score_out != nullptr)
     for (int64_t i = fresh + tid; i < a.score_out_stride; i += threads) score_out[i] = 0.f;
   if (!FUSED && k == 0) return;  // the same for every CTA of the cluster
+  int first_kept = 0, kept_here = 0;    // FUSED: this CTA's places, without the recent tokens
   if (k > 0) {
 
   // keys above the threshold stay, and `need` of those at it; k >= elig: every key
@@ -379,17 +379,19 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   const uint32_t lane_gt = lane < kSelWarps ? s_gt[lane] : 0u;
   const uint32_t lane_eq = lane < kSelWarps ? s_eq[lane] : 0u;
   uint32_t base_gt = 0, base_eq = 0;    // kept / at the threshold before this CTA's
+  const uint32_t all_gt = __reduce_add_sync(0xFFFFFFFFu, lane_gt);
+  const uint32_t all_eq = __reduce_add_sync(0xFFFFFFFFu, lane_eq);
   if (k >= elig) {
     base_gt = e0;
   } else if (cluster > 1) {
-    const uint32_t all_gt = __reduce_add_sync(0xFFFFFFFFu, lane_gt);
-    const uint32_t all_eq = __reduce_add_sync(0xFFFFFFFFu, lane_eq);
     // to all of them (which run: the passes had a barrier), so that none has to stay for reads
     if (threadIdx.x < cluster) st_cluster_u2(cluster_map(s_count[rank], threadIdx.x), all_gt, all_eq);
     cluster_sync();
     base_gt = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? s_count[lane][0] : 0u);
     base_eq = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? s_count[lane][1] : 0u);
   }
+  first_kept = base_gt + min(base_eq, need);
+  kept_here = base_gt + all_gt + min(base_eq + all_eq, need) - first_kept;
   for (int round = 0; round < rounds; ++round) {
     uint32_t warp_gt, warp_eq;          // before this warp's
     if (rounds > 1) {  // the round's own counts
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       if (o < total && at < static_cast<uint32_t>(k)) {  // (more only if the scores change meanwhile)
         const int pos = e0 + w0 + 32 * i + bit;
         kept[at] = pos;
-        if (FUSED) s_kept[at] = pos;
+        if (FUSED) s_kept[at - first_kept] = pos;
         if (score_out != nullptr) score_out[at] = __ldg(score + pos);
       }
     }
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   if constexpr (FUSED) {
     __syncthreads();
     const int mine = pages_of(a, fresh);
-    if (g == 0 && threadIdx.x < 32) {
+    if (g == 0 && rank == 0 && threadIdx.x < 32) {
       bool bad = n < 0;
       for (int j = lane; j <= mine; j += 32) bad |= s_bad[j] != 0;
       bad = __any_sync(0xFFFFFFFFu, bad);
@@ -471,9 +473,15 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     }
     const int shift = a.row_bytes == 256 ? 4 : a.row_bytes == 128 ? 3 : 2;  // 16-byte pieces a row
     const int mask = (1 << a.page_shift) - 1;
+    // the recent tokens are dealt out evenly
+    const int r0 = rank * recent / cluster, r1 = (rank + 1) * recent / cluster;
+    const int items = kept_here + r1 - r0;
 #pragma unroll 4
-    for (int u = threadIdx.x; u < fresh << shift; u += kSelThreads) {
-      const int i = u >> shift, c = u & ((1 << shift) - 1), pos = s_kept[i];
+    for (int u = threadIdx.x; u < items << shift; u += kSelThreads) {
+      const int at = u >> shift, c = u & ((1 << shift) - 1);
+      const bool old = at < kept_here;
+      const int i = old ? first_kept + at : k + r0 + at - kept_here;
+      const int pos = old ? s_kept[at] : elig + r0 + at - kept_here;
       if (pos < 0 || pos >= n) continue;  // only if the scores changed meanwhile
       const int from = __ldg(a.table + b * a.max_pages + (pos >> a.page_shift));
       if (s_bad[i >> a.page_shift] || from < 0 || from >= a.num_pages) continue;
@@ -575,28 +583,44 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   const int most = a.budget < a.max_len ? a.budget : a.max_len;
   const int64_t own = (most + page - 1) / page;
   const int64_t others = a.num_seqs * (own + (a.same_pool ? (a.max_len + page - 1) / page : 0));
-  // (every CTA compares its `own` pages with all the `others`)
-  if (a.max_len <= kSmallKeys && most <= kSmallKept && others <= 1024 && own * others <= 65536) {
-    evict_select_kernel<4, false, true><<<static_cast<unsigned>(pairs), kSelThreads, 0, stream>>>(a, 1, 0, 0);
-    return cudaGetLastError();
-  }
   cudaError_t e = cudaSuccess;
-  // CTAs per (sequence, head): enough to hold the keys, and more while SMs are idle and a
-  // CTA has thousands of keys
   int cluster = 1;
-  while (cluster < kMaxCluster &&
-         (a.max_len > static_cast<int64_t>(kSelThreads) * kMaxKeys * cluster ||
-          (pairs * cluster * 2 <= num_sms && a.max_len > 2048 * cluster)))
-    cluster *= 2;
-  const int per = (a.max_len + cluster - 1) / cluster;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.stream = stream;
   cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kSelThreads);
+  // One launch: up to 2,048 tokens per CTA. Few tokens that stay may lie in one CTA's hands, whose
+  // moving them alone is slow, so with clusters at most 128 per CTA stay, and idle SMs join in.
+  // Measured against two launches (8 KV heads, d = 128): one sequence of 4,000 to 128 10.5 us
+  // and 11.9, to 1,000 12.7 and 13.0, one of 16,000 to 500 11.2 and 12.8, four of 16,000 (e4m3)
+  // to 1,000 15.8 and 20.1; past the rule, one of 8,000 to 2,000 15.4 and 13.5, of 16,000 to
+  // 4,000 26 and 18; and 2 us less on the host.
+  const bool brief = a.max_len <= kSmallKeys && most <= kSmallKept;
+  while (cluster < kMaxCluster && (a.max_len > kSmallKeys * cluster ||
+                                   (pairs * cluster * 2 <= num_sms && most > 128 * cluster)))
+    cluster *= 2;
+  // (every CTA compares its `own` pages with all the `others`)
+  if (a.max_len <= kSmallKeys * cluster && (brief || most <= 128 * cluster) &&
+      (cluster == 1 || pairs * cluster <= 2 * num_sms) && others <= 1024 && own * others <= 65536) {
+    attr[0].val.clusterDim.x = cluster;
+    cfg.numAttrs = cluster > 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<4, false, true>, a, cluster, 0, 0);
+  }
+  // CTAs per (sequence, head): enough to hold the keys, and more while SMs are idle and a
+  // CTA has thousands of keys
+  cluster = 1;
+  while (cluster < kMaxCluster &&
+         (a.max_len > static_cast<int64_t>(kSelThreads) * kMaxKeys * cluster ||
+          (pairs * cluster * 2 <= num_sms && a.max_len > 2048 * cluster)))
+    cluster *= 2;
+  const int per = (a.max_len + cluster - 1) / cluster;
+  attr[0].val.clusterDim.x = cluster;
   cfg.numAttrs = 1;
   // The notes have blocks of their own in front, up to 32 (the claims' fences and exchanges
   // would keep one head's selection, and so its cluster, 2 us longer).
@@ -606,7 +630,6 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   while (note_blocks < 32 && note_blocks * kSelWarps < a.num_seqs * static_cast<int64_t>(note_chunks))
     note_blocks += cluster;
   cfg.gridDim = dim3(static_cast<unsigned>(note_blocks + pairs * cluster));
-  cfg.blockDim = dim3(kSelThreads);
   if (per <= 4 * kSelThreads) {
     e = cudaLaunchKernelEx(&cfg, evict_select_kernel<4, false, false>, a, cluster, note_blocks,
                            note_chunks);

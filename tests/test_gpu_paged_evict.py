@@ -107,7 +107,7 @@ def check(cache, score, budget, recent, got, only=None):
                 np.testing.assert_array_equal(y[z, g], x[a, g])
 
 
-@pytest.mark.parametrize("most", [0, 3000])    # (0: the longest; see below)
+@pytest.mark.parametrize("most", [0, 3000, 20000])    # (0: the longest; see below)
 @pytest.mark.parametrize("name", list(CASES))
 @pytest.mark.parametrize("kind", ["heavy", "ties", "equal", "special"])
 @pytest.mark.parametrize("fp8", [False, True])
@@ -127,6 +127,9 @@ def test_cases(name, kind, fp8, most):
     ([400003, 3, 262144], 30000, 1000, 1),
     ([5000] * 40, 1000, 16, 4),    # one CTA each
     ([20481, 20480, 4097], 20480, 0, 2),
+    ([16384, 9000, 5], 1024, 100, 1),  # one launch of clusters of eight
+    ([16000, 900, 1024], 1000, 990, 1),
+    ([4096, 2049, 256, 300], 256, 17, 2),  # and of two
 ])
 @pytest.mark.parametrize("kind", ["heavy", "normal", "equal"])
 def test_long(lens, budget, recent, hkv, kind):
@@ -137,8 +140,8 @@ def test_long(lens, budget, recent, hkv, kind):
     check(cache, score, budget, recent, got)
 
 
-# max_seq_len 200: one launch; 3,000: select and copy are two
-@pytest.mark.parametrize("most", [200, 3000])
+# max_seq_len 200: one launch; 3,000: one of clusters; 20,000: select and copy are two
+@pytest.mark.parametrize("most", [200, 3000, 20000])
 def test_same_pool_and_shared_source_pages(most):
     cache = Cache([200, 200, 90], 2, 128, 16, False, width=-(-most // 16))
     cache.table_np[1, :6] = cache.table_np[0, :6]       # a shared prefix
@@ -149,7 +152,7 @@ def test_same_pool_and_shared_source_pages(most):
     check(cache, score, 64, 8, got)
 
 
-@pytest.mark.parametrize("most", [200, 3000])
+@pytest.mark.parametrize("most", [200, 3000, 20000])
 @pytest.mark.parametrize("where", ["twice", "itself", "held", "outside"])
 def test_destination_pages_that_break_the_rules(where, most):
     """The sequences concerned end with -1 and nothing written there; the others are right."""
@@ -181,7 +184,7 @@ def test_destination_pages_that_break_the_rules(where, most):
     assert torch.equal(cache.k[:before.shape[0]].view(torch.int16), before.view(torch.int16))
 
 
-@pytest.mark.parametrize("most", [200, 3000])
+@pytest.mark.parametrize("most", [200, 3000, 20000])
 def test_bad_sources_and_lengths(most):
     cache = Cache([200, 150, 90, 60], 2, 128, 16, False, width=-(-most // 16))
     score = scores_for(cache.lens, 2, most, "normal")
