@@ -184,6 +184,29 @@ def test_destination_pages_that_break_the_rules(where, most):
     assert torch.equal(cache.k[:before.shape[0]].view(torch.int16), before.view(torch.int16))
 
 
+@pytest.mark.parametrize("most", [100, 20000])
+def test_many_sequences(most):
+    """More tables than the blocks that look them over take at once; two sequences that claim
+    one page."""
+    rng = np.random.default_rng(2)
+    lens = rng.integers(0, 101, 700).tolist()
+    lens[3], lens[699] = 80, 90
+    cache = Cache(lens, 1, 64, 16, False, width=-(-most // 16))
+    score = scores_for(lens, 1, most, "normal")
+
+    def spoil(table):
+        table = table.copy()
+        table[699, 1] = table[3, 2]
+        return table
+
+    got = run(cache, score, 40, 4, dst="same", dst_table=spoil, max_len=most)
+    torch.cuda.synchronize()
+    assert q.get_device_error() == q.QUAIL_ERR_DEVICE_BOUNDS
+    new = got[1].tolist()
+    assert new[3] == new[699] == -1
+    check(cache, score, 40, 4, got, only=set(range(700)) - {3, 699})
+
+
 @pytest.mark.parametrize("most", [200, 3000, 20000])
 def test_bad_sources_and_lengths(most):
     cache = Cache([200, 150, 90, 60], 2, 128, 16, False, width=-(-most // 16))
