@@ -74,7 +74,8 @@ DecodeLayout decode_layout(const quail_paged_desc& d, bool with_scores) {
   const int tile = quail::decode_tile_keys(d.head_dim, fp8);
   const size_t parts = 2 * static_cast<size_t>(quail::decode_ctas(
                                quail::kDecodeMaxCtas, d.num_seqs, d.num_kv_heads, d.max_seq_len,
-                               tile));
+                               tile)) *
+                       (quail::decode_by_warps(d.num_seqs, d.num_kv_heads, d.max_seq_len, tile) ? 4 : 1);
   DecodeLayout l;
   l.raw_stride = (static_cast<int64_t>(d.max_seq_len) + tile - 1) / tile * tile;
   l.rec = 0;

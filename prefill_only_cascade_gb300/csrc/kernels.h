@@ -190,7 +190,7 @@ struct PagedAppendArgs {
 cudaError_t launch_paged_append(const PagedAppendArgs& a, bool fp8, int num_sms,
                                 cudaStream_t stream);
 
-// What a CTA of the decode attention leaves for the join: the (sequence, head) that begins
+// What a CTA (or a warp, see decode_by_warps) of the decode attention leaves for the join: the (sequence, head) that begins
 // in it and goes on in the next CTAs (seq < 0: none) up to CTA `last`; sparse: the number of
 // tiles where there are fewer than CTAs (some then have none), else 0.
 struct DecodeRec {
@@ -227,6 +227,8 @@ struct PagedDecodeArgs {
 constexpr int kDecodeMaxCtas = 320;
 int decode_tile_keys(int head_dim, bool fp8);
 int decode_ctas(int num_sms, int num_seqs, int hkv, int max_len, int tile);
+// Whether runs are dealt to warps, four per CTA (the workspace then holds four times the parts).
+bool decode_by_warps(int num_seqs, int hkv, int max_len, int tile);
 cudaError_t launch_paged_decode(PagedDecodeArgs& a, int head_dim, bool fp8, int num_sms,
                                 cudaStream_t stream);
 

@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 // rows come through a ring of its own in shared memory, filled by 16-byte asynchronous
 // copies two steps (16 KB a warp, 128 KB an SM) ahead, also over the borders between
 // sequences and heads, so the loads never wait for the arithmetic. No warp waits for
-// another but where the parts of a (sequence, head) are put together.
+// another but where the parts of a (sequence, head) are put together. Where there are many and
+// none can be long, the runs are dealt to the warps themselves (kWarps), and none waits at all.
 //
 // Both products run on mma.sync m16n8k16: one new token gives at most 16 query rows per KV
 // head, so the padded products cost a few per cent of the tensor rate of the legacy pipe.
@@ -370,10 +371,19 @@ __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
   return v;
 }
 
-template <int D, bool FP8, int NT, bool ONE>
+// How the tiles are dealt out.
+enum DecMode {
+  kSplit,  // runs of CTA tiles, a run per CTA
+  kOne,    // one launch: a cluster per (sequence, head)
+  kWarps   // runs of a warp's steps, a run per warp: no warp waits for another
+};
+
+template <int D, bool FP8, int NT, DecMode MODE>
 __global__ void __launch_bounds__(kDecThreads, 2)
     paged_decode_kernel(const PagedDecodeArgs a, int cluster) {
   using C = DecCfg<D, FP8>;
+  constexpr bool ONE = MODE == kOne, WARPS = MODE == kWarps;
+  constexpr int kTile = WARPS ? C::kKeys : C::kTile;  // keys that a run is counted in
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ float s_m[kDecWarps][8 * NT], s_l[kDecWarps][8 * NT];
   __shared__ int s_bad[kDecWarps];
@@ -384,8 +394,10 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, q4 = lane & 3;
   const int G = a.group;
-  const int cta = ONE ? static_cast<int>(blockIdx.x) % cluster : blockIdx.x;  // ONE: the rank
-  const int ctas = gridDim.x;
+  // who takes a run (a CTA, a warp), or ONE: the rank
+  const int cta = ONE ? static_cast<int>(blockIdx.x) % cluster
+                      : WARPS ? static_cast<int>(blockIdx.x) * kDecWarps + warp : blockIdx.x;
+  const int ctas = WARPS ? static_cast<int>(gridDim.x) * kDecWarps : gridDim.x;
   Piece cur;
   int64_t run_end, run_total = 0;
   if constexpr (ONE) {
@@ -404,36 +416,37 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   } else {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // sequences without tokens (0 and -inf) and with lengths out of range (NaN)
-    for (int b = cta; b < a.num_seqs; b += ctas) {
+    for (int b = blockIdx.x; b < a.num_seqs; b += gridDim.x) {
       const int n = checked_len(a, b);
       if (n <= 0) write_empty(a, b, n, 0, a.hq, D);
     }
-    const RunStart run = find_run(a, C::kTile, cta, ctas);
-    if (threadIdx.x == 0) a.rec[cta] = DecodeRec{-1, 0, 0, 0};
+    const RunStart run = find_run(a, kTile, cta, ctas);
+    if (WARPS ? lane == 0 : threadIdx.x == 0) a.rec[cta] = DecodeRec{-1, 0, 0, 0};
     if (run.begin >= run.end) return;
     cur.b = run.seq;
     cur.len = checked_len(a, cur.b);
-    const int tiles = (cur.len + C::kTile - 1) / C::kTile;
+    const int tiles = (cur.len + kTile - 1) / kTile;
     cur.g = static_cast<int>((run.begin - run.seq_tile0) / tiles);
     cur.piece0 = run.seq_tile0 + static_cast<int64_t>(cur.g) * tiles;
     cur.at = run.begin;
     run_end = run.end;
     run_total = run.total;
   }
-  set_piece<C::kTile>(a, run_end, cur);
+  set_piece<kTile>(a, run_end, cur);
 
   // ------------------------------------------------------ loads: a cursor of their own
   const int64_t row_stride = static_cast<int64_t>(a.hkv) * C::kRB;
   const uint32_t ring = smem_u32(dyn) + warp * (kStages * 2 * kStepBytes);
   Piece ld = cur;
-  int ld_key = ld.kb + warp * C::kKeys;  // first key of the next step to load
+  const int own = WARPS ? 0 : warp * C::kKeys;  // the warp's first key in a tile
+  int ld_key = ld.kb + own;              // first key of the next step to load
   bool ld_more = true;
   int page[C::kSteps16];                 // pages of its 16-key blocks
   uint32_t bad_steps = 0;                // bit s: a page of the step in stage s is no page
   auto seek = [&]() {                    // on to a piece that has a step for this warp
     while (ld_more && ld_key >= ld.ke) {
-      ld_more = next_piece<C::kTile>(a, run_end, ld);
-      ld_key = ld.kb + warp * C::kKeys;
+      ld_more = next_piece<kTile>(a, run_end, ld);
+      ld_key = ld.kb + own;
     }
     if (ld_more) {
       const int32_t* table = a.table + static_cast<int64_t>(ld.b) * a.max_pages;
@@ -471,7 +484,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         copy16(vdst + 16 * v_place<C::kNC>(row, c), a.v_pages + off, real);
       }
       bad_steps = bad ? bad_steps | (1u << stage) : bad_steps & ~(1u << stage);
-      ld_key += C::kTile;
+      ld_key += kTile;
       seek();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -551,7 +564,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     }
     bool bad = false;
 
-    for (int key0 = cur.kb + warp * C::kKeys; key0 < cur.ke; key0 += C::kTile) {
+    for (int key0 = cur.kb + own; key0 < cur.ke; key0 += kTile) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();  // every lane's copies are there, and the stage before was read
       bad |= (bad_steps >> stage) & 1u;
@@ -712,15 +725,70 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 
     // the next piece's queries are on their way while this one is put together
     Piece nxt = cur;
-    const bool more = !ONE && next_piece<C::kTile>(a, run_end, nxt);
+    const bool more = !ONE && next_piece<kTile>(a, run_end, nxt);
     if (more) load_q(nxt.b, nxt.g);
 
     // ---------------------------------------------------- the four warps' parts together
     const float vs = FP8 ? __ldg(a.v_scale + static_cast<int64_t>(cur.b) * a.hkv + cur.g) : 1.f;
     // slot 0: the run began inside this (b, g); slot 1: the run's last, begun here
     const int64_t part = 2 * static_cast<int64_t>(cta) + (cur.at == cur.piece0 ? 1 : 0);
+    auto note = [&](bool any_bad) {      // by one thread, about (b, g)
+      if (any_bad) atomicOr(a.err_word, kErrDeviceBounds);
+      if (ONE || cur.at != cur.piece0) return;
+      if (a.begun != nullptr)
+        a.begun[static_cast<int64_t>(cur.b) * a.hkv + cur.g] = cur.whole ? -1 : cta;
+      if (!cur.whole) {  // goes on in the next runs: the join's entry
+        const int64_t end = cur.piece0 + (cur.len + kTile - 1) / kTile;
+        // the last run of (b, g) is the one that holds tile end - 1
+        a.rec[cta] = DecodeRec{cur.b, cur.g, static_cast<int>((end * ctas - 1) / run_total),
+                               run_total < ctas ? static_cast<int>(run_total) : 0};
+      }
+    };
+    if constexpr (WARPS) {
+      if (lane == 0) note(bad);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NT; ++n) {
+        l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 1);
+        l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 2);
+        if (bad) l[n] = __int_as_float(0x7FFFFFFF);
+        const int64_t row = static_cast<int64_t>(cur.b) * a.hq + cur.g * G + 8 * n;
+        if (q4 == 0 && r + 8 * n < G) {
+          if (cur.whole) {
+            const float lse2 = m[n] + (log2f(l[n]) - (FP8 ? 14.f : 0.f));
+            if (a.lse != nullptr) a.lse[row + r] = lse2 * 0.6931471805599453f;
+            if (a.lse2 != nullptr) a.lse2[row + r] = lse2;
+          } else {
+            a.part_ml[part * G + 8 * n + r] = make_float2(m[n], l[n]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // the lane's output rows are heads 2 q4 and 2 q4 + 1
+          const float sum = __shfl_sync(0xFFFFFFFFu, l[n], 8 * q4 + 4 * h);
+          const int hh = 2 * q4 + h;
+          if (8 * n + hh >= G) continue;
+          const float inv = vs / sum;
+#pragma unroll
+          for (int t = 0; t < C::kMT; t += 4) {  // eight neighbouring d
+            const int d = out_d<D, FP8>(r, t);
+            if (cur.whole) {
+              uint4 x;
+              x.x = pack2<false>(o[n][t][h] * inv, o[n][t][h + 2] * inv);
+              x.y = pack2<false>(o[n][t + 1][h] * inv, o[n][t + 1][h + 2] * inv);
+              x.z = pack2<false>(o[n][t + 2][h] * inv, o[n][t + 2][h + 2] * inv);
+              x.w = pack2<false>(o[n][t + 3][h] * inv, o[n][t + 3][h + 2] * inv);
+              *reinterpret_cast<uint4*>(a.out + (row + hh) * D + d) = x;
+            } else {
+              float4* to = reinterpret_cast<float4*>(a.part_o + (part * G + 8 * n + hh) * D + d);
+              to[0] = make_float4(o[n][t][h], o[n][t][h + 2], o[n][t + 1][h], o[n][t + 1][h + 2]);
+              to[1] = make_float4(o[n][t + 2][h], o[n][t + 2][h + 2], o[n][t + 3][h],
+                                  o[n][t + 3][h + 2]);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < (WARPS ? 0 : NT); ++n) {
       l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 1);
       l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 2);
       if (q4 == 0) {
@@ -766,17 +834,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           if (d == 0) a.part_ml[part * G + hh] = make_float2(top, sum);
         }
       }
-      if (n == 0 && threadIdx.x == 0) {
-        if (any_bad) atomicOr(a.err_word, kErrDeviceBounds);
-        if (!ONE && a.begun != nullptr && cur.at == cur.piece0)
-          a.begun[static_cast<int64_t>(cur.b) * a.hkv + cur.g] = cur.whole ? -1 : cta;
-        if (!ONE && !cur.whole && cur.at == cur.piece0) {  // goes on in the next CTAs: the join's entry
-          const int64_t end = cur.piece0 + (cur.len + C::kTile - 1) / C::kTile;
-          // the last CTA of (b, g) is the one that holds tile end - 1
-          a.rec[cta] = DecodeRec{cur.b, cur.g, static_cast<int>((end * ctas - 1) / run_total),
-                                 run_total < ctas ? static_cast<int>(run_total) : 0};
-        }
-      }
+      if (n == 0 && threadIdx.x == 0) note(any_bad);
       __syncthreads();  // the shared parts may be overwritten
     }
     if constexpr (ONE) break;
@@ -1097,7 +1155,7 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
   while (cluster < kOneCluster && cluster < tiles) cluster *= 2;
   if (tiles <= 8 * cluster && pairs * cluster <= 2 * num_sms) {
     static std::atomic<uint64_t> one_ready{0};
-    e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT, true>), C::kSmem,
+    e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT, kOne>), C::kSmem,
                    one_ready);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute dims;
@@ -1112,14 +1170,26 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
     one.stream = stream;
     one.attrs = &dims;
     one.numAttrs = 1;
-    return cudaLaunchKernelEx(&one, paged_decode_kernel<D, FP8, NT, true>, a, cluster);
+    return cudaLaunchKernelEx(&one, paged_decode_kernel<D, FP8, NT, kOne>, a, cluster);
   }
+  // runs of warps or of CTAs
+  const bool warps = decode_by_warps(a.num_seqs, a.hkv, a.max_len, C::kTile);
+  const int tile = warps ? C::kKeys : C::kTile;
   const int ctas = decode_ctas(num_sms, a.num_seqs, a.hkv, a.max_len, C::kTile);
-  static std::atomic<uint64_t> ready{0};
-  e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT, false>), C::kSmem,
-                 ready);
-  if (e != cudaSuccess) return e;
-  paged_decode_kernel<D, FP8, NT, false><<<ctas, kDecThreads, C::kSmem, stream>>>(a, 1);
+  const int runs = warps ? ctas * kDecWarps : ctas;
+  if (warps) {
+    static std::atomic<uint64_t> warps_ready{0};
+    e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT, kWarps>), C::kRing,
+                   warps_ready);
+    if (e != cudaSuccess) return e;
+    paged_decode_kernel<D, FP8, NT, kWarps><<<ctas, kDecThreads, C::kRing, stream>>>(a, 1);
+  } else {
+    static std::atomic<uint64_t> ready{0};
+    e = allow_smem(reinterpret_cast<const void*>(paged_decode_kernel<D, FP8, NT, kSplit>), C::kSmem,
+                   ready);
+    if (e != cudaSuccess) return e;
+    paged_decode_kernel<D, FP8, NT, kSplit><<<ctas, kDecThreads, C::kSmem, stream>>>(a, 1);
+  }
   e = cudaGetLastError();
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1129,8 +1199,8 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   // left out where no (sequence, head) can have more than one tile and no weights are wanted
-  if (e == cudaSuccess && (a.max_len > C::kTile || (a.raw != nullptr && a.max_len > 0))) {
-    int64_t blocks = ctas;
+  if (e == cudaSuccess && (a.max_len > tile || (a.raw != nullptr && a.max_len > 0))) {
+    int64_t blocks = runs;
     int chunks = 1;
     if (a.raw != nullptr) {
       const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
@@ -1143,7 +1213,7 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
     }
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(kFinishThreads);
-    e = cudaLaunchKernelEx(&cfg, paged_finish_kernel<D>, a, ctas, FP8 ? 14.f : 0.f, chunks);
+    e = cudaLaunchKernelEx(&cfg, paged_finish_kernel<D>, a, runs, FP8 ? 14.f : 0.f, chunks);
   }
   return e;
 }
@@ -1152,6 +1222,15 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
 
 int decode_tile_keys(int head_dim, bool fp8) {
   return kDecWarps * kStepBytes / (head_dim * (fp8 ? 1 : 2));
+}
+
+// Where a CTA has several short pieces in its run, putting its warps' parts together is what
+// takes the time (8 us a piece). Measured against runs of CTAs: 181 sequences of 20-83 tokens
+// (8 KV heads, G = 16, e4m3) 25.7 us and 38.6, 256 of 16-128 (8, G = 4) 27.7 and 37.3, 100 of
+// 100-500 (8, G = 8) 33.1 and 38.2, 128 of 300-600 (8, G = 4, e4m3) 33.6 and 36.8; past the rule,
+// 93 of 431-589 42.6 and 41.0, 128 of 500-1,000 71.8 and 68.5 (parts of more runs to join).
+bool decode_by_warps(int num_seqs, int hkv, int max_len, int tile) {
+  return static_cast<int64_t>(num_seqs) * hkv >= 2 * kDecodeMaxCtas && max_len <= 8 * tile;
 }
 
 int decode_ctas(int num_sms, int num_seqs, int hkv, int max_len, int tile) {

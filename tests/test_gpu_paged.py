@@ -60,6 +60,52 @@ def test_splits(lens, d, fp8):
     check_decode(cache, qt, 8, out, lse, score, score_in)
 
 
+@pytest.mark.parametrize("hq,hkv,B", [(2, 2, 320), (8, 4, 170), (4, 1, 640), (32, 4, 165), (16, 1, 700)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scored", [False, True])
+def test_many_short_sequences(hq, hkv, B, d, fp8, scored):
+    """At least 640 (sequence, head)s of at most 512 tokens: runs of warps."""
+    rng = np.random.default_rng(hq + d)
+    lens = rng.integers(0, 120, B).tolist()
+    for b, n in ((0, 1), (1, 512), (2, 0), (5, 400), (B // 2, 257), (B - 2, 64), (B - 1, 499)):
+        lens[b] = n
+    cache = Cache(lens, hkv, d, 16 if d == 64 else 64, fp8, seed=hq)
+    qt = queries(B, hq, d, seed=d)
+    base = torch.rand(B, hkv, 512 + 5, device=DEV) if scored else None
+    out, lse, score = run_decode(cache, qt, hq, scored, base)
+    ok()
+    some = {0, 1, 2, 3, 4, 5, B // 2, B - 2, B - 1} | set(rng.integers(0, B, 25).tolist())
+    check_decode(cache, qt, hq, out, lse, score, base, only=some)
+    again = run_decode(cache, qt, hq, scored, base)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    # a larger bound on the lengths takes the CTAs' runs; each within the bound of the true value
+    wide = Cache(lens, hkv, d, cache.page, fp8, seed=hq, width=-(-2049 // cache.page))
+    other = run_decode(wide, qt, hq, max_len=2049)
+    ok()
+    assert torch.allclose(out.float(), other[0].float(), rtol=2 ** -6, atol=2 ** -7)
+    assert torch.allclose(lse, other[1], rtol=0, atol=1e-4)
+
+
+def test_many_short_sequences_with_bad_pages_and_lengths():
+    lens = [50] * 700
+    cache = Cache(lens, 1, 64, 16, False)
+    table = cache.table_np.copy()
+    table[10, 1], table[699, 3], table[300, 0] = cache.pages, -1, 1 << 30
+    cache.table = torch.from_numpy(table).to(DEV)
+    n = torch.tensor(lens, dtype=torch.int32)
+    n[20], n[400] = -1, 51
+    cache.seq_lens = n.to(DEV)
+    qt = queries(700, 4, 64)
+    out, lse, score = run_decode(cache, qt, 4, True)
+    torch.cuda.synchronize()
+    assert q.get_device_error() == q.QUAIL_ERR_DEVICE_BOUNDS
+    bad = [10, 20, 300, 400, 699]
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    assert (score[[20, 400]] == -3.0).all() and (score[[10, 300, 699], :, :50] == 0).all()
+    check_decode(cache, qt, 4, out, lse, score, only=[0, 9, 11, 19, 21, 299, 301, 399, 401, 698])
+
+
 def test_weights_into_their_own_buffer_and_repeatable():
     cache = Cache([500, 31, 0, 3000], 2, 128, 32, False)
     qt = queries(4, 8, 128)
