@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "kernels.h"
@@ -153,10 +154,14 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 //   O^T [16 d x 8 heads]    A = V^T: lane (r, q) holds keys 2q, 2q+1, 2q+8, 2q+9, piece r
 //                           (two keys' values interleaved by byte permutes), B = P, whose
 //                           fragment is the score fragment packed in place
-// bf16 pages: bf16 products, P as the sum of two bf16 (hi + lo: 16 bits of P). e4m3 pages:
-// f16 products (codes are exact in f16), P in f16 (11 bits, scaled by 2^14 so that weights
-// down to 2^-38 of the largest count), Q scaled per head by a power of two into f16's
+// bf16 pages: bf16 products, P as the sum of three bf16 (all 24 bits of P). e4m3 pages: f16
+// products (codes are exact in f16), P as the sum of two f16 (22 bits, scaled by 2^14 so that
+// weights down to 2^-38 of the largest count), Q scaled per head by a power of two into f16's
 // range: q bits below 2^-38 of the head's largest |q| are lost, under fp32's own rounding.
+// Against fewer terms of P (two bf16, 16 bits; one f16, 11 bits), whose errors showed in the last
+// bit of one output in a few hundred: 64 sequences of 128-4,096 tokens (G = 4, bf16) 90.4 -> 90.8 us,
+// one of 131,007 86.7 -> 87.2, of 777 5.9 -> 6.1, 32 of 2,048-8,192 (e4m3) 69.1 -> 69.7; the tensor
+// pipe shows with 16 heads per KV head only: 117 -> 120.5 (bf16), 77.6 -> 87 (e4m3).
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 
@@ -175,6 +180,7 @@ struct DecCfg {
   static constexpr int kTile = kDecWarps * kKeys;    // keys per CTA tile
   static constexpr int kMT = D / 16;                 // 16-row tiles of O^T
   static constexpr int kQS = D / 16;                 // k-steps of the score product
+  static constexpr int kTerms = FP8 ? 2 : 3;         // P as a sum of so many 16-bit values
   static constexpr int kRing = kDecWarps * kStages * 2 * kStepBytes;
   static constexpr int kSmem = kRing + kDecWarps * 8 * D * 4;  // + the warps' O, 8 heads
 };
@@ -255,6 +261,24 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// x = hi + lo in f16: 22 bits, down to f16's smallest step.
+__device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack2<true>(x0, x1);
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  lo = pack2<true>(x0 - h.x, x1 - h.y);
+}
+// x = hi + mid + lo in bf16: all 24 bits, 8 at a time from the top.
+__device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& mid,
+                                           uint32_t& lo) {
+  auto top = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); };
+  auto tops = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); };
+  hi = tops(x0, x1);
+  x0 -= top(x0);
+  x1 -= top(x1);
+  mid = tops(x0, x1);
+  lo = tops(x0 - top(x0), x1 - top(x1));
 }
 
 // The d of lane row r's first output row in tile t (its second is the next d).
@@ -660,18 +684,20 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       }
 
       // ---- O^T += V^T P^T
+      constexpr int kTerms = C::kTerms;
 #pragma unroll
       for (int i = 0; i < C::kSteps16; ++i) {
-        uint32_t hi[NT][2], lo[NT][2];
+        uint32_t ps[NT][kTerms][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float* x = p[n][2 * i + h];
-            hi[n][h] = pack2<FP8>(x[0], x[1]);
-            lo[n][h] = FP8 ? 0u
-                           : pack2<false>(x[0] - __uint_as_float(hi[n][h] << 16),
-                                          x[1] - __uint_as_float(hi[n][h] & 0xFFFF0000u));
+            if constexpr (FP8) {
+              split_f16(x[0], x[1], ps[n][0][h], ps[n][1][h]);
+            } else {
+              split_bf16(x[0], x[1], ps[n][0][h], ps[n][1][h], ps[n][2][h]);
+            }
           }
         constexpr int kParts = C::kNC == 16 ? 2 : 1;  // 16-byte (or one 8-byte) parts of a lane
         constexpr int kWords = C::kNC == 4 ? 2 : 4;
@@ -703,9 +729,11 @@ __global__ void __launch_bounds__(kDecThreads, 2)
                 const uint32_t x = __byte_perm(w[0][k], w[1][k], sel);
                 const uint32_t y = __byte_perm(w[2][k], w[3][k], sel);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                  mma16816<true>(o[n][2 * k + h], e4m3_lo(x), e4m3_hi(x), e4m3_lo(y), e4m3_hi(y),
-                                 hi[n][0], hi[n][1]);
+                for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+                    mma16816<true>(o[n][2 * k + h], e4m3_lo(x), e4m3_hi(x), e4m3_lo(y), e4m3_hi(y),
+                                   ps[n][t][0], ps[n][t][1]);
               }
             } else {
               const uint32_t a0 = __byte_perm(w[0][k], w[1][k], 0x5410);
@@ -713,10 +741,10 @@ __global__ void __launch_bounds__(kDecThreads, 2)
               const uint32_t a2 = __byte_perm(w[2][k], w[3][k], 0x5410);
               const uint32_t a3 = __byte_perm(w[2][k], w[3][k], 0x7632);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                mma16816<false>(o[n][4 * part + k], a0, a1, a2, a3, hi[n][0], hi[n][1]);
-                mma16816<false>(o[n][4 * part + k], a0, a1, a2, a3, lo[n][0], lo[n][1]);
-              }
+              for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  mma16816<false>(o[n][4 * part + k], a0, a1, a2, a3, ps[n][t][0], ps[n][t][1]);
             }
           }
         }
