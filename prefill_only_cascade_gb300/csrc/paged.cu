@@ -269,7 +269,19 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
   lo = pack2<true>(x0 - h.x, x1 - h.y);
 }
-// x = hi + mid + lo in bf16: all 24 bits, 8 at a time from the top.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// x = hi + mid + lo in bf16: all 24 bits, 8 at a time from the top. Where mid and lo are zero they
+// take 2^-30 of hi (far under fp32's rounding), so that all three of a positive x are positive: an
+// infinite V times zero would be NaN.
 __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& mid,
                                            uint32_t& lo) {
   auto top = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); };
@@ -277,8 +289,9 @@ __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uin
   hi = tops(x0, x1);
   x0 -= top(x0);
   x1 -= top(x1);
-  mid = tops(x0, x1);
-  lo = tops(x0 - top(x0), x1 - top(x1));
+  const uint32_t least = mul_bf16x2(hi, 0x30803080u);
+  mid = max_bf16x2(tops(x0, x1), least);
+  lo = max_bf16x2(tops(x0 - top(x0), x1 - top(x1)), least);
 }
 
 // The d of lane row r's first output row in tile t (its second is the next d).

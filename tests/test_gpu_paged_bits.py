@@ -1,4 +1,4 @@
-"""How many bits the weights of quail_paged_decode_attn keep."""
+"""How many bits the weights of quail_paged_decode_attn keep, and what an infinite V gives."""
 import math
 
 import numpy as np
@@ -65,3 +65,44 @@ def test_weights_keep_their_bits(d, fp8, hkv, B):
         + 8 * U32 * size
     assert (np.abs(got - ref) <= err + BF16 * (np.abs(ref) + err)).all(), \
         np.max(np.abs(got - ref) / (err + BF16 * (np.abs(ref) + err)))
+
+@pytest.mark.parametrize("hq,hkv,lens", [(8, 2, [40, 777]), (16, 1, [2, 20000]), (4, 1, [70] * 700)])
+def test_infinite_values(hq, hkv, lens):
+    """An infinite V that a query sees makes its column infinite (both signs: NaN), as the sum
+    of the products does; the other columns are as without it."""
+    gen = torch.Generator().manual_seed(3)
+    B, d, page = len(lens), 128, 16
+    width = -(-max(lens) // page)
+    k = torch.randn(B * width, page, hkv, d, generator=gen).bfloat16().to(DEV)
+    v = torch.randn(B * width, page, hkv, d, generator=gen).bfloat16().to(DEV)
+    table = torch.arange(B * width, dtype=torch.int32, device=DEV).view(B, width)
+    qt = (torch.randn(B, hq, d, generator=gen) * 0.3).bfloat16().to(DEV)
+    clean, lse0 = call(qt, k, v, table, lens)
+    rows = v.view(B, width * page, hkv, d)
+    for b, n in enumerate(lens):
+        rows[b, n - 1, :, 3] = math.inf
+        rows[b, 0, :, 60] = -math.inf
+        rows[b, 0, :, 127], rows[b, n - 1, :, 127] = math.inf, -math.inf
+        rows[b, n // 2, :, 90] = math.nan
+    got, lse = call(qt, k, v, table, lens)
+    assert (got[:, :, 3] == math.inf).all() and (got[:, :, 60] == -math.inf).all()
+    assert np.isnan(got[:, :, [90, 127]]).all()
+    rest = [c for c in range(d) if c not in (3, 60, 90, 127)]
+    assert (got[:, :, rest] == clean[:, :, rest]).all() and (lse == lse0).all()
+
+
+def test_values_without_weight():
+    """Keys whose score is -inf have no weight: a finite V of any size adds nothing, also the
+    largest."""
+    B, d, page, n = 2, 64, 16, 40
+    gen = torch.Generator().manual_seed(4)
+    k = torch.randn(B * 3, page, 1, d, generator=gen).bfloat16().to(DEV)
+    v = torch.randn(B * 3, page, 1, d, generator=gen).bfloat16().to(DEV)
+    table = torch.arange(B * 3, dtype=torch.int32, device=DEV).view(B, 3)
+    qt = torch.rand(B, 1, d, generator=gen).add(0.1).bfloat16().to(DEV)
+    k.view(B, 48, 1, d)[:, 10:n] = -math.inf
+    v.view(B, 48, 1, d)[:, 10:n] = 0.0
+    want, lse0 = call(qt, k, v, table, [n, n])
+    v.view(B, 48, 1, d)[:, 10:n] = torch.finfo(torch.bfloat16).max
+    got, lse = call(qt, k, v, table, [n, n])
+    assert (got == want).all() and (lse == lse0).all() and np.isfinite(got).all()
