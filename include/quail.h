@@ -480,7 +480,8 @@ size_t quail_paged_decode_workspace_size(const quail_paged_desc* desc, int32_t w
  *            is left out and QUAIL_ERR_DEVICE_BOUNDS reported)
  *   score_in, score_out [num_seqs, Hkv, score_stride] fp32, score_stride >= max_k_len;
  *            score_in NULL: zeros; both may be the same buffer. Entries past the sequence's
- *            keys are left as they were.
+ *            keys are left as they were, and after QUAIL_ERR_TIMEOUT those of keys whose
+ *            weights are not whole.
  * Limits: d in {64, 128}, Hq/Hkv in {1, 2, 4, 8, 16}.
  */
 quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t total_k_tokens,
@@ -549,8 +550,10 @@ void quail_set_wait_timeout_ns(uint64_t ns);
 
 /*
  * Host-side fault injection for the timeout tests: with `skip_first_kv_load` != 0 the
- * next cascade launches never issue the load of their first KV tile, so the consumer's
- * bounded wait runs out and the launch reports QUAIL_ERR_TIMEOUT. Nothing faults.
+ * next cascade launches never issue the load of their first KV tile, and the next
+ * quail_attn_scores launches never that of a sequence's first keys (where a cluster of CTAs
+ * shares its queries, in the last of them), so the consumer's bounded wait runs out and the
+ * launch reports QUAIL_ERR_TIMEOUT. Nothing faults.
  */
 void quail_debug_inject(int32_t skip_first_kv_load);
 

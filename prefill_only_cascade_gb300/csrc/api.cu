@@ -111,7 +111,7 @@ int quail::current_device_info(DeviceInfo* info) {
   const quail_status s = device_state(&st);
   if (s != QUAIL_OK) return s;
   std::lock_guard<std::mutex> lock(g_mutex);
-  *info = DeviceInfo{st->num_sms, st->err_word, g_timeout_ns};
+  *info = DeviceInfo{st->num_sms, st->err_word, g_timeout_ns, g_inject_skip};
   return QUAIL_OK;
 }
 

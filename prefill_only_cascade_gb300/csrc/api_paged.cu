@@ -297,6 +297,7 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
   a.score_stride = score_stride;
   a.err_word = info.err_word;
   a.timeout_ns = info.timeout_ns;
+  a.inject_skip_first_kv = info.inject_skip_first_kv;
   const cudaError_t e = quail::launch_attn_scores(a, q_map, k_map, head_dim, info.num_sms,
                                                   reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QUAIL_OK : QUAIL_ERR_CUDA;

@@ -164,6 +164,7 @@ struct DeviceInfo {
   int num_sms;
   unsigned* err_word;
   uint64_t timeout_ns;
+  int inject_skip_first_kv;
 };
 // A quail_status; `info` is filled when it is QUAIL_OK.
 int current_device_info(DeviceInfo* info);
@@ -246,6 +247,7 @@ struct AttnScoresArgs {
   int64_t score_stride;
   unsigned* err_word;
   uint64_t timeout_ns;
+  int inject_skip_first_kv;
 };
 cudaError_t launch_attn_scores(const AttnScoresArgs& a, const CUtensorMap& q_map,
                                const CUtensorMap& k_map, int head_dim, int num_sms,

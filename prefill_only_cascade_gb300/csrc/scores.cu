@@ -80,6 +80,7 @@ struct Shared {
   uint64_t s_full[kGroups], s_empty[kGroups];
   uint32_t tmem;
   int abort_flag;
+  uint32_t others_failed;                   // rank 0: a wait ran out in another CTA
   int dead[kQStages];                       // the tile has rows whose lse is -inf
 };
 struct WinShared {
@@ -296,6 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int mine = left > rank ? (left - rank + cluster - 1) / cluster : 0;
   auto tile_at = [&](int i) { return t_first[0] + rank + i * cluster; };
 
+  // fault injection: the first keys never reach the last CTA of a cluster
+  const bool skip_k = a.inject_skip_first_kv != 0 && j0 == 0 && rank == cluster - 1;
   const uint64_t keep = l2_policy_evict_last();   // queries: read by every key tile
   const uint64_t once = l2_policy_evict_first();
   auto load_q = [&](int i) {
@@ -319,10 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.s_empty[i], 128);
     }
     sh.abort_flag = 0;
+    sh.others_failed = 0;
     fence_mbar_init();
     if (mine > 0) {  // the first loads do not wait for the rest of the set-up
-      mbar_arrive_expect_tx(&sh.k_full, kKeyTiles * C::kTileBytes);
-      for (int kt = 0; kt < kKeyTiles; ++kt)  // keys past the tensor read as zeros
+      if (!skip_k) mbar_arrive_expect_tx(&sh.k_full, kKeyTiles * C::kTileBytes);
+      for (int kt = 0; kt < (skip_k ? 0 : kKeyTiles); ++kt)  // keys past the tensor read as zeros
         for (int kb = 0; kb < C::kKB; ++kb)
           tma_load_3d_hint(&k_map, &sh.k_full, s_k + kt * C::kTileBytes + kb * kBlock, kb * 64, g,
                            static_cast<int>(sr.k0) + j0 + kt * kBM, once);
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++armed;
       }
       const uint64_t deadline = global_timer_ns() + 100000000ull;
-      drain(&sh.k_full, 0, deadline);
+      if (!skip_k) drain(&sh.k_full, 0, deadline);
       for (int i = armed > kQStages ? armed - kQStages : 0; i < armed; ++i)
         drain(&sh.q_full[i % kQStages], (i / kQStages) & 1u, deadline);
     }
@@ -480,14 +484,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool owner = warp < kWarpLoad && !((warp >> 2) & 1);  // the even groups
   const int at = (warp >> 3) * kBM + (threadIdx.x & 127);     // key of the thread
   if (owner) total += sh.part[0][at];
+  bool failed = sh.abort_flag != 0;  // a wait ran out: the sums are not whole
   if (cluster > 1) {  // the cluster's sums, added in rank order by its first CTA
     if (rank > 0 && owner) st_cluster_f32(cluster_map(&sh.part[rank][at], 0), total);
+    if (rank > 0 && failed && threadIdx.x == 0) st_cluster_u32(cluster_map(&sh.others_failed, 0), 1u);
     cluster_sync();
     if (rank > 0) return;
+    failed |= sh.others_failed != 0;
     if (owner)
       for (int r = 1; r < cluster; ++r) total += sh.part[r][at];
   }
-  if (owner && j0 + at < sr.nk) {
+  if (owner && !failed && j0 + at < sr.nk) {
     const int64_t out = (static_cast<int64_t>(s) * a.hkv + g) * a.score_stride + j0 + at;
     a.score_out[out] = a.score_in != nullptr ? a.score_in[out] + total : total;
   }
@@ -528,6 +535,7 @@ __global__ void __launch_bounds__(Win<QT>::kThreads, QT == 1 ? 2 : 1)
 
   const int tok = kBN / G, q_tiles = (sr.w + tok - 1) / tok;  // at most QT
   const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+  const int k_skip = a.inject_skip_first_kv != 0 && j0 == 0;  // fault injection: without tile 0
   auto load_k = [&](int i) {
     const int st = i % W::kStages;
     mbar_arrive_expect_tx(&sh.k_full[st], C::kTileBytes);
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(Win<QT>::kThreads, QT == 1 ? 2 : 1)
       for (int kb = 0; kb < C::kKB; ++kb)
         tma_load_3d_hint(&q_map, &sh.q_full, s_q + qt * C::kTileBytes + kb * kBlock, kb * 64, g * G,
                          static_cast<int>(sr.q0) + sr.f + qt * tok, keep);
-    for (int i = 0; i < min(count, W::kStages); ++i) load_k(i);
+    for (int i = k_skip; i < min(count, W::kStages); ++i) load_k(i);
   }
   if (warp == W::kMma) {
     tmem_alloc(&sh.tmem, W::kTmem);
@@ -585,7 +593,7 @@ __global__ void __launch_bounds__(Win<QT>::kThreads, QT == 1 ? 2 : 1)
     }
     const uint64_t deadline = global_timer_ns() + 100000000ull;
     drain(&sh.q_full, 0, deadline);
-    for (int i = armed > W::kStages ? armed - W::kStages : 0; i < armed; ++i)
+    for (int i = armed > W::kStages ? armed - W::kStages : k_skip; i < armed; ++i)
       drain(&sh.k_full[i % W::kStages], (i / W::kStages) & 1u, deadline);
   } else if (warp == W::kMma) {
     const bool leader = elect_one();
