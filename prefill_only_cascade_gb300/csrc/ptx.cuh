@@ -172,6 +172,15 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.arrive.release;\n\t"
       "barrier.cluster.wait.acquire;" ::: "memory");
 }
+// Its halves: every thread arrives, and waits later (before it arrives again).
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 // Address of `p` (this CTA's shared memory) in the shared memory of cluster CTA `rank`.
 __device__ __forceinline__ uint32_t cluster_map(const void* p, uint32_t rank) {
   uint32_t r;

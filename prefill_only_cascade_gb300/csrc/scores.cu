@@ -339,7 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (cluster > 1) cluster_sync();  // the others run: their shared memory may be written
+  // Waited for at the end, when the TMEM columns are free again: all 512 of an SM are taken here,
+  // and a CTA that kept them while it waits for its cluster could keep another cluster's CTA from
+  // theirs, which that cluster's other CTAs wait for in turn.
+  if (cluster > 1) cluster_arrive();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const WaitCtl wc{a.timeout_ns, &sh.abort_flag, a.err_word};
@@ -486,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (owner) total += sh.part[0][at];
   bool failed = sh.abort_flag != 0;  // a wait ran out: the sums are not whole
   if (cluster > 1) {  // the cluster's sums, added in rank order by its first CTA
+    cluster_wait();   // the others run: their shared memory may be written
     if (rank > 0 && owner) st_cluster_f32(cluster_map(&sh.part[rank][at], 0), total);
     if (rank > 0 && failed && threadIdx.x == 0) st_cluster_u32(cluster_map(&sh.others_failed, 0), 1u);
     cluster_sync();
