@@ -414,18 +414,25 @@ def _explain(what, t, dtypes, shape, index):
     raise ValueError(f"{what}: strides {t.stride()} are not those of contiguous rows")
 
 
+def _index(what, t, axes):
+    """The device index (-1: CPU) of a tensor with so many axes."""
+    if not isinstance(t, torch.Tensor) or t.dim() != axes:
+        _explain(what, t, (getattr(t, "dtype", None),), (None,) * axes, 0)
+    return t.get_device()
+
+
 def _need(what, t, dtype, shape, index):
     """A contiguous tensor of exactly this type, shape and device; its address."""
-    if (t.dtype is not dtype or t.shape != shape or t.get_device() != index
-            or not t.is_contiguous()):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+            or t.get_device() != index or not t.is_contiguous()):
         _explain(what, t, (dtype,), shape, index)
     return t.data_ptr()
 
 
 def _need_rows(what, t, shape, index):
     """bf16 rows [n, heads, d] any distance apart: their address and that distance."""
-    st = t.stride()
-    if (t.dtype is not _BF16 or t.shape != shape or index < 0 or t.get_device() != index
+    st = t.stride() if isinstance(t, torch.Tensor) else ()
+    if (not st or t.dtype is not _BF16 or t.shape != shape or index < 0 or t.get_device() != index
             or len(st) != 3
             or (st[2] != 1 and shape[0]) or (st[1] != shape[2] and shape[1] > 1 and shape[0])):
         _explain(what, t, (_BF16,), shape, index)
@@ -435,14 +442,16 @@ def _need_rows(what, t, shape, index):
 def _need_pool(k_name, k, v_name, v, desc, pages, index):
     """K and V of a pool of `pages` pages; their addresses."""
     shape = (pages, desc.page_size, desc.num_kv_heads, desc.head_dim)
-    dtype = k.dtype
-    if ((dtype not in _CODES if desc.kv_dtype else dtype is not _BF16) or k.shape != shape
-            or k.get_device() != index or not k.is_contiguous() or v.dtype is not dtype
-            or v.shape != shape or v.get_device() != index or not v.is_contiguous()):
+    both = isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor)
+    dtype = k.dtype if both else None
+    if (not both or (dtype not in _CODES if desc.kv_dtype else dtype is not _BF16)
+            or k.shape != shape or k.get_device() != index or not k.is_contiguous()
+            or v.dtype is not dtype or v.shape != shape or v.get_device() != index
+            or not v.is_contiguous()):
         dtypes = _CODES if desc.kv_dtype == QUAIL_FP8_E4M3 else (_BF16,)
         for name, t in ((k_name, k), (v_name, v)):
-            if (t.dtype not in dtypes or t.shape != shape or t.get_device() != index
-                    or not t.is_contiguous()):
+            if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape
+                    or t.get_device() != index or not t.is_contiguous()):
                 _explain(name, t, dtypes, shape, index)
         raise ValueError(f"{k_name} and {v_name}: dtypes {k.dtype} and {v.dtype} differ")
     return k.data_ptr(), v.data_ptr()
@@ -460,8 +469,8 @@ def _need_scales(desc, k_scale, v_scale, index):
 
 def _need_score(what, t, rows, heads, least, index):
     """[rows, heads, n] fp32 with n >= least: its address and n."""
-    shape = t.shape
-    if (t.dtype is not _F32 or len(shape) != 3 or shape[0] != rows or shape[1] != heads
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    if (len(shape) != 3 or t.dtype is not _F32 or shape[0] != rows or shape[1] != heads
             or t.get_device() != index or not t.is_contiguous()):
         _explain(what, t, (_F32,), (rows, heads, None), index)
     if shape[2] < least:
@@ -470,7 +479,8 @@ def _need_score(what, t, rows, heads, least, index):
 
 
 def _need_workspace(t, index):
-    if t.dtype is not torch.uint8 or t.dim() != 1 or t.get_device() != index or not t.is_contiguous():
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.dim() != 1
+            or t.get_device() != index or not t.is_contiguous()):
         _explain("workspace", t, (torch.uint8,), (None,), index)
     return t.data_ptr(), t.numel()
 
@@ -499,7 +509,7 @@ def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pag
     """quail_paged_kv_append: rows k_new / v_new ([T, Hkv, d] bf16, any row stride) into the
     pages at start_pos[b] + i; new_offsets ([B+1] int32) delimits the sequences' rows (None:
     one token each). With e4m3 pages the rows become codes under the given scales."""
-    dev, B, pages = k_new.get_device(), desc.num_seqs, desc.num_pages
+    dev, B, pages = _index("k_new", k_new, 3), desc.num_seqs, desc.num_pages
     shape = (k_new.shape[0], desc.num_kv_heads, desc.head_dim)
     k, k_stride = _need_rows("k_new", k_new, shape, dev)
     v, v_stride = _need_rows("v_new", v_new, shape, dev)
@@ -526,7 +536,7 @@ def paged_decode_attn(desc: PagedDesc, q, k_pages, v_pages, block_table, seq_len
     the weight that each cached token receives (score_in may be score_out)."""
     if workspace is None:
         raise ValueError("workspace is required (size: paged_decode_workspace_size(...))")
-    dev, B, hq, pages = q.get_device(), desc.num_seqs, desc.num_q_heads, desc.num_pages
+    dev, B, hq, pages = _index("q", q, 3), desc.num_seqs, desc.num_q_heads, desc.num_pages
     shape = (B, hq, desc.head_dim)
     qp, q_stride = _need_rows("q", q, shape, dev)
     ws, ws_bytes = _need_workspace(workspace, dev)
@@ -554,11 +564,13 @@ def attn_scores(q, k, lse, q_offsets, k_offsets, score_out, max_q_len, max_k_len
     """quail_attn_scores: the attention weight that each key receives from the queries of its
     sequence (q [Tq, Hq, d], k [Tk, Hkv, d] bf16 with any row stride, lse [Tq, Hq] from the
     attention call), added to score_in into score_out [num_seqs, Hkv, n] fp32."""
-    dev = k.get_device()
+    dev = _index("k", k, 3)
+    _index("q", q, 3)
     tq, hq, d = q.shape
     tk, hkv, _ = k.shape
     qp, q_stride = _need_rows("q", q, (tq, hq, d), dev)
     kp, k_stride = _need_rows("k", k, (tk, hkv, d), dev)
+    _index("k_offsets", k_offsets, 1)
     seqs = k_offsets.shape[0] - 1
     max_q_len, max_k_len = int(max_q_len), int(max_k_len)
     so, width = _need_score("score_out", score_out, seqs, hkv, max_k_len, dev)
@@ -585,15 +597,15 @@ def paged_kv_evict(desc: PagedDesc, budget, recent, k_pages, v_pages, block_tabl
     if workspace is None:
         raise ValueError("workspace is required (size: paged_evict_workspace_size(...))")
     budget, recent = int(budget), int(recent)
-    dev, B, hkv, pages = k_pages.get_device(), desc.num_seqs, desc.num_kv_heads, desc.num_pages
+    dev, B, hkv, pages = _index("k_pages", k_pages, 4), desc.num_seqs, desc.num_kv_heads, desc.num_pages
     ws, ws_bytes = _need_workspace(workspace, dev)
     sp, width = _need_score("score", score, B, hkv, desc.max_seq_len, dev)
     so, out_width = None, 0
     if score_out is not None:
         so, out_width = _need_score("score_out", score_out, B, hkv, budget, dev)
+    _index("dst_table", dst_table, 2)
+    _index("k_dst", k_dst, 4)
     dst_shape, dst_pages = dst_table.shape, k_dst.shape[0]
-    if len(dst_shape) != 2:
-        _explain("dst_table", dst_table, (_I32,), (B, None), dev)
     _on_device(lib.quail_paged_kv_evict, "quail_paged_kv_evict", dev, stream, ctypes.byref(desc),
                budget, recent,
                *_need_pool("k_pages", k_pages, "v_pages", v_pages, desc, pages, dev),
