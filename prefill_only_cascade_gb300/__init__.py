@@ -384,11 +384,22 @@ def quantize_kv_fp8_with_scales(kv_bf16, anchor_offsets, amax, codes, scale, str
     _check(st, "quail_quantize_kv_fp8_with_scales")
 
 
+def _int32(what, x):
+    """x as an int that the C ABI's int32 holds (ctypes would drop the bits above)."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{what}: {x} does not fit 32 bits")
+    return x
+
+
 def make_paged_desc(num_seqs, max_seq_len, num_pages, page_size, max_pages_per_seq, num_q_heads,
                     num_kv_heads, head_dim, softmax_scale=0.0, kv_fp8=False) -> PagedDesc:
-    return PagedDesc(int(num_seqs), int(max_seq_len), int(num_pages), int(page_size),
-                     int(max_pages_per_seq), int(num_q_heads), int(num_kv_heads), int(head_dim),
-                     float(softmax_scale), QUAIL_FP8_E4M3 if kv_fp8 else QUAIL_BF16)
+    return PagedDesc(_int32("num_seqs", num_seqs), _int32("max_seq_len", max_seq_len),
+                     _int32("num_pages", num_pages), _int32("page_size", page_size),
+                     _int32("max_pages_per_seq", max_pages_per_seq),
+                     _int32("num_q_heads", num_q_heads), _int32("num_kv_heads", num_kv_heads),
+                     _int32("head_dim", head_dim), float(softmax_scale),
+                     QUAIL_FP8_E4M3 if kv_fp8 else QUAIL_BF16)
 
 
 # The paged calls run once per generated token, so their checks are written to be cheap: one
@@ -572,10 +583,11 @@ def attn_scores(q, k, lse, q_offsets, k_offsets, score_out, max_q_len, max_k_len
     kp, k_stride = _need_rows("k", k, (tk, hkv, d), dev)
     _index("k_offsets", k_offsets, 1)
     seqs = k_offsets.shape[0] - 1
-    max_q_len, max_k_len = int(max_q_len), int(max_k_len)
+    max_q_len, max_k_len = _int32("max_q_len", max_q_len), _int32("max_k_len", max_k_len)
+    window = _int32("window", window)
     so, width = _need_score("score_out", score_out, seqs, hkv, max_k_len, dev)
     _on_device(lib.quail_attn_scores, "quail_attn_scores", dev, stream, seqs, tq, tk, max_q_len,
-               max_k_len, hq, hkv, d, softmax_scale, 1 if causal else 0, int(window), qp, q_stride,
+               max_k_len, hq, hkv, d, softmax_scale, 1 if causal else 0, window, qp, q_stride,
                kp, k_stride, _need("lse", lse, _F32, (tq, hq), dev),
                _need("q_offsets", q_offsets, _I32, (seqs + 1,), dev),
                _need("k_offsets", k_offsets, _I32, (seqs + 1,), dev),
@@ -584,7 +596,8 @@ def attn_scores(q, k, lse, q_offsets, k_offsets, score_out, max_q_len, max_k_len
 
 
 def paged_evict_workspace_size(desc: PagedDesc, dst_num_pages) -> int:
-    return int(lib.quail_paged_evict_workspace_size(ctypes.byref(desc), int(dst_num_pages)))
+    return int(lib.quail_paged_evict_workspace_size(ctypes.byref(desc),
+                                                    _int32("dst_num_pages", dst_num_pages)))
 
 
 def paged_kv_evict(desc: PagedDesc, budget, recent, k_pages, v_pages, block_table, seq_lens, score,
@@ -596,7 +609,7 @@ def paged_kv_evict(desc: PagedDesc, budget, recent, k_pages, v_pages, block_tabl
     many, score_out [B, Hkv, n] takes their scores."""
     if workspace is None:
         raise ValueError("workspace is required (size: paged_evict_workspace_size(...))")
-    budget, recent = int(budget), int(recent)
+    budget, recent = _int32("budget", budget), _int32("recent", recent)
     dev, B, hkv, pages = _index("k_pages", k_pages, 4), desc.num_seqs, desc.num_kv_heads, desc.num_pages
     ws, ws_bytes = _need_workspace(workspace, dev)
     sp, width = _need_score("score", score, B, hkv, desc.max_seq_len, dev)

@@ -1,5 +1,6 @@
 """Host-only checks of the paged calls' Python arguments: what is no tensor, or a tensor of other
-dimensions, is named in the error."""
+dimensions, is named in the error; numbers that the C ABI's 32 bits do not hold are refused instead of
+wrapped."""
 import pytest
 import torch
 
@@ -78,3 +79,22 @@ def test_optional_tensors(on_gpu):
     codes = q.make_paged_desc(2, 30, 8, 16, 2, 4, 2, 64, kv_fp8=True)
     with pytest.raises(TypeError, match="k_scale: expected a tensor"):
         q.paged_decode_attn(codes, **DECODE, k_scale=1.0, v_scale=1.0)
+
+
+@pytest.mark.parametrize("big", [1 << 31, 1 << 32, (1 << 32) + 4, -(1 << 31) - 1])
+def test_numbers_past_32_bits(big, on_gpu):
+    for name in ("window", "max_q_len", "max_k_len"):
+        with pytest.raises(ValueError, match=name):
+            q.attn_scores(**{**SCORES, name: big})
+    for name in ("budget", "recent"):
+        with pytest.raises(ValueError, match=name):
+            q.paged_kv_evict(DESC, **{**EVICT, name: big})
+    with pytest.raises(ValueError, match="dst_num_pages"):
+        q.paged_evict_workspace_size(DESC, big)
+    names = ("num_seqs", "max_seq_len", "num_pages", "page_size", "max_pages_per_seq", "num_q_heads",
+             "num_kv_heads", "head_dim")
+    for i, name in enumerate(names):
+        sizes = [2, 30, 8, 16, 2, 4, 2, 64]
+        sizes[i] = big
+        with pytest.raises(ValueError, match=name):
+            q.make_paged_desc(*sizes)
