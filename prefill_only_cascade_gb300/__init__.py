@@ -425,47 +425,56 @@ def _explain(what, t, dtypes, shape, index):
     raise ValueError(f"{what}: strides {t.stride()} are not those of contiguous rows")
 
 
-def _index(what, t, axes):
-    """The device index (-1: CPU) of a tensor with so many axes."""
+def _axes(what, t, axes):
+    """Why `t` is not a tensor with so many axes, if it is not."""
     if not isinstance(t, torch.Tensor) or t.dim() != axes:
         _explain(what, t, (getattr(t, "dtype", None),), (None,) * axes, 0)
-    return t.get_device()
 
 
+# What is no tensor has no `dtype` or `get_device`: found out by the AttributeError, since asking
+# for the type first costs 0.04 us a tensor.
 def _need(what, t, dtype, shape, index):
     """A contiguous tensor of exactly this type, shape and device; its address."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
-            or t.get_device() != index or not t.is_contiguous()):
-        _explain(what, t, (dtype,), shape, index)
-    return t.data_ptr()
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _explain(what, t, (dtype,), shape, index)
 
 
 def _need_rows(what, t, shape, index):
     """bf16 rows [n, heads, d] any distance apart: their address and that distance."""
-    st = t.stride() if isinstance(t, torch.Tensor) else ()
-    if (not st or t.dtype is not _BF16 or t.shape != shape or index < 0 or t.get_device() != index
-            or len(st) != 3
-            or (st[2] != 1 and shape[0]) or (st[1] != shape[2] and shape[1] > 1 and shape[0])):
-        _explain(what, t, (_BF16,), shape, index)
-    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
+    try:
+        st = t.stride()
+        if (t.dtype is _BF16 and t.shape == shape and index >= 0 and t.get_device() == index
+                and len(st) == 3
+                and (st[2] == 1 or not shape[0])
+                and (st[1] == shape[2] or shape[1] <= 1 or not shape[0])):
+            return t.data_ptr(), st[0] if shape[0] > 1 else shape[1] * shape[2]
+    except AttributeError:
+        pass
+    _explain(what, t, (_BF16,), shape, index)
 
 
 def _need_pool(k_name, k, v_name, v, desc, pages, index):
     """K and V of a pool of `pages` pages; their addresses."""
     shape = (pages, desc.page_size, desc.num_kv_heads, desc.head_dim)
-    both = isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor)
-    dtype = k.dtype if both else None
-    if (not both or (dtype not in _CODES if desc.kv_dtype else dtype is not _BF16)
-            or k.shape != shape or k.get_device() != index or not k.is_contiguous()
-            or v.dtype is not dtype or v.shape != shape or v.get_device() != index
-            or not v.is_contiguous()):
-        dtypes = _CODES if desc.kv_dtype == QUAIL_FP8_E4M3 else (_BF16,)
-        for name, t in ((k_name, k), (v_name, v)):
-            if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape
-                    or t.get_device() != index or not t.is_contiguous()):
-                _explain(name, t, dtypes, shape, index)
-        raise ValueError(f"{k_name} and {v_name}: dtypes {k.dtype} and {v.dtype} differ")
-    return k.data_ptr(), v.data_ptr()
+    try:
+        dtype = k.dtype
+        if ((dtype in _CODES if desc.kv_dtype else dtype is _BF16) and k.shape == shape
+                and k.get_device() == index and k.is_contiguous() and v.dtype is dtype
+                and v.shape == shape and v.get_device() == index and v.is_contiguous()):
+            return k.data_ptr(), v.data_ptr()
+    except AttributeError:
+        pass
+    dtypes = _CODES if desc.kv_dtype == QUAIL_FP8_E4M3 else (_BF16,)
+    for name, t in ((k_name, k), (v_name, v)):
+        if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape
+                or t.get_device() != index or not t.is_contiguous()):
+            _explain(name, t, dtypes, shape, index)
+    raise ValueError(f"{k_name} and {v_name}: dtypes {k.dtype} and {v.dtype} differ")
 
 
 def _need_scales(desc, k_scale, v_scale, index):
@@ -480,9 +489,13 @@ def _need_scales(desc, k_scale, v_scale, index):
 
 def _need_score(what, t, rows, heads, least, index):
     """[rows, heads, n] fp32 with n >= least: its address and n."""
-    shape = t.shape if isinstance(t, torch.Tensor) else ()
-    if (len(shape) != 3 or t.dtype is not _F32 or shape[0] != rows or shape[1] != heads
-            or t.get_device() != index or not t.is_contiguous()):
+    try:
+        shape = t.shape
+        good = (t.dtype is _F32 and len(shape) == 3 and shape[0] == rows and shape[1] == heads
+                and t.get_device() == index and t.is_contiguous())
+    except AttributeError:
+        good = False
+    if not good:
         _explain(what, t, (_F32,), (rows, heads, None), index)
     if shape[2] < least:
         raise ValueError(f"{what}: {shape[2]} entries a row, at least {least} are needed")
@@ -490,10 +503,13 @@ def _need_score(what, t, rows, heads, least, index):
 
 
 def _need_workspace(t, index):
-    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.dim() != 1
-            or t.get_device() != index or not t.is_contiguous()):
-        _explain("workspace", t, (torch.uint8,), (None,), index)
-    return t.data_ptr(), t.numel()
+    try:
+        if (t.dtype is torch.uint8 and t.dim() == 1 and t.get_device() == index
+                and t.is_contiguous()):
+            return t.data_ptr(), t.numel()
+    except AttributeError:
+        pass
+    _explain("workspace", t, (torch.uint8,), (None,), index)
 
 
 def _on_device(fn, what, index, stream, *args):
@@ -520,8 +536,11 @@ def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pag
     """quail_paged_kv_append: rows k_new / v_new ([T, Hkv, d] bf16, any row stride) into the
     pages at start_pos[b] + i; new_offsets ([B+1] int32) delimits the sequences' rows (None:
     one token each). With e4m3 pages the rows become codes under the given scales."""
-    dev, B, pages = _index("k_new", k_new, 3), desc.num_seqs, desc.num_pages
-    shape = (k_new.shape[0], desc.num_kv_heads, desc.head_dim)
+    B, pages = desc.num_seqs, desc.num_pages
+    try:
+        dev, shape = k_new.get_device(), (k_new.shape[0], desc.num_kv_heads, desc.head_dim)
+    except (AttributeError, IndexError):
+        _axes("k_new", k_new, 3)
     k, k_stride = _need_rows("k_new", k_new, shape, dev)
     v, v_stride = _need_rows("v_new", v_new, shape, dev)
     off = None
@@ -547,8 +566,12 @@ def paged_decode_attn(desc: PagedDesc, q, k_pages, v_pages, block_table, seq_len
     the weight that each cached token receives (score_in may be score_out)."""
     if workspace is None:
         raise ValueError("workspace is required (size: paged_decode_workspace_size(...))")
-    dev, B, hq, pages = _index("q", q, 3), desc.num_seqs, desc.num_q_heads, desc.num_pages
+    B, hq, pages = desc.num_seqs, desc.num_q_heads, desc.num_pages
     shape = (B, hq, desc.head_dim)
+    try:
+        dev = q.get_device()
+    except AttributeError:
+        _axes("q", q, 3)
     qp, q_stride = _need_rows("q", q, shape, dev)
     ws, ws_bytes = _need_workspace(workspace, dev)
     ks, vs = _need_scales(desc, k_scale, v_scale, dev)
@@ -575,22 +598,28 @@ def attn_scores(q, k, lse, q_offsets, k_offsets, score_out, max_q_len, max_k_len
     """quail_attn_scores: the attention weight that each key receives from the queries of its
     sequence (q [Tq, Hq, d], k [Tk, Hkv, d] bf16 with any row stride, lse [Tq, Hq] from the
     attention call), added to score_in into score_out [num_seqs, Hkv, n] fp32."""
-    dev = _index("k", k, 3)
-    _index("q", q, 3)
-    tq, hq, d = q.shape
-    tk, hkv, _ = k.shape
+    try:
+        dev = k.get_device()
+        tq, hq, d = q.shape
+        tk, hkv, _ = k.shape
+        seqs = k_offsets.shape[0] - 1
+    except (AttributeError, IndexError, ValueError):
+        _axes("q", q, 3)
+        _axes("k", k, 3)
+        _axes("k_offsets", k_offsets, 1)
     qp, q_stride = _need_rows("q", q, (tq, hq, d), dev)
     kp, k_stride = _need_rows("k", k, (tk, hkv, d), dev)
-    _index("k_offsets", k_offsets, 1)
-    seqs = k_offsets.shape[0] - 1
-    max_q_len, max_k_len = _int32("max_q_len", max_q_len), _int32("max_k_len", max_k_len)
-    window = _int32("window", window)
+    max_q_len, max_k_len, window = int(max_q_len), int(max_k_len), int(window)
+    if (max_q_len | max_k_len | window) >> 31:
+        for name, x in (("max_q_len", max_q_len), ("max_k_len", max_k_len), ("window", window)):
+            _int32(name, x)
+    ko = _need("k_offsets", k_offsets, _I32, (seqs + 1,), dev)
     so, width = _need_score("score_out", score_out, seqs, hkv, max_k_len, dev)
     _on_device(lib.quail_attn_scores, "quail_attn_scores", dev, stream, seqs, tq, tk, max_q_len,
                max_k_len, hq, hkv, d, softmax_scale, 1 if causal else 0, window, qp, q_stride,
                kp, k_stride, _need("lse", lse, _F32, (tq, hq), dev),
                _need("q_offsets", q_offsets, _I32, (seqs + 1,), dev),
-               _need("k_offsets", k_offsets, _I32, (seqs + 1,), dev),
+               ko,
                None if score_in is None else _need("score_in", score_in, _F32, score_out.shape, dev),
                so, width)
 
@@ -609,16 +638,24 @@ def paged_kv_evict(desc: PagedDesc, budget, recent, k_pages, v_pages, block_tabl
     many, score_out [B, Hkv, n] takes their scores."""
     if workspace is None:
         raise ValueError("workspace is required (size: paged_evict_workspace_size(...))")
-    budget, recent = _int32("budget", budget), _int32("recent", recent)
-    dev, B, hkv, pages = _index("k_pages", k_pages, 4), desc.num_seqs, desc.num_kv_heads, desc.num_pages
+    budget, recent = int(budget), int(recent)
+    if (budget | recent) >> 31:
+        _int32("budget", budget), _int32("recent", recent)
+    B, hkv, pages = desc.num_seqs, desc.num_kv_heads, desc.num_pages
+    try:
+        dev = k_pages.get_device()
+        dst_shape, dst_pages = dst_table.shape, k_dst.shape[0]
+    except (AttributeError, IndexError):
+        _axes("k_pages", k_pages, 4)
+        _axes("dst_table", dst_table, 2)
+        _axes("k_dst", k_dst, 4)
     ws, ws_bytes = _need_workspace(workspace, dev)
     sp, width = _need_score("score", score, B, hkv, desc.max_seq_len, dev)
     so, out_width = None, 0
     if score_out is not None:
         so, out_width = _need_score("score_out", score_out, B, hkv, budget, dev)
-    _index("dst_table", dst_table, 2)
-    _index("k_dst", k_dst, 4)
-    dst_shape, dst_pages = dst_table.shape, k_dst.shape[0]
+    if len(dst_shape) != 2:
+        _explain("dst_table", dst_table, (_I32,), (B, None), dev)
     _on_device(lib.quail_paged_kv_evict, "quail_paged_kv_evict", dev, stream, ctypes.byref(desc),
                budget, recent,
                *_need_pool("k_pages", k_pages, "v_pages", v_pages, desc, pages, dev),
