@@ -1,6 +1,10 @@
 """Host-only checks of the paged calls' Python arguments: what is no tensor, or a tensor of other
 dimensions, is named in the error; numbers that the C ABI's 32 bits do not hold are refused instead of
-wrapped."""
+wrapped; and the module does without PyTorch's private names."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -98,3 +102,21 @@ def test_numbers_past_32_bits(big, on_gpu):
         sizes[i] = big
         with pytest.raises(ValueError, match=name):
             q.make_paged_desc(*sizes)
+
+
+def test_without_private_names():
+    """A PyTorch that has no such names: the module loads, and its host-side parts work."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    hasattr(torch._C, n) and delattr(torch._C, n)\n"
+            "class S: cuda_stream = 77\n"
+            "torch.cuda.current_stream = lambda i: S if i == 3 else None\n"
+            "torch.cuda.current_device = lambda: 3\n"
+            "import prefill_only_cascade_gb300 as q\n"
+            "assert q.paged_decode_workspace_size(q.make_paged_desc(2, 30, 8, 16, 2, 4, 2, 64)) > 0\n"
+            "got = []\n"
+            "q._on_device(lambda *a: got.append(a) or 0, 'x', 3, None, 1, 2)\n"
+            "assert got == [(1, 2, 77)], got\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert run.returncode == 0, run.stderr
