@@ -443,8 +443,8 @@ quail_status quail_paged_kv_append(const quail_paged_desc* desc, int64_t num_new
  *            log), may be NULL
  *   score_in, score_out [B, Hkv, score_stride] fp32, score_stride >= max_seq_len;
  *            score_out NULL: no weights are formed; score_in NULL: zeros; both may be the
- *            same buffer. Entries at seq_lens[b] and beyond are left as they were. A head
- *            whose lse is NaN or -inf adds nothing.
+ *            same buffer, else they must not overlap. Entries at seq_lens[b] and beyond are
+ *            left as they were. A head whose lse is NaN or -inf adds nothing.
  *   workspace: at least quail_paged_decode_workspace_size(desc, score_out != NULL) bytes,
  *            16-byte aligned, overwritten; calls that share one must not overlap on the GPU.
  */
@@ -479,9 +479,9 @@ size_t quail_paged_decode_workspace_size(const quail_paged_desc* desc, int32_t w
  *            sequence whose ranges lie outside the totals or exceed max_q_len / max_k_len
  *            is left out and QUAIL_ERR_DEVICE_BOUNDS reported)
  *   score_in, score_out [num_seqs, Hkv, score_stride] fp32, score_stride >= max_k_len;
- *            score_in NULL: zeros; both may be the same buffer. Entries past the sequence's
- *            keys are left as they were, and after QUAIL_ERR_TIMEOUT those of keys whose
- *            weights are not whole.
+ *            score_in NULL: zeros; both may be the same buffer, else they must not overlap.
+ *            Entries past the sequence's keys are left as they were, and after
+ *            QUAIL_ERR_TIMEOUT those of keys whose weights are not whole.
  * Limits: d in {64, 128}, Hq/Hkv in {1, 2, 4, 8, 16}.
  */
 quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t total_k_tokens,

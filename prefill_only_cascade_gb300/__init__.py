@@ -405,7 +405,8 @@ def make_paged_desc(num_seqs, max_seq_len, num_pages, page_size, max_pages_per_s
 # The paged calls run once per generated token, so their checks are written to be cheap: one
 # test per tensor, the reason worked out only when it fails, the stream's handle without a
 # Stream object, the device switched only when it is not the current one.
-# (PyTorch's own short cuts where it has them: 0.08 us instead of 1.1 for the stream, 0.12 instead of 0.25 for the device.)
+# (PyTorch's own short cuts where it has them: 0.08 us instead of 1.1 for the stream, 0.12
+# instead of 0.25 for the device.)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device

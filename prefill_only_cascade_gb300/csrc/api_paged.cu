@@ -25,6 +25,21 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
+// Whether [p, p + n) meets one of `rows` rows of `row` bytes that lie `stride` bytes apart.
+bool meets_rows(const void* p, size_t n, const void* base, int64_t rows, int64_t row, int64_t stride) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(base);
+  if (n == 0 || rows <= 0 || row <= 0) return false;
+  // the first row that ends past p
+  const int64_t i = a < b + row ? 0 : static_cast<int64_t>((a - b - row) / stride + 1);
+  return i < rows && b + static_cast<uintptr_t>(i) * stride < a + n;
+}
+
+// score_in and score_out, rows of both `stride` entries apart: one buffer, or two that do not meet.
+bool scores_apart(const float* in, const float* out, int64_t rows, int64_t stride) {
+  const size_t n = 4 * static_cast<size_t>(rows) * static_cast<size_t>(stride);
+  return in == nullptr || in == out || !overlap(in, n, out, n);
+}
+
 // The checks of every paged call.
 quail_status check_desc(const quail_paged_desc* desc) {
   if (desc == nullptr) return QUAIL_ERR_INVALID_ARG;
@@ -171,6 +186,11 @@ quail_status quail_paged_decode_attn(const quail_paged_desc* desc, const void* q
     return QUAIL_ERR_INVALID_ARG;
   if (score_in != nullptr && !scored) return QUAIL_ERR_INVALID_ARG;
   if (scored && score_stride < d.max_seq_len) return QUAIL_ERR_INVALID_ARG;
+  // written by some blocks while others read
+  const int64_t row = static_cast<int64_t>(d.num_q_heads) * d.head_dim * 2;
+  if (meets_rows(out, static_cast<size_t>(d.num_seqs) * row, q, d.num_seqs, row, 2 * q_row_stride) ||
+      !scores_apart(score_in, score_out, static_cast<int64_t>(d.num_seqs) * d.num_kv_heads, score_stride))
+    return QUAIL_ERR_INVALID_ARG;
   if (d.num_seqs > 0) {
     if (q == nullptr || seq_lens == nullptr || out == nullptr || !aligned(q, 16) ||
         !aligned(seq_lens, 4) || !aligned(out, 16))
@@ -257,6 +277,8 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
   if (total_k_tokens > 0 && (k == nullptr || score_out == nullptr || !aligned(k, 16)))
     return QUAIL_ERR_INVALID_ARG;
   if (!aligned(score_in, 4) || !aligned(score_out, 4)) return QUAIL_ERR_INVALID_ARG;
+  if (!scores_apart(score_in, score_out, static_cast<int64_t>(num_seqs) * num_kv_heads, score_stride))
+    return QUAIL_ERR_INVALID_ARG;
   // TMA coordinates and key numbers run up to two tiles past the last token
   if (total_q_tokens > kInt32Max - 1024 || total_k_tokens > kInt32Max - 1024 ||
       max_k_len > kInt32Max - 1024)
