@@ -125,8 +125,10 @@ __device__ void write_notes(const PagedEvictArgs& a, int warp, int warps, int ch
 // pass); in a round each warp has a contiguous run, lane by lane, so that the order of the
 // tokens is (round, warp, i, lane).
 constexpr int kSmallKeys = 4 * kSelThreads;   // FUSED: tokens per CTA at most
-constexpr int kSmallKept = 512;               // kept ones per CTA of the cluster at most
-constexpr int kSmallPages = kMaxCluster * kSmallKept / 16;  // their pages at most
+constexpr int kSmallKept = 512;               // kept tokens of a sequence that fits one CTA, at most
+constexpr int kSmallShare = 128;              // kept ones per CTA of longer sequences' clusters
+constexpr int kSmallPages =                   // the kept ones' pages at most (of 16 tokens or more)
+    (kSmallKept > kMaxCluster * kSmallShare ? kSmallKept : kMaxCluster * kSmallShare) / 16;
 template <int KPT, bool SHARED, bool FUSED>
 __global__ void __launch_bounds__(kSelThreads, 2)
     evict_select_kernel(const PagedEvictArgs a, int cluster, int note_blocks, int note_chunks) {
@@ -602,10 +604,10 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   // 4,000 26 and 18; and 2 us less on the host.
   const bool brief = a.max_len <= kSmallKeys && most <= kSmallKept;
   while (cluster < kMaxCluster && (a.max_len > kSmallKeys * cluster ||
-                                   (pairs * cluster * 2 <= num_sms && most > 128 * cluster)))
+                                   (pairs * cluster * 2 <= num_sms && most > kSmallShare * cluster)))
     cluster *= 2;
   // (every CTA compares its `own` pages with all the `others`)
-  if (a.max_len <= kSmallKeys * cluster && (brief || most <= 128 * cluster) &&
+  if (a.max_len <= kSmallKeys * cluster && (brief || most <= kSmallShare * cluster) &&
       (cluster == 1 || pairs * cluster <= 2 * num_sms) && others <= 1024 && own * others <= 65536) {
     attr[0].val.clusterDim.x = cluster;
     cfg.numAttrs = cluster > 1;
