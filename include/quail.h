@@ -384,6 +384,9 @@ quail_status quail_quantize_kv_fp8_with_scales(int32_t num_anchors,
  * Block tables, lengths and positions are read on the device. What they name outside the
  * pool, the table or max_seq_len is not touched; the call says below what becomes of the
  * sequence, and quail_get_device_error() reports QUAIL_ERR_DEVICE_BOUNDS.
+ * Kernels, grids and workspaces are chosen by max_seq_len (the lengths are on the device), so a
+ * bound far above the longest length is right but slower; max_k_len and max_q_len of
+ * quail_attn_scores likewise.
  * Limits: page_size a power of two from 16 to 256; max_seq_len at most 2^30 and at most
  * max_pages_per_seq * page_size; d in {64, 128}; Hq/Hkv in {1, 2, 4, 8, 16};
  * num_seqs * Hq < 2^28; num_seqs * max_pages_per_seq < 2^31.

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 // none can be long, the runs are dealt to the warps themselves (kWarps), and none waits at all.
 //
 // Both products run on mma.sync m16n8k16: one new token gives at most 16 query rows per KV
-// head, so the padded products cost a few per cent of the tensor rate of the legacy pipe.
+// head, so the padded products do not bound it but with 16 heads over e4m3 pages (see below).
 // Since sums over d (scores) and the order of d (output rows) may be permuted freely,
 // 16-byte pieces of plain rows ARE the operand fragments:
 //   S  [16 heads x 8 keys]  A = Q (rows: heads), B = K: lane (r, q) holds key r, piece q + 4i
@@ -1187,9 +1187,9 @@ cudaError_t launch_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream
   cudaError_t e;
   // One launch where clusters of up to eight CTAs, eight tiles each at most, all fit the GPU
   // at once: there a launch less is worth more than an even division. Measured against the
-  // divided runs (8 KV heads, d = 128): one sequence of 777 tokens 5.9 us and 7.4, four of
-  // 2,000 8.9 and 12.8, four of 4,000 15.5 and 20.0, four of 1,000-4,000 with weights 15.2 and
-  // 13.9; past the rule, one of 8,000 14.9 and 12.4, sixteen of 2,000 38 and 30.
+  // divided runs (8 KV heads, d = 128): one sequence of 777 tokens 6.0 us and 7.6, four of
+  // 2,000 9.2 and 12.9, four of 4,000 15.7 and 20.7, four of 1,000-4,000 with weights 19.5 and
+  // 18.4; past the rule, one of 8,000 15.8 and 13.1, sixteen of 2,000 39.5 and 30.4.
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
   const int tiles = (a.max_len + C::kTile - 1) / C::kTile;
   int cluster = 1;
@@ -1267,9 +1267,9 @@ int decode_tile_keys(int head_dim, bool fp8) {
 
 // Where a CTA has several short pieces in its run, putting its warps' parts together is what
 // takes the time (8 us a piece). Measured against runs of CTAs: 181 sequences of 20-83 tokens
-// (8 KV heads, G = 16, e4m3) 25.7 us and 38.6, 256 of 16-128 (8, G = 4) 27.7 and 37.3, 100 of
-// 100-500 (8, G = 8) 33.1 and 38.2, 128 of 300-600 (8, G = 4, e4m3) 33.6 and 36.8; past the rule,
-// 93 of 431-589 42.6 and 41.0, 128 of 500-1,000 71.8 and 68.5 (parts of more runs to join).
+// (8 KV heads, G = 16, e4m3) 27.0 us and 40.8, 256 of 16-128 (8, G = 4) 29.2 and 38.7, 100 of
+// 100-500 (8, G = 8) 33.6 and 39.8, 128 of 300-600 (8, G = 4, e4m3) 35.0 and 37.8; past the rule,
+// 93 of 431-589 43.9 and 41.9, 128 of 500-1,000 73.6 and 70.7 (parts of more runs to join).
 bool decode_by_warps(int num_seqs, int hkv, int max_len, int tile) {
   return static_cast<int64_t>(num_seqs) * hkv >= 2 * kDecodeMaxCtas && max_len <= 8 * tile;
 }

@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // The long CTAs start first: with causal masking the first keys, which have the most queries,
   // of all sequences, otherwise the sequences by their queries, as found here (8 anchors, 2,000
-  // to 4,000 queries each: 156 us instead of 163; it costs a CTA 0.5 us).
+  // to 4,000 queries each: 157 us instead of 163; it costs a CTA 0.5 us).
   int id = blockIdx.x / cluster;
   const int g = id % a.hkv;
   id /= a.hkv;
