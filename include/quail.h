@@ -48,7 +48,11 @@ typedef enum {
   QUAIL_ERR_DEVICE_BOUNDS = 5  /* offsets on the device disagree with the descriptor */
 } quail_status;
 
-typedef enum { QUAIL_BF16 = 0, QUAIL_FP8_E4M3 = 1 } quail_dtype;
+typedef enum {
+  QUAIL_BF16 = 0,
+  QUAIL_FP8_E4M3 = 1,
+  QUAIL_FP4_E2M1 = 2 /* pages of a paged cache only */
+} quail_dtype;
 
 /*
  * Shape of one ragged cascade-attention batch. A = anchors, S = suffixes, T_A / T_S =
@@ -376,11 +380,15 @@ quail_status quail_quantize_kv_fp8_with_scales(int32_t num_anchors,
  * T / page_size pages as it stands), and a block table that names the pages of each
  * sequence in order. It holds the anchor KV that [P1] "Como funciona" keeps between
  * prefills, and lets it grow and be cut token by token.
- *   k_pages, v_pages [num_pages, page_size, Hkv, d] bf16, or e4m3 codes (16-byte aligned)
+ *   k_pages, v_pages [num_pages, page_size, Hkv, d] bf16, or e4m3 codes (16-byte aligned), or
+ *               fp4: [num_pages, Hkv, head] bytes, a head being the e2m1 codes of page_size
+ *               tokens (d / 2 bytes each, two codes a byte, the even d in the low bits) and then
+ *               their block scales (d / 16 bytes each, an e4m3 number per 16 values of d):
+ *               4.5 bits a value. quail_paged_page_bytes() bytes a page in every form.
  *   block_table [num_seqs, max_pages_per_seq] int32; entries past a sequence's last page
  *               are not read. Sequences may share pages that no call writes.
- *   k_scale, v_scale [num_seqs, Hkv] fp32 (value = e4m3(code) * scale), with e4m3 pages
- *               only; NULL with bf16 pages
+ *   k_scale, v_scale [num_seqs, Hkv] fp32 (value = e4m3(code) * scale; fp4: e2m1(code) *
+ *               block scale * scale), with e4m3 and fp4 pages; NULL with bf16 pages
  * Block tables, lengths and positions are read on the device. What they name outside the
  * pool, the table or max_seq_len is not touched; the call says below what becomes of the
  * sequence, and quail_get_device_error() reports QUAIL_ERR_DEVICE_BOUNDS.
@@ -409,7 +417,10 @@ typedef struct {
  * prefill read) or one token per sequence. Row i of sequence b goes to position
  * start_pos[b] + i. With e4m3 pages the code is e4m3(x / scale), x / scale rounded to fp32
  * first, then to nearest even with saturation at +-448 - quail_quantize_kv_fp8's codes when
- * the scales are.
+ * the scales are. With fp4 pages, per 16 values x and with scale S = amax / 2688 using both
+ * formats whole: the block scale is b = e4m3(max|x| / (6 S)), the codes are e2m1(x / (b S)),
+ * products and quotients rounded to fp32 first, then to nearest even with saturation at +-448
+ * and +-6. A block whose scale rounds to 0 holds zeros, one that holds a NaN is all NaN.
  *   num_new     T, new tokens of all sequences
  *   k_new, v_new [T, Hkv, d] bf16, rows k_row_stride / v_row_stride elements apart (>=
  *               Hkv * d, a multiple of 8; e.g. columns of a fused projection), 16-byte
@@ -428,6 +439,32 @@ quail_status quail_paged_kv_append(const quail_paged_desc* desc, int64_t num_new
                                    const int32_t* start_pos, const int32_t* block_table,
                                    const float* k_scale, const float* v_scale, void* k_pages,
                                    void* v_pages, quail_stream_t stream);
+
+/*
+ * Reads rows back from the pages as bf16: row i of sequence b is its position start_pos[b] + i.
+ * What quail_cascade_attn takes as k_anc / v_anc, or quail_attn_scores as k. fp4 and e4m3 values
+ * are products in fp32 (the code's exactly, times the scale) rounded to bf16; bf16 ones are
+ * copied.
+ *   num_rows    T, rows of all sequences
+ *   offsets     [B+1] int32 prefix sums into k_out / v_out, or NULL for one row per sequence
+ *               (then T = B)
+ *   start_pos   [B] int32: the first position read of each sequence
+ *   k_out, v_out [T, Hkv, d] bf16, rows k_row_stride / v_row_stride elements apart (>= Hkv * d, a
+ *               multiple of 8), 16-byte aligned, overlapping neither the pages nor each other;
+ *               NULL: that side is not read (its pages may be NULL too), but not both
+ * Positions from seq_lens on are read as they are in the pages. A row whose position is not in
+ * [0, max_seq_len) or whose page is out of range becomes NaN, one that no sequence holds is left
+ * as it was; both are reported (see above), and so are offsets that do not increase from 0 to T.
+ */
+quail_status quail_paged_kv_read(const quail_paged_desc* desc, int64_t num_rows,
+                                 const int32_t* offsets, const int32_t* start_pos,
+                                 const int32_t* block_table, const float* k_scale,
+                                 const float* v_scale, const void* k_pages, const void* v_pages,
+                                 void* k_out, void* v_out, int64_t k_row_stride,
+                                 int64_t v_row_stride, quail_stream_t stream);
+
+/* Bytes of one page of K, and of V (0 when desc is not valid). */
+size_t quail_paged_page_bytes(const quail_paged_desc* desc);
 
 /*
  * Attention of one new token per sequence over its cached tokens (its own K and V appended

@@ -25,6 +25,7 @@ QUAIL_ERR_TIMEOUT = 4
 QUAIL_ERR_DEVICE_BOUNDS = 5
 QUAIL_BF16 = 0
 QUAIL_FP8_E4M3 = 1
+QUAIL_FP4_E2M1 = 2
 
 # Every symbol include/quail.h declares.
 EXPORTED_SYMBOLS = (
@@ -37,7 +38,7 @@ EXPORTED_SYMBOLS = (
     "quail_cascade_attn_two_pass", "quail_cascade_two_pass_workspace_size",
     "quail_quantize_kv_fp8_with_scales", "quail_paged_kv_append", "quail_paged_decode_attn",
     "quail_paged_decode_workspace_size", "quail_attn_scores", "quail_paged_kv_evict",
-    "quail_paged_evict_workspace_size",
+    "quail_paged_evict_workspace_size", "quail_paged_kv_read", "quail_paged_page_bytes",
 )
 
 
@@ -153,6 +154,11 @@ def _load():
     lib.quail_paged_kv_append.argtypes = [paged, i64, vp, vp, i64, i64, i32p, i32p, i32p, f32p,
                                           f32p, vp, vp, vp]
     lib.quail_paged_kv_append.restype = ctypes.c_int
+    lib.quail_paged_kv_read.argtypes = [paged, i64, i32p, i32p, i32p, f32p, f32p, vp, vp, vp, vp,
+                                        i64, i64, vp]
+    lib.quail_paged_kv_read.restype = ctypes.c_int
+    lib.quail_paged_page_bytes.argtypes = [paged]
+    lib.quail_paged_page_bytes.restype = sz
     lib.quail_paged_decode_attn.argtypes = [paged, vp, i64, vp, vp, i32p, i32p, f32p, f32p, vp,
                                             f32p, f32p, f32p, i64, vp, sz, vp]
     lib.quail_paged_decode_attn.restype = ctypes.c_int
@@ -393,13 +399,32 @@ def _int32(what, x):
 
 
 def make_paged_desc(num_seqs, max_seq_len, num_pages, page_size, max_pages_per_seq, num_q_heads,
-                    num_kv_heads, head_dim, softmax_scale=0.0, kv_fp8=False) -> PagedDesc:
+                    num_kv_heads, head_dim, softmax_scale=0.0, kv_fp8=False,
+                    kv_fp4=False) -> PagedDesc:
+    """quail_paged_desc with bf16 pages, e4m3 codes (kv_fp8) or fp4 (kv_fp4)."""
+    if kv_fp8 and kv_fp4:
+        raise ValueError("kv_fp8 and kv_fp4: pages have one form")
     return PagedDesc(_int32("num_seqs", num_seqs), _int32("max_seq_len", max_seq_len),
                      _int32("num_pages", num_pages), _int32("page_size", page_size),
                      _int32("max_pages_per_seq", max_pages_per_seq),
                      _int32("num_q_heads", num_q_heads), _int32("num_kv_heads", num_kv_heads),
                      _int32("head_dim", head_dim), float(softmax_scale),
-                     QUAIL_FP8_E4M3 if kv_fp8 else QUAIL_BF16)
+                     QUAIL_FP4_E2M1 if kv_fp4 else QUAIL_FP8_E4M3 if kv_fp8 else QUAIL_BF16)
+
+
+def paged_pool_shape(desc: PagedDesc, pages=None):
+    """Shape of a K or V pool of `pages` pages (the descriptor's): [pages, page_size, Hkv, d], or
+    with fp4 pages [pages, Hkv, bytes of a page's head] of uint8 (its codes, then its block
+    scales; see include/quail.h)."""
+    if pages is None:
+        pages = desc.num_pages
+    if desc.kv_dtype == QUAIL_FP4_E2M1:
+        return (pages, desc.num_kv_heads, desc.page_size * desc.head_dim * 9 // 16)
+    return (pages, desc.page_size, desc.num_kv_heads, desc.head_dim)
+
+
+def paged_page_bytes(desc: PagedDesc) -> int:
+    return int(lib.quail_paged_page_bytes(ctypes.byref(desc)))
 
 
 # The paged calls run once per generated token, so their checks are written to be cheap: one
@@ -411,7 +436,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-_CODES = (torch.float8_e4m3fn, torch.uint8)
+_POOL_DTYPES = {QUAIL_BF16: (_BF16,), QUAIL_FP8_E4M3: (torch.float8_e4m3fn, torch.uint8),
+                QUAIL_FP4_E2M1: (torch.uint8,)}
 
 
 def _explain(what, t, dtypes, shape, index):
@@ -463,16 +489,17 @@ def _need_rows(what, t, shape, index):
 
 def _need_pool(k_name, k, v_name, v, desc, pages, index):
     """K and V of a pool of `pages` pages; their addresses."""
-    shape = (pages, desc.page_size, desc.num_kv_heads, desc.head_dim)
+    form = desc.kv_dtype
+    shape = paged_pool_shape(desc, pages)
+    dtypes = _POOL_DTYPES.get(form, ())
     try:
         dtype = k.dtype
-        if ((dtype in _CODES if desc.kv_dtype else dtype is _BF16) and k.shape == shape
+        if (dtype in dtypes and k.shape == shape
                 and k.get_device() == index and k.is_contiguous() and v.dtype is dtype
                 and v.shape == shape and v.get_device() == index and v.is_contiguous()):
             return k.data_ptr(), v.data_ptr()
     except AttributeError:
         pass
-    dtypes = _CODES if desc.kv_dtype == QUAIL_FP8_E4M3 else (_BF16,)
     for name, t in ((k_name, k), (v_name, v)):
         if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape
                 or t.get_device() != index or not t.is_contiguous()):
@@ -484,7 +511,7 @@ def _need_scales(desc, k_scale, v_scale, index):
     if k_scale is None and v_scale is None and not desc.kv_dtype:
         return None, None
     if k_scale is None or v_scale is None:
-        raise ValueError("e4m3 pages need k_scale and v_scale, bf16 pages neither")
+        raise ValueError("e4m3 and fp4 pages need k_scale and v_scale, bf16 pages neither")
     shape = (desc.num_seqs, desc.num_kv_heads)
     return (_need("k_scale", k_scale, _F32, shape, index),
             _need("v_scale", v_scale, _F32, shape, index))
@@ -538,7 +565,8 @@ def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pag
                     new_offsets=None, k_scale=None, v_scale=None, stream=None):
     """quail_paged_kv_append: rows k_new / v_new ([T, Hkv, d] bf16, any row stride) into the
     pages at start_pos[b] + i; new_offsets ([B+1] int32) delimits the sequences' rows (None:
-    one token each). With e4m3 pages the rows become codes under the given scales."""
+    one token each). With e4m3 and fp4 pages the rows become codes under the given scales (fp4:
+    amax / 2688 uses the format whole)."""
     B, pages = desc.num_seqs, desc.num_pages
     try:
         dev, shape = k_new.get_device(), (k_new.shape[0], desc.num_kv_heads, desc.head_dim)
@@ -555,6 +583,41 @@ def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pag
                _need("start_pos", start_pos, _I32, (B,), dev),
                _need("block_table", block_table, _I32, (B, desc.max_pages_per_seq), dev), ks, vs,
                *_need_pool("k_pages", k_pages, "v_pages", v_pages, desc, pages, dev))
+
+
+def paged_kv_read(desc: PagedDesc, k_pages, v_pages, start_pos, block_table, k_out, v_out,
+                  offsets=None, k_scale=None, v_scale=None, stream=None):
+    """quail_paged_kv_read: positions start_pos[b] + i of the sequences as bf16 rows into k_out /
+    v_out ([T, Hkv, d] bf16, any row stride; None: not read); offsets ([B+1] int32) delimits the
+    sequences' rows (None: one each)."""
+    B, pages = desc.num_seqs, desc.num_pages
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        raise ValueError("k_out and v_out: at least one is needed")
+    try:
+        dev, shape = some.get_device(), (some.shape[0], desc.num_kv_heads, desc.head_dim)
+    except (AttributeError, IndexError):
+        _axes("k_out" if k_out is not None else "v_out", some, 3)
+    k = v = kp = vp = None
+    k_stride = v_stride = 0
+    if k_out is not None:
+        k, k_stride = _need_rows("k_out", k_out, shape, dev)
+    if v_out is not None:
+        v, v_stride = _need_rows("v_out", v_out, shape, dev)
+    if k_out is not None and v_out is not None:
+        kp, vp = _need_pool("k_pages", k_pages, "v_pages", v_pages, desc, pages, dev)
+    elif k_out is not None:
+        kp, _ = _need_pool("k_pages", k_pages, "k_pages", k_pages, desc, pages, dev)
+    else:
+        vp, _ = _need_pool("v_pages", v_pages, "v_pages", v_pages, desc, pages, dev)
+    off = None
+    if offsets is not None:
+        off = _need("offsets", offsets, _I32, (B + 1,), dev)
+    ks, vs = _need_scales(desc, k_scale, v_scale, dev)
+    _on_device(lib.quail_paged_kv_read, "quail_paged_kv_read", dev, stream, ctypes.byref(desc),
+               shape[0], off, _need("start_pos", start_pos, _I32, (B,), dev),
+               _need("block_table", block_table, _I32, (B, desc.max_pages_per_seq), dev), ks, vs,
+               kp, vp, k, v, k_stride, v_stride)
 
 
 def paged_decode_workspace_size(desc: PagedDesc, with_scores=False) -> int:

@@ -34,6 +34,18 @@ bool meets_rows(const void* p, size_t n, const void* base, int64_t rows, int64_t
   return i < rows && b + static_cast<uintptr_t>(i) * stride < a + n;
 }
 
+// Whether a row of `row` bytes of one tensor meets one of the other (`n` rows each, sa and sb
+// bytes apart): the rows of each lie in its first stride's columns where both have one stride
+// and begin within one of each other, else their whole ranges count.
+bool rows_meet(const void* a, int64_t sa, const void* b, int64_t sb, int64_t n, int64_t row) {
+  const size_t na = static_cast<size_t>((n - 1) * sa + row), nb = static_cast<size_t>((n - 1) * sb + row);
+  if (!overlap(a, na, b, nb)) return false;
+  if (sa != sb) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const int64_t apart = static_cast<int64_t>((x < y ? y - x : x - y) % static_cast<uintptr_t>(sa));
+  return apart < row || apart > sa - row;  // columns of one wider row do not meet
+}
+
 // score_in and score_out, rows of both `stride` entries apart: one buffer, or two that do not meet.
 bool scores_apart(const float* in, const float* out, int64_t rows, int64_t stride) {
   const size_t n = 4 * static_cast<size_t>(rows) * static_cast<size_t>(stride);
@@ -50,7 +62,8 @@ quail_status check_desc(const quail_paged_desc* desc) {
   if (d.num_q_heads <= 0 || d.num_kv_heads <= 0 || d.num_q_heads % d.num_kv_heads != 0)
     return QUAIL_ERR_INVALID_ARG;
   if (!(d.softmax_scale >= 0.0f) || !std::isfinite(d.softmax_scale)) return QUAIL_ERR_INVALID_ARG;
-  if (d.kv_dtype != QUAIL_BF16 && d.kv_dtype != QUAIL_FP8_E4M3) return QUAIL_ERR_INVALID_ARG;
+  if (d.kv_dtype != QUAIL_BF16 && d.kv_dtype != QUAIL_FP8_E4M3 && d.kv_dtype != QUAIL_FP4_E2M1)
+    return QUAIL_ERR_INVALID_ARG;
   if (d.head_dim != 64 && d.head_dim != 128) return QUAIL_ERR_UNSUPPORTED;
   if (!valid_group(d.num_q_heads / d.num_kv_heads)) return QUAIL_ERR_UNSUPPORTED;
   if (d.page_size < 16 || d.page_size > 256 || (d.page_size & (d.page_size - 1)) != 0)
@@ -64,14 +77,44 @@ quail_status check_desc(const quail_paged_desc* desc) {
   return QUAIL_OK;
 }
 
-// e4m3 pages come with scales, bf16 pages without.
+// e4m3 and fp4 pages come with scales, bf16 pages without.
 bool scales_ok(const quail_paged_desc& d, const float* k_scale, const float* v_scale) {
-  if (d.kv_dtype == QUAIL_FP8_E4M3)
-    return k_scale != nullptr && v_scale != nullptr && aligned(k_scale, 4) && aligned(v_scale, 4);
+  if (d.kv_dtype != QUAIL_BF16)  // (no sequences have none)
+    return ((k_scale != nullptr && v_scale != nullptr) || d.num_seqs == 0) && aligned(k_scale, 4) &&
+           aligned(v_scale, 4);
   return k_scale == nullptr && v_scale == nullptr;
 }
 
-int elem_bytes(const quail_paged_desc& d) { return d.kv_dtype == QUAIL_FP8_E4M3 ? 1 : 2; }
+// Bytes of a (token, KV head) row and of a page.
+int row_bytes(const quail_paged_desc& d) {
+  if (d.kv_dtype == QUAIL_FP4_E2M1) return d.head_dim / 2 + d.head_dim / 16;
+  return d.head_dim * (d.kv_dtype == QUAIL_FP8_E4M3 ? 1 : 2);
+}
+size_t page_bytes(const quail_paged_desc& d) {
+  return static_cast<size_t>(d.page_size) * d.num_kv_heads * row_bytes(d);
+}
+
+quail::PagedRows rows_of(const quail_paged_desc& d, int64_t total, int64_t k_stride, int64_t v_stride,
+                         const int32_t* offsets, const int32_t* start_pos, const int32_t* table,
+                         const float* k_scale, const float* v_scale, const quail::DeviceInfo& info) {
+  quail::PagedRows p{};
+  p.num_seqs = d.num_seqs;
+  p.hkv = d.num_kv_heads;
+  p.max_len = d.max_seq_len;
+  p.page_shift = log2_of(d.page_size);
+  p.max_pages = d.max_pages_per_seq;
+  p.num_pages = d.num_pages;
+  p.total = total;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.offsets = offsets;
+  p.start_pos = start_pos;
+  p.table = table;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.err_word = info.err_word;
+  return p;
+}
 
 float scale_log2_of(float softmax_scale, int head_dim) {
   const float s = softmax_scale > 0.0f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
@@ -84,11 +127,10 @@ struct DecodeLayout {
 };
 DecodeLayout decode_layout(const quail_paged_desc& d, bool with_scores) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const bool fp8 = d.kv_dtype == QUAIL_FP8_E4M3;
   const int group = d.num_q_heads / d.num_kv_heads;
-  const int tile = quail::decode_tile_keys(d.head_dim, fp8);
+  const int tile = quail::decode_tile_keys(d.head_dim, d.kv_dtype);
   const size_t parts = 2 * static_cast<size_t>(quail::decode_ctas(
-                               quail::kDecodeMaxCtas, d.num_seqs, d.num_kv_heads, d.max_seq_len,
+                               quail::kDecodeMaxSms, quail::decode_ctas_per_sm(d.kv_dtype), d.num_seqs, d.num_kv_heads, d.max_seq_len,
                                tile)) *
                        (quail::decode_by_warps(d.num_seqs, d.num_kv_heads, d.max_seq_len, tile) ? 4 : 1);
   DecodeLayout l;
@@ -131,13 +173,24 @@ quail_status quail_paged_kv_append(const quail_paged_desc* desc, int64_t num_new
     if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_pages, 16) ||
         !aligned(v_pages, 16) || !aligned(start_pos, 4) || !aligned(block_table, 4))
       return QUAIL_ERR_INVALID_ARG;
-    const size_t pool = static_cast<size_t>(d.num_pages) * d.page_size * row * elem_bytes(d);
+    const size_t pool = static_cast<size_t>(d.num_pages) * page_bytes(d);
     if (overlap(k_pages, pool, v_pages, pool)) return QUAIL_ERR_INVALID_ARG;
   }
   quail::DeviceInfo info;
   const int ds = quail::current_device_info(&info);
   if (ds != QUAIL_OK) return static_cast<quail_status>(ds);
   if (num_new == 0) return QUAIL_OK;
+  if (d.kv_dtype == QUAIL_FP4_E2M1) {
+    quail::PagedRows p = rows_of(d, num_new, k_row_stride, v_row_stride, new_offsets, start_pos,
+                                 block_table, k_scale, v_scale, info);
+    p.k_new = static_cast<const uint16_t*>(k_new);
+    p.v_new = static_cast<const uint16_t*>(v_new);
+    p.k_pages = static_cast<uint8_t*>(k_pages);
+    p.v_pages = static_cast<uint8_t*>(v_pages);
+    const cudaError_t e = quail::launch_fp4_append(p, d.head_dim, info.num_sms,
+                                                   reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QUAIL_OK : QUAIL_ERR_CUDA;
+  }
   quail::PagedAppendArgs a{};
   a.num_seqs = d.num_seqs;
   a.hkv = d.num_kv_heads;
@@ -162,6 +215,63 @@ quail_status quail_paged_kv_append(const quail_paged_desc* desc, int64_t num_new
   a.err_word = info.err_word;
   const cudaError_t e = quail::launch_paged_append(a, d.kv_dtype == QUAIL_FP8_E4M3, info.num_sms,
                                                    reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QUAIL_OK : QUAIL_ERR_CUDA;
+}
+
+size_t quail_paged_page_bytes(const quail_paged_desc* desc) {
+  return check_desc(desc) == QUAIL_OK ? page_bytes(*desc) : 0;
+}
+
+quail_status quail_paged_kv_read(const quail_paged_desc* desc, int64_t num_rows,
+                                 const int32_t* offsets, const int32_t* start_pos,
+                                 const int32_t* block_table, const float* k_scale,
+                                 const float* v_scale, const void* k_pages, const void* v_pages,
+                                 void* k_out, void* v_out, int64_t k_row_stride,
+                                 int64_t v_row_stride, quail_stream_t stream) {
+  const quail_status c = check_desc(desc);
+  if (c != QUAIL_OK) return c;
+  const quail_paged_desc& d = *desc;
+  const int row = d.num_kv_heads * d.head_dim;
+  if (num_rows < 0 || num_rows > kInt32Max || (d.num_seqs == 0 && num_rows != 0))
+    return QUAIL_ERR_INVALID_ARG;
+  if (offsets == nullptr && num_rows != d.num_seqs) return QUAIL_ERR_INVALID_ARG;
+  if (!scales_ok(d, k_scale, v_scale) || !aligned(offsets, 4)) return QUAIL_ERR_INVALID_ARG;
+  const struct {
+    const void* pages;
+    const void* out;
+    int64_t stride;
+  } sides[2] = {{k_pages, k_out, k_row_stride}, {v_pages, v_out, v_row_stride}};
+  if (num_rows > 0) {
+    if (start_pos == nullptr || block_table == nullptr || !aligned(start_pos, 4) ||
+        !aligned(block_table, 4) || (k_out == nullptr && v_out == nullptr))
+      return QUAIL_ERR_INVALID_ARG;
+    const size_t pool = static_cast<size_t>(d.num_pages) * page_bytes(d);
+    for (const auto& s : sides) {
+      if (s.out == nullptr) continue;
+      if (s.pages == nullptr || !aligned(s.pages, 16) || !aligned(s.out, 16) || s.stride < row ||
+          s.stride % 8 != 0)
+        return QUAIL_ERR_INVALID_ARG;
+      // written by some blocks while others read
+      for (const auto& t : sides)
+        if (t.out != nullptr && meets_rows(t.pages, pool, s.out, num_rows, 2 * row, 2 * s.stride))
+          return QUAIL_ERR_INVALID_ARG;
+    }
+    if (k_out != nullptr && v_out != nullptr &&
+        rows_meet(k_out, 2 * k_row_stride, v_out, 2 * v_row_stride, num_rows, 2 * row))
+      return QUAIL_ERR_INVALID_ARG;
+  }
+  quail::DeviceInfo info;
+  const int ds = quail::current_device_info(&info);
+  if (ds != QUAIL_OK) return static_cast<quail_status>(ds);
+  if (num_rows == 0) return QUAIL_OK;
+  quail::PagedRows p = rows_of(d, num_rows, k_row_stride, v_row_stride, offsets, start_pos,
+                               block_table, k_scale, v_scale, info);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.k_pages = static_cast<uint8_t*>(const_cast<void*>(k_pages));
+  p.v_pages = static_cast<uint8_t*>(const_cast<void*>(v_pages));
+  const cudaError_t e = quail::launch_paged_read(p, d.head_dim, d.kv_dtype, info.num_sms,
+                                                 reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QUAIL_OK : QUAIL_ERR_CUDA;
 }
 
@@ -241,7 +351,7 @@ quail_status quail_paged_decode_attn(const quail_paged_desc* desc, const void* q
   a.raw_stride = l.raw_stride;
   a.err_word = info.err_word;
   const cudaError_t e =
-      quail::launch_paged_decode(a, d.head_dim, d.kv_dtype == QUAIL_FP8_E4M3, info.num_sms,
+      quail::launch_paged_decode(a, d.head_dim, d.kv_dtype, info.num_sms,
                                  reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QUAIL_OK : QUAIL_ERR_CUDA;
 }
@@ -356,9 +466,8 @@ quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, 
   if (d.num_seqs > 0 &&
       (static_cast<int64_t>(budget) * d.num_kv_heads + 255) / 256 > kInt32Max / d.num_seqs)
     return QUAIL_ERR_UNSUPPORTED;
-  const int row_bytes = d.head_dim * elem_bytes(d);
-  const size_t page_bytes = static_cast<size_t>(d.page_size) * d.num_kv_heads * row_bytes;
-  const size_t src_bytes = page_bytes * d.num_pages, dst_bytes = page_bytes * dst_num_pages;
+  if (d.kv_dtype == QUAIL_FP4_E2M1) return QUAIL_ERR_UNSUPPORTED;
+  const size_t src_bytes = page_bytes(d) * d.num_pages, dst_bytes = page_bytes(d) * dst_num_pages;
   const bool same_pool = k_dst == k_pages;
   if (d.num_seqs > 0) {
     if (seq_lens == nullptr || kept == nullptr || new_lens == nullptr) return QUAIL_ERR_INVALID_ARG;
@@ -396,7 +505,7 @@ quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, 
   quail::PagedEvictArgs a{};
   a.num_seqs = d.num_seqs;
   a.hkv = d.num_kv_heads;
-  a.row_bytes = row_bytes;
+  a.row_bytes = row_bytes(d);
   a.max_len = d.max_seq_len;
   a.page_shift = log2_of(d.page_size);
   a.max_pages = d.max_pages_per_seq;

@@ -190,6 +190,27 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, bool fp8, int num_sms,
                                 cudaStream_t stream);
+// Token rows written into fp4 pages, or read back from pages of any form.
+struct PagedRows {
+  int num_seqs, hkv;
+  int max_len, page_shift, max_pages, num_pages;
+  int64_t total, k_stride, v_stride;       // token rows; elements between them
+  const uint16_t* k_new;                   // append: bf16
+  const uint16_t* v_new;
+  uint16_t* k_out;                         // read: bf16; one of the two may be NULL
+  uint16_t* v_out;
+  const int32_t* offsets;                  // NULL: one token per sequence
+  const int32_t* start_pos;
+  const int32_t* table;
+  const float* k_scale;
+  const float* v_scale;
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  unsigned* err_word;
+};
+cudaError_t launch_fp4_append(const PagedRows& p, int head_dim, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_read(const PagedRows& p, int head_dim, int kv_dtype, int num_sms,
+                              cudaStream_t stream);
 
 // What a CTA (or a warp, see decode_by_warps) of the decode attention leaves for the join: the (sequence, head) that begins
 // in it and goes on in the next CTAs (seq < 0: none) up to CTA `last`; sparse: the number of
@@ -225,13 +246,16 @@ struct PagedDecodeArgs {
   int64_t raw_stride;
   unsigned* err_word;
 };
-constexpr int kDecodeMaxCtas = 320;
-int decode_tile_keys(int head_dim, bool fp8);
-int decode_ctas(int num_sms, int num_seqs, int hkv, int max_len, int tile);
+constexpr int kDecodeMaxSms = 160;  // the workspace holds the parts of so many SMs' CTAs
+int decode_tile_keys(int head_dim, int kv_dtype);
+int decode_ctas_per_sm(int kv_dtype);
+int decode_ctas(int num_sms, int per_sm, int num_seqs, int hkv, int max_len, int tile);
 // Whether runs are dealt to warps, four per CTA (the workspace then holds four times the parts).
 bool decode_by_warps(int num_seqs, int hkv, int max_len, int tile);
-cudaError_t launch_paged_decode(PagedDecodeArgs& a, int head_dim, bool fp8, int num_sms,
+cudaError_t launch_paged_decode(PagedDecodeArgs& a, int head_dim, int kv_dtype, int num_sms,
                                 cudaStream_t stream);
+cudaError_t launch_paged_decode_fp4(PagedDecodeArgs& a, int head_dim, int num_sms,
+                                    cudaStream_t stream);
 
 struct AttnScoresArgs {
   int num_seqs, hq, hkv, group;
