@@ -544,8 +544,8 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
  *   1 <= budget <= 2^30, 0 <= recent <= budget
  *   score [B, Hkv, score_stride] fp32, score_stride >= max_seq_len
  *   dst_table [B, dst_max_pages_per_seq] int32 into the destination pool k_dst / v_dst
- *            [dst_num_pages, page_size, Hkv, d]: either the same pool (same pointers and
- *            page count) or one that does not overlap it. Each destination page belongs to
+ *            [dst_num_pages, page_size, Hkv, d] (fp4: as its pages are): either the same pool
+ *            (same pointers and page count) or one that does not overlap it. Each destination page belongs to
  *            one sequence and is none that a sequence of the call holds; rows for pages
  *            that break this are not written and new_lens[b] becomes -1, as it does for a
  *            length out of range and for a source page outside the pool (at least where a
@@ -556,7 +556,7 @@ quail_status quail_attn_scores(int32_t num_seqs, int64_t total_q_tokens, int64_t
  *            overlapping score: the kept tokens' scores, zeros behind them
  *   workspace: at least quail_paged_evict_workspace_size(desc, dst_num_pages) bytes,
  *            16-byte aligned, overwritten; calls that share one must not overlap on the GPU.
- * The scales of e4m3 pages stay those of the sequence. Limits: num_seqs * budget * Hkv <
+ * The scales of e4m3 and fp4 pages stay those of the sequence. Limits: num_seqs * budget * Hkv <
  * 2^38, num_seqs * dst_max_pages_per_seq < 2^31.
  */
 quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, int32_t recent,

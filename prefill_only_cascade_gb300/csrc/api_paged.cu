@@ -466,7 +466,6 @@ quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, 
   if (d.num_seqs > 0 &&
       (static_cast<int64_t>(budget) * d.num_kv_heads + 255) / 256 > kInt32Max / d.num_seqs)
     return QUAIL_ERR_UNSUPPORTED;
-  if (d.kv_dtype == QUAIL_FP4_E2M1) return QUAIL_ERR_UNSUPPORTED;
   const size_t src_bytes = page_bytes(d) * d.num_pages, dst_bytes = page_bytes(d) * dst_num_pages;
   const bool same_pool = k_dst == k_pages;
   if (d.num_seqs > 0) {
@@ -505,7 +504,8 @@ quail_status quail_paged_kv_evict(const quail_paged_desc* desc, int32_t budget, 
   quail::PagedEvictArgs a{};
   a.num_seqs = d.num_seqs;
   a.hkv = d.num_kv_heads;
-  a.row_bytes = row_bytes(d);
+  a.block_bytes = d.kv_dtype == QUAIL_FP4_E2M1 ? d.head_dim / 16 : 0;
+  a.row_bytes = row_bytes(d) - a.block_bytes;
   a.max_len = d.max_seq_len;
   a.page_shift = log2_of(d.page_size);
   a.max_pages = d.max_pages_per_seq;

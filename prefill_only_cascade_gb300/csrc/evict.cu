@@ -36,6 +36,33 @@ __device__ __forceinline__ int evict_len(const PagedEvictArgs& a, int b) {
   return n >= 0 && n <= a.max_len ? n : -1;
 }
 
+// Byte offset in a pool of the row of KV head g at place `at` of a page; fp4: of its codes, and of
+// its block scales (a head's codes lie together, and behind them its block scales).
+__device__ __forceinline__ int64_t row_at(const PagedEvictArgs& a, int page, int at, int g) {
+  if (a.block_bytes == 0)
+    return (((static_cast<int64_t>(page) << a.page_shift) + at) * a.hkv + g) * a.row_bytes;
+  return (static_cast<int64_t>(page) * a.hkv + g) *
+             (static_cast<int64_t>(a.row_bytes + a.block_bytes) << a.page_shift) +
+         static_cast<int64_t>(at) * a.row_bytes;
+}
+__device__ __forceinline__ int64_t blocks_at(const PagedEvictArgs& a, int page, int at, int g) {
+  return row_at(a, page, 0, g) + (static_cast<int64_t>(a.row_bytes) << a.page_shift) +
+         at * a.block_bytes;
+}
+// log2 of a row's 16-byte pieces
+__device__ __forceinline__ int row_shift(const PagedEvictArgs& a) {
+  return a.row_bytes == 256 ? 4 : a.row_bytes == 128 ? 3 : a.row_bytes == 64 ? 2 : 1;
+}
+// A row's block scales, 8 bytes of them or 4.
+__device__ __forceinline__ uint2 load_blocks(const uint8_t* p, int bytes) {
+  return bytes == 8 ? *reinterpret_cast<const uint2*>(p)
+                    : make_uint2(*reinterpret_cast<const uint32_t*>(p), 0u);
+}
+__device__ __forceinline__ void store_blocks(uint8_t* p, int bytes, uint2 x) {
+  if (bytes == 8) *reinterpret_cast<uint2*>(p) = x;
+  else *reinterpret_cast<uint32_t*>(p) = x.x;
+}
+
 __device__ __forceinline__ int pages_of(const PagedEvictArgs& a, int tokens) {
   return (tokens + (1 << a.page_shift) - 1) >> a.page_shift;
 }
@@ -473,7 +500,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         if (bad) atomicOr(a.err_word, kErrDeviceBounds);
       }
     }
-    const int shift = a.row_bytes == 256 ? 4 : a.row_bytes == 128 ? 3 : 2;  // 16-byte pieces a row
+    const int shift = row_shift(a);
     const int mask = (1 << a.page_shift) - 1;
     // the recent tokens are dealt out evenly
     const int r0 = rank * recent / cluster, r1 = (rank + 1) * recent / cluster;
@@ -487,13 +514,16 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       if (pos < 0 || pos >= n) continue;  // only if the scores changed meanwhile
       const int from = __ldg(a.table + b * a.max_pages + (pos >> a.page_shift));
       if (s_bad[i >> a.page_shift] || from < 0 || from >= a.num_pages) continue;
-      const int64_t src =
-          (((static_cast<int64_t>(from) << a.page_shift) + (pos & mask)) * a.hkv + g) * a.row_bytes +
-          16 * c;
-      const int64_t dst = (((static_cast<int64_t>(s_to[i >> a.page_shift]) << a.page_shift) +
-                            (i & mask)) * a.hkv + g) * a.row_bytes + 16 * c;
+      const int to = s_to[i >> a.page_shift];
+      const int64_t src = row_at(a, from, pos & mask, g) + 16 * c;
+      const int64_t dst = row_at(a, to, i & mask, g) + 16 * c;
       const uint4 x = *reinterpret_cast<const uint4*>(a.k_pages + src);
       const uint4 y = *reinterpret_cast<const uint4*>(a.v_pages + src);
+      if (a.block_bytes != 0 && c < 2) {  // one lane K's, one V's
+        const uint8_t* from_pages = c == 0 ? a.k_pages : a.v_pages;
+        store_blocks((c == 0 ? a.k_dst : a.v_dst) + blocks_at(a, to, i & mask, g), a.block_bytes,
+                     load_blocks(from_pages + blocks_at(a, from, pos & mask, g), a.block_bytes));
+      }
       *reinterpret_cast<uint4*>(a.k_dst + dst) = x;
       *reinterpret_cast<uint4*>(a.v_dst + dst) = y;
     }
@@ -542,15 +572,18 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const Paged
       atomicOr(a.err_word, kErrDeviceBounds);
       a.new_lens[b] = -1;
     }
-    s_src[threadIdx.x] =
-        ok ? (((static_cast<int64_t>(from) << a.page_shift) + (pos & mask)) * a.hkv + g) * a.row_bytes
-           : -1;
-    s_dst[threadIdx.x] =
-        ok ? (((static_cast<int64_t>(to) << a.page_shift) + (i & mask)) * a.hkv + g) * a.row_bytes
-           : -1;
+    s_src[threadIdx.x] = ok ? row_at(a, from, pos & mask, g) : -1;
+    s_dst[threadIdx.x] = ok ? row_at(a, to, i & mask, g) : -1;
+    if (ok && a.block_bytes != 0) {
+      const int64_t src = blocks_at(a, from, pos & mask, g), dst = blocks_at(a, to, i & mask, g);
+      const uint2 x = load_blocks(a.k_pages + src, a.block_bytes);
+      const uint2 y = load_blocks(a.v_pages + src, a.block_bytes);
+      store_blocks(a.k_dst + dst, a.block_bytes, x);
+      store_blocks(a.v_dst + dst, a.block_bytes, y);
+    }
   }
   __syncthreads();
-  const int shift = a.row_bytes == 256 ? 4 : a.row_bytes == 128 ? 3 : 2;  // 16-byte pieces a row
+  const int shift = row_shift(a);
   const int pieces = count << shift;
   for (int u0 = threadIdx.x; u0 < pieces; u0 += kCopyThreads * kCopyUnroll) {
     uint4 x[kCopyUnroll], y[kCopyUnroll];

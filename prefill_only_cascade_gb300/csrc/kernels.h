@@ -278,7 +278,8 @@ cudaError_t launch_attn_scores(const AttnScoresArgs& a, const CUtensorMap& q_map
                                cudaStream_t stream);
 
 struct PagedEvictArgs {
-  int num_seqs, hkv, row_bytes;      // row_bytes of one (token, head)
+  int num_seqs, hkv, row_bytes;      // row_bytes of one (token, head); fp4: of its codes
+  int block_bytes;                   // fp4: of its block scales, 0 otherwise
   int max_len, page_shift, max_pages, num_pages;
   int budget, recent;
   int dst_max_pages, dst_num_pages;
