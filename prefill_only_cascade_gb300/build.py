@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libquail.so")
 SOURCES = ["api.cu", "api_paged.cu", "cascade.cu", "evict.cu", "head.cu", "kv_plan.cu",
-           "noalloc.cu", "paged.cu", "paged_rows.cu", "prefill.cu", "quantize.cu", "scores.cu", "select.cu",
+           "noalloc.cu", "paged.cu", "paged_rows.cu", "fp4_decode.cu", "prefill.cu", "quantize.cu", "scores.cu", "select.cu",
            "shard.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

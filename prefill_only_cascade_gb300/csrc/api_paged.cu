@@ -130,7 +130,7 @@ DecodeLayout decode_layout(const quail_paged_desc& d, bool with_scores) {
   const int group = d.num_q_heads / d.num_kv_heads;
   const int tile = quail::decode_tile_keys(d.head_dim, d.kv_dtype);
   const size_t parts = 2 * static_cast<size_t>(quail::decode_ctas(
-                               quail::kDecodeMaxSms, quail::decode_ctas_per_sm(d.kv_dtype), d.num_seqs, d.num_kv_heads, d.max_seq_len,
+                               quail::kDecodeMaxSms, quail::decode_ctas_per_sm(d.kv_dtype, group), d.num_seqs, d.num_kv_heads, d.max_seq_len,
                                tile)) *
                        (quail::decode_by_warps(d.num_seqs, d.num_kv_heads, d.max_seq_len, tile) ? 4 : 1);
   DecodeLayout l;

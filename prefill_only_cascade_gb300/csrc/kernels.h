@@ -190,6 +190,12 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, bool fp8, int num_sms,
                                 cudaStream_t stream);
+// How pages hold their values (quail_dtype's numbers).
+enum KvForm {
+  kBf16,
+  kE4m3,  // codes, a scale per sequence and KV head
+  kFp4    // e2m1 codes, an e4m3 scale per 16 values and a scale per sequence and KV head
+};
 // Token rows written into fp4 pages, or read back from pages of any form.
 struct PagedRows {
   int num_seqs, hkv;
@@ -248,14 +254,16 @@ struct PagedDecodeArgs {
 };
 constexpr int kDecodeMaxSms = 160;  // the workspace holds the parts of so many SMs' CTAs
 int decode_tile_keys(int head_dim, int kv_dtype);
-int decode_ctas_per_sm(int kv_dtype);
+int decode_ctas_per_sm(int kv_dtype, int group);
 int decode_ctas(int num_sms, int per_sm, int num_seqs, int hkv, int max_len, int tile);
 // Whether runs are dealt to warps, four per CTA (the workspace then holds four times the parts).
 bool decode_by_warps(int num_seqs, int hkv, int max_len, int tile);
 cudaError_t launch_paged_decode(PagedDecodeArgs& a, int head_dim, int kv_dtype, int num_sms,
                                 cudaStream_t stream);
-cudaError_t launch_paged_decode_fp4(PagedDecodeArgs& a, int head_dim, int num_sms,
-                                    cudaStream_t stream);
+// Keys of a CTA's tile over fp4 pages: 8 KB of codes.
+constexpr int fp4_tile_keys(int head_dim) { return 16384 / head_dim; }
+int fp4_decode_per_sm(int group);
+cudaError_t launch_fp4_decode(PagedDecodeArgs& a, int head_dim, int num_sms, cudaStream_t stream);
 
 struct AttnScoresArgs {
   int num_seqs, hq, hkv, group;

@@ -18,8 +18,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "fp4.cuh"
 #include "kernels.h"
-#include "paged_decode.cuh"
 #include "ptx.cuh"
 
 namespace quail {
@@ -210,7 +210,7 @@ struct Held {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-        o[k] = pack2<false>(__fmul_rn(f.x, S), __fmul_rn(f.y, S));
+        o[k] = pack_bf16x2(__fmul_rn(f.x, S), __fmul_rn(f.y, S));
       }
       a = make_uint4(o[0], o[1], o[2], o[3]);
       b = make_uint4(o[4], o[5], o[6], o[7]);
@@ -289,17 +289,6 @@ cudaError_t launch_paged_read(const PagedRows& p, int head_dim, int kv_dtype, in
     run(kv_dtype == kFp4 ? paged_read_kernel<64, kFp4>
         : kv_dtype == kE4m3 ? paged_read_kernel<64, kE4m3> : paged_read_kernel<64, kBf16>);
   return cudaGetLastError();
-}
-
-// The attention over fp4 pages, compiled here beside the other kernels that know the form.
-cudaError_t launch_paged_decode_fp4(PagedDecodeArgs& a, int head_dim, int num_sms,
-                                    cudaStream_t stream) {
-  const bool two = a.group > 8;
-  if (head_dim == 128)
-    return two ? launch_decode_t<128, kFp4, 2>(a, num_sms, stream)
-               : launch_decode_t<128, kFp4, 1>(a, num_sms, stream);
-  return two ? launch_decode_t<64, kFp4, 2>(a, num_sms, stream)
-             : launch_decode_t<64, kFp4, 1>(a, num_sms, stream);
 }
 
 }  // namespace quail
