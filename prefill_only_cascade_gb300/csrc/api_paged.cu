@@ -350,6 +350,8 @@ quail_status quail_paged_decode_attn(const quail_paged_desc* desc, const void* q
   a.raw = scored ? reinterpret_cast<float*>(w + l.raw) : nullptr;
   a.raw_stride = l.raw_stride;
   a.err_word = info.err_word;
+  a.timeout_ns = info.timeout_ns;
+  a.inject_skip_loads = info.inject_skip_first_kv;
   const cudaError_t e =
       quail::launch_paged_decode(a, d.head_dim, d.kv_dtype, info.num_sms,
                                  reinterpret_cast<cudaStream_t>(stream));

@@ -33,8 +33,12 @@ namespace quail {
 
 namespace {
 
+constexpr int kFp4PerSm = 3;  // CTAs per SM
+constexpr int kSide = 2;      // 16-key blocks whose scores are worked out side by side
+
 template <int D>
 struct Fp4Cfg {
+  static constexpr int kStages = 2;                  // steps in a warp's ring
   static constexpr int kCB = D / 2;                  // code bytes of a (token, head) row
   static constexpr int kSB = D / 16;                 // its block scales
   static constexpr int kKeys = fp4_tile_keys(D) / kDecWarps;  // keys per warp step: 32 or 64
@@ -50,56 +54,94 @@ struct Fp4Cfg {
   static constexpr int kSmem = kRing + kDecWarps * 8 * D * 4;  // + the warps' O, 8 heads
 };
 
-// Place of 16-byte piece c of V row `row`: the rows 2q of a read's lanes on different banks.
-template <int D>
-__device__ __forceinline__ int fp4_v_place(int row, int c) {
-  return D == 128 ? (row * 4 + c) ^ (((row >> 1) & 3) << 1) : (row * 2 + c) ^ (((row >> 2) & 1) << 1);
+// The step's data is read only here, and every read is volatile like the wait before it: no clobber of
+// memory, so that reads may pass other memory operations.
+__device__ __forceinline__ uint4 step16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
 }
-
+__device__ __forceinline__ uint2 step8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
   uint32_t v;
-  asm volatile("{\n\t.reg .b16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
-               : "=r"(v)
-               : "r"(a)
-               : "memory");
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_shared4(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-// 16 bytes of which `real` come from global memory and the others are zeros.
-__device__ __forceinline__ void copy16_part(uint32_t smem, const uint8_t* p, int real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(p), "r"(real)
-               : "memory");
+__device__ __forceinline__ void st_shared_u8(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+// `bytes` (a multiple of 16, both addresses too) to shared memory, counted at mbarrier `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t smem, const uint8_t* p, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem),
+      "l"(p), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits for a step's copies; false (and the device error word is set) past the limit.
+__device__ __noinline__ bool fp4_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                      unsigned* err_word) {
+  const uint64_t deadline = global_timer_ns() + timeout_ns;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0 && global_timer_ns() > deadline) {
+      atomicOr(err_word, kErrTimeout);
+      return false;
+    }
+  }
 }
 // An 8 x 8 matrix of 16-bit values, transposed: lane (r, q) gives row r's 2q, 2q + 1 and takes
 // column r's.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t both(uint32_t h2, int high) {
   return __byte_perm(h2, h2, high ? 0x3232 : 0x1010);
 }
 
-template <int D, int NT, DecMode MODE>
-__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
+template <int D, int H, DecMode MODE>
+__global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     fp4_decode_kernel(const PagedDecodeArgs a, int cluster) {
   using C = Fp4Cfg<D>;
   constexpr bool ONE = MODE == kOne, WARPS = MODE == kWarps;
+  constexpr int NT = H <= 8 ? 1 : 2;     // tiles of 8 heads
+  constexpr bool FOLD = H == 4;          // columns 4 to 7 are the same heads: there P's second term
   constexpr int kTile = WARPS ? C::kKeys : C::kTile;  // keys that a run is counted in
   constexpr float kShift = 14.f;
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ float s_m[kDecWarps][8 * NT], s_l[kDecWarps][8 * NT];
   __shared__ int s_bad[kDecWarps];
+  // pieces and run of each warp: read at their borders, not worth registers in between
+  __shared__ Piece s_piece[kDecWarps], s_ld[kDecWarps];
+  __shared__ int64_t s_run[kDecWarps][2];
+  __shared__ uint64_t s_full[kDecWarps][C::kStages];  // a step's copies have landed
   float(*s_o)[8][D] = reinterpret_cast<float(*)[8][D]>(dyn + C::kRing);  // [warp][head][d]
   float* s_part = reinterpret_cast<float*>(dyn);  // ONE, at the end: [head][d]
   __shared__ float2 s_pml[ONE ? 8 * NT : 1];
@@ -111,20 +153,20 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
   const int cta = ONE ? static_cast<int>(blockIdx.x) % cluster
                       : WARPS ? static_cast<int>(blockIdx.x) * kDecWarps + warp : blockIdx.x;
   const int ctas = WARPS ? static_cast<int>(gridDim.x) * kDecWarps : gridDim.x;
-  Piece cur;
+  Piece first;
   int64_t run_end, run_total = 0;
   if constexpr (ONE) {
     const int pair = static_cast<int>(blockIdx.x) / cluster;
-    cur.b = pair / a.hkv;
-    cur.g = pair % a.hkv;
-    cur.len = checked_len(a, cur.b);
-    if (cur.len <= 0) {  // the same for every CTA of the cluster
-      if (cta == 0) write_empty(a, cur.b, cur.len, cur.g * G, (cur.g + 1) * G, D);
+    first.b = pair / a.hkv;
+    first.g = pair % a.hkv;
+    first.len = checked_len(a, first.b);
+    if (first.len <= 0) {  // the same for every CTA of the cluster
+      if (cta == 0) write_empty(a, first.b, first.len, first.g * G, (first.g + 1) * G, D);
       return;
     }
-    const int tiles = (cur.len + C::kTile - 1) / C::kTile;
-    cur.piece0 = 0;
-    cur.at = first_tile(cta, tiles, cluster);
+    const int tiles = (first.len + C::kTile - 1) / C::kTile;
+    first.piece0 = 0;
+    first.at = first_tile(cta, tiles, cluster);
     run_end = first_tile(cta + 1, tiles, cluster);
   } else {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -136,80 +178,98 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
     const RunStart run = find_run(a, kTile, cta, ctas);
     if (WARPS ? lane == 0 : threadIdx.x == 0) a.rec[cta] = DecodeRec{-1, 0, 0, 0};
     if (run.begin >= run.end) return;
-    cur.b = run.seq;
-    cur.len = checked_len(a, cur.b);
-    const int tiles = (cur.len + kTile - 1) / kTile;
-    cur.g = static_cast<int>((run.begin - run.seq_tile0) / tiles);
-    cur.piece0 = run.seq_tile0 + static_cast<int64_t>(cur.g) * tiles;
-    cur.at = run.begin;
+    first.b = run.seq;
+    first.len = checked_len(a, first.b);
+    const int tiles = (first.len + kTile - 1) / kTile;
+    first.g = static_cast<int>((run.begin - run.seq_tile0) / tiles);
+    first.piece0 = run.seq_tile0 + static_cast<int64_t>(first.g) * tiles;
+    first.at = run.begin;
     run_end = run.end;
     run_total = run.total;
   }
-  set_piece<kTile>(a, run_end, cur);
+  set_piece<kTile>(a, run_end, first);
 
   // ------------------------------------------------------ loads: a cursor of their own
+  // A step's keys of one page (all of them, or the page's 16 or 32) lie together in memory and in the
+  // ring: four copies, issued by one lane.
+  constexpr int kStages = C::kStages;
   const uint32_t ring = smem_u32(dyn) + warp * (kStages * C::kStep);
-  Piece ld = cur;
+  const uint32_t full = smem_u32(&s_full[warp][0]);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
+    fence_mbar_init();
+    s_piece[warp] = s_ld[warp] = first;
+    s_run[warp][0] = run_end;
+    s_run[warp][1] = run_total;
+  }
+  __syncwarp();
+  const int64_t head_bytes = static_cast<int64_t>(C::kCB + C::kSB) << a.page_shift;
+  const int64_t page_bytes = head_bytes * a.hkv;
+  const int64_t scales_at = static_cast<int64_t>(C::kCB) << a.page_shift;
+  const int page_mask = (1 << a.page_shift) - 1;
   const int own = WARPS ? 0 : warp * C::kKeys;  // the warp's first key in a tile
-  int ld_key = ld.kb + own;              // first key of the next step to load
-  bool ld_more = true;
-  int page[C::kG16];                     // pages of its 16-key blocks
+  int ld_key = first.kb + own;           // first key of the next step to load
+  int ld_ke = first.ke;
+  const int32_t* ld_table = a.table + static_cast<int64_t>(first.b) * a.max_pages;
+  int64_t ld_head = first.g * head_bytes;
+  int page = 0;                          // page of ld_key
+  bool ld_more = true, late = false;     // late: a wait ran out, the results are NaN
   uint32_t bad_steps = 0;                // bit s: a page of the step in stage s is no page
   auto seek = [&]() {                    // on to a piece that has a step for this warp
-    while (ld_more && ld_key >= ld.ke) {
-      ld_more = next_piece<kTile>(a, run_end, ld);
+    while (ld_key >= ld_ke) {
+      Piece ld = s_ld[warp];
+      ld_more = next_piece<kTile>(a, s_run[warp][0], ld);
+      if (!ld_more) return;
+      __syncwarp();
+      if (lane == 0) s_ld[warp] = ld;
+      __syncwarp();
       ld_key = ld.kb + own;
+      ld_ke = ld.ke;
+      ld_table = a.table + static_cast<int64_t>(ld.b) * a.max_pages;
+      ld_head = ld.g * head_bytes;
     }
-    if (ld_more) {
-      const int32_t* table = a.table + static_cast<int64_t>(ld.b) * a.max_pages;
-#pragma unroll
-      for (int i = 0; i < C::kG16; ++i)
-        page[i] = ld_key + 16 * i < ld.ke ? __ldg(table + ((ld_key + 16 * i) >> a.page_shift)) : 0;
-    }
+    page = __ldg(ld_table + (ld_key >> a.page_shift));
   };
-  const int64_t head_bytes = static_cast<int64_t>(C::kCB + C::kSB) << a.page_shift;
-  const int page_mask = (1 << a.page_shift) - 1;
-  // lanes 0-15 copy K's block scales, 16-31 V's: 16 bytes each, of kPieceKeys keys
-  constexpr int kPieceKeys = 16 / C::kSB;
-  const int sc_key = (lane & 15) * kPieceKeys;
-  const uint8_t* const sc_pages = lane < 16 ? a.k_pages : a.v_pages;
-  auto issue = [&](int stage) {
-    if (ld_more) {
-      // K codes, V codes, K scales, V scales
-      const uint32_t kdst = ring + stage * C::kStep, vdst = kdst + C::kCodes;
-      const uint32_t sdst = kdst + 2 * C::kCodes + 16 * lane;
-      bool bad = false;
-      int64_t base[C::kG16];             // codes of the block's first key
-      int64_t sc_at = -1;
-#pragma unroll
-      for (int i = 0; i < C::kG16; ++i) {
-        const int pos = ld_key + 16 * i;
-        const bool ok = page[i] >= 0 && page[i] < a.num_pages;
-        if (pos < ld.ke && !ok) bad = true;
-        const int at = pos & page_mask;
-        const int64_t head = (static_cast<int64_t>(page[i]) * a.hkv + ld.g) * head_bytes;
-        base[i] = pos < ld.ke && ok ? head + at * C::kCB + 16 * lane : -1;
-        if ((sc_key >> 4) == i && pos < ld.ke && ok)
-          sc_at = head + (static_cast<int64_t>(C::kCB) << a.page_shift) +
-                  (at + (sc_key & 15)) * C::kSB;
+  auto issue = [&](int stage) {          // the stage's last step has been read by every lane
+    if (!ld_more) return;
+    const uint32_t bar = full + 8 * stage, to = ring + stage * C::kStep;
+    // `keys` from the step's `from` on, in one page
+    auto load = [&](int pg, int from, int keys) {
+      const int64_t base = pg * page_bytes + ld_head;
+      const int at = (ld_key + from) & page_mask;
+      const int64_t c = base + at * C::kCB, sc = base + scales_at + at * C::kSB;
+      const uint32_t codes = to + from * C::kCB, scales = to + 2 * C::kCodes + from * C::kSB;
+      bulk_load(codes, a.k_pages + c, keys * C::kCB, bar);
+      bulk_load(codes + C::kCodes, a.v_pages + c, keys * C::kCB, bar);
+      bulk_load(scales, a.k_pages + sc, keys * C::kSB, bar);
+      bulk_load(scales + C::kScales, a.v_pages + sc, keys * C::kSB, bar);
+    };
+    bool bad = static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages);
+    if (page_mask >= C::kKeys - 1) {     // a step is in one page, whose end it may pass the keys' by
+      if (!bad && elect_one()) {
+        mbar_expect_tx(bar, C::kStep);
+        if (a.inject_skip_loads == 0) load(page, 0, C::kKeys);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        constexpr int kPieces = C::kCB / 16;  // of a row
-        const int row = lane / kPieces + j * (32 / kPieces), c = lane % kPieces;
-        const int64_t at = base[j * (32 / kPieces) >> 4];
-        const bool real = at >= 0 && ld_key + row < ld.ke;
-        const int64_t off = real ? at + (D == 128 ? (j & 1) * 512 : 0) : 0;
-        copy16(kdst + 16 * (lane + 32 * j), a.k_pages + off, real);
-        copy16(vdst + 16 * fp4_v_place<D>(row, c), a.v_pages + off, real);
+      if (bad && elect_one()) mbar_expect_tx(bar, 0);
+    } else {
+      const int parts = (min(C::kKeys, ld_ke - ld_key) + page_mask) >> a.page_shift;
+      const int pg = lane < parts ? __ldg(ld_table + (ld_key >> a.page_shift) + lane) : 0;
+      const unsigned none = __ballot_sync(
+          0xFFFFFFFFu, static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages));
+      bad = none != 0;
+      if (elect_one())
+        mbar_expect_tx(bar, static_cast<uint32_t>(parts - __popc(none)) * (2 * (C::kCB + C::kSB)) * (page_mask + 1));
+      __syncwarp();
+      for (int i = 0; i < parts; ++i) {
+        const int pg_i = __shfl_sync(0xFFFFFFFFu, pg, i);
+        if (((none >> i) & 1u) == 0 && a.inject_skip_loads == 0 && elect_one())
+          load(pg_i, i << a.page_shift, page_mask + 1);
       }
-      const int keys = sc_at >= 0 ? max(0, min(kPieceKeys, ld.ke - ld_key - sc_key)) : 0;
-      copy16_part(sdst, sc_pages + (keys > 0 ? sc_at : 0), keys * C::kSB);
-      bad_steps = bad ? bad_steps | (1u << stage) : bad_steps & ~(1u << stage);
-      ld_key += kTile;
-      seek();
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    bad_steps = bad ? bad_steps | (1u << stage) : bad_steps & ~(1u << stage);
+    ld_key += kTile;
+    seek();
   };
 
   // Q of a piece as it is in memory: the D / 4 values from d = q4 D / 4 of head r (+ 8)
@@ -217,7 +277,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
   auto load_q = [&](int b, int g) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int h = r + 8 * n;
+      const int h = FOLD ? r & 3 : r + 8 * n;
       const uint4* qp = reinterpret_cast<const uint4*>(
           a.q + static_cast<int64_t>(b) * a.q_stride + static_cast<int64_t>(g * G + h) * D +
           q4 * (D / 4));
@@ -227,18 +287,25 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
     }
   };
 
+  // Row i of a product's 8 keys is key i ^ (i / 2 % 2): the rows that a read of V's takes at once
+  // lie half on even and half on odd keys, on different banks.
+  const int kr = r ^ ((r >> 1) & 1);
+  const int v_row[2] = {2 * q4 + (q4 & 1), 2 * q4 + (~q4 & 1)};
+
   seek();
-  load_q(cur.b, cur.g);
+  load_q(first.b, first.g);
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) issue(s);
   int stage = 0;
+  uint32_t parity = 0;
 
   while (true) {
     // ---------------------------------------------------- one piece
+    const int key_end = s_piece[warp].ke, key_begin = s_piece[warp].kb;
     uint32_t qb[NT][C::kQS][2];
     float c_log2[NT][2];                 // of heads 2 q4, 2 q4 + 1 (+ 8 n)
     {
-      const float ks = __ldg(a.k_scale + static_cast<int64_t>(cur.b) * a.hkv + cur.g);
+      const float ks = __ldg(a.k_scale + static_cast<int64_t>(s_piece[warp].b) * a.hkv + s_piece[warp].g);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint32_t top = 0;
@@ -281,58 +348,77 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
     }
     bool bad = false;
 
-    for (int key0 = cur.kb + own; key0 < cur.ke; key0 += kTile) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncwarp();  // every lane's copies are there, and the stage before was read
-      bad |= (bad_steps >> stage) & 1u;
+    for (int key0 = key_begin + own; key0 < key_end; key0 += kTile) {
+      __syncwarp();  // the stage before was read by every lane
       issue(stage == 0 ? kStages - 1 : stage - 1);
+      if (!late && !__all_sync(0xFFFFFFFFu, mbar_try_wait(full + 8 * stage, parity)))
+        late = !__all_sync(0xFFFFFFFFu, fp4_wait(full + 8 * stage, parity, a.timeout_ns, a.err_word)),
+        ld_more &= !late;
+      bad |= late || ((bad_steps >> stage) & 1u);
       const uint32_t kbuf = ring + stage * C::kStep, vbuf = kbuf + C::kCodes;
       const uint32_t ksc = kbuf + 2 * C::kCodes, vsc = ksc + C::kScales;
-      stage = stage == kStages - 1 ? 0 : stage + 1;
+      if (++stage == kStages) {
+        stage = 0;
+        parity ^= 1;
+      }
+      const bool tail = key0 + C::kKeys > key_end;
+      if (tail) {  // what a page holds behind the last key may be no number: scales of zero
+        __syncwarp();
+        for (int i = (key_end - key0) * C::kSB + lane; i < C::kScales; i += 32) st_shared_u8(vsc + i, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a later copy there
+        __syncwarp();
+      }
 
       // ---- scores of this step's keys: s[i][n] = keys r, r + 8 of block i by heads 2 q4, + 1
       float s[C::kG16][NT][4];
 #pragma unroll
-      for (int i = 0; i < C::kG16; ++i) {
+      for (int i0 = 0; i0 < C::kG16; i0 += kSide) {  // blocks of keys side by side
+        uint32_t w[kSide][2][D / 32], sc[kSide][2][D / 64];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = 0.f;
-        uint32_t w[2][D / 32], sc[2][D / 64];
+        for (int i = 0; i < kSide; ++i)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int key = 16 * i + 8 * u + r;
-          if constexpr (D == 128) {
-            const uint4 x = ld_shared16(kbuf + key * C::kCB + 16 * q4);
-            w[u][0] = x.x;
-            w[u][1] = x.y;
-            w[u][2] = x.z;
-            w[u][3] = x.w;
-            const uint32_t h2 = e4m3_lo(ld_shared_u16(ksc + key * C::kSB + 2 * q4));
-            sc[u][0] = both(h2, 0);
-            sc[u][1] = both(h2, 1);
-          } else {
-            const uint2 x = ld_shared8(kbuf + key * C::kCB + 8 * q4);
-            w[u][0] = x.x;
-            w[u][1] = x.y;
-            sc[u][0] = both(e4m3_lo(ld_shared_u8(ksc + key * C::kSB + q4)), 0);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {  // 8 codes of each key: two k-steps
-          uint32_t x[4], y[4];
-          e2m1x8(w[0][j], x);
-          e2m1x8(w[1][j], y);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[k] = mul_f16x2(x[k], sc[0][j >> 1]);
-            y[k] = mul_f16x2(y[k], sc[1][j >> 1]);
+          for (int u = 0; u < 2; ++u) {
+            const int key = 16 * (i0 + i) + 8 * u + kr;
+            if constexpr (D == 128) {
+              const uint4 x = step16(kbuf + key * C::kCB + 16 * q4);
+              w[i][u][0] = x.x;
+              w[i][u][1] = x.y;
+              w[i][u][2] = x.z;
+              w[i][u][3] = x.w;
+              const uint32_t h2 = e4m3_lo(ld_shared_u16(ksc + key * C::kSB + 2 * q4));
+              sc[i][u][0] = both(h2, 0);
+              sc[i][u][1] = both(h2, 1);
+            } else {
+              const uint2 x = step8(kbuf + key * C::kCB + 8 * q4);
+              w[i][u][0] = x.x;
+              w[i][u][1] = x.y;
+              sc[i][u][0] = both(e4m3_lo(ld_shared_u8(ksc + key * C::kSB + q4)), 0);
+            }
           }
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+        for (int i = 0; i < kSide; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma16816<true>(s[i][n], x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1],
-                             qb[n][2 * j + k][0], qb[n][2 * j + k][1]);
-        }
+          for (int n = 0; n < NT; ++n)
+            s[i0 + i][n][0] = s[i0 + i][n][1] = s[i0 + i][n][2] = s[i0 + i][n][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)  // 8 codes of each key: two k-steps
+#pragma unroll
+          for (int i = 0; i < kSide; ++i) {
+            uint32_t x[4], y[4];
+            e2m1x8(w[i][0][j], x);
+            e2m1x8(w[i][1][j], y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = mul_f16x2(x[k], sc[i][0][j >> 1]);
+              y[k] = mul_f16x2(y[k], sc[i][1][j >> 1]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16(s[i0 + i][n], x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1],
+                               qb[n][2 * j + k][0], qb[n][2 * j + k][1]);
+          }
       }
 
       // ---- running max and sum; x = score in log2 units
@@ -342,12 +428,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[i][n][j] *= c_log2[n][j & 1];
-      if (key0 + C::kKeys > cur.ke) {
+      if (tail) {
 #pragma unroll
         for (int i = 0; i < C::kG16; ++i)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            if (key0 + 16 * i + 8 * u + r >= cur.ke) {
+            if (key0 + 16 * i + 8 * u + kr >= key_end) {
 #pragma unroll
               for (int n = 0; n < NT; ++n) s[i][n][2 * u] = s[i][n][2 * u + 1] = -INFINITY;
             }
@@ -360,11 +446,11 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
             const int h = 8 * n + 2 * q4 + j;
             if (h < G) {
               float* row =
-                  a.raw + (static_cast<int64_t>(cur.b) * a.hq + cur.g * G + h) * a.raw_stride;
+                  a.raw + (static_cast<int64_t>(s_piece[warp].b) * a.hq + s_piece[warp].g * G + h) * a.raw_stride;
 #pragma unroll
               for (int i = 0; i < C::kG16; ++i) {  // rows are padded to whole tiles
-                row[key0 + 16 * i + r] = s[i][n][j];
-                row[key0 + 16 * i + 8 + r] = s[i][n][2 + j];
+                row[key0 + 16 * i + kr] = s[i][n][j];
+                row[key0 + 16 * i + 8 + kr] = s[i][n][2 + j];
               }
             }
           }
@@ -412,7 +498,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
       // ---- O^T += V^T P^T
 #pragma unroll
       for (int i = 0; i < C::kG16; ++i) {
-        uint32_t ps[NT][2][2];           // [head tile][f16 term][8 keys]
+        constexpr int kTerms = FOLD ? 1 : 2;
+        uint32_t ps[NT][kTerms][2];      // [head tile][f16 term][8 keys]
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -422,20 +509,20 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
             l[n][1] += x1;
             uint32_t hi, lo;
             split_f16(x0, x1, hi, lo);
-            ps[n][0][u] = transpose8(hi);
-            ps[n][1][u] = transpose8(lo);
+            ps[n][0][u] = transpose8(FOLD && q4 >= 2 ? lo : hi);
+            if constexpr (!FOLD) ps[n][1][u] = transpose8(lo);
           }
-        uint32_t w[4][C::kWords], sb[4];
+        uint32_t w[4][C::kWords], sb[4];  // codes and scales of keys 2 q4, 2 q4 + 1, and 8 on
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int row = 16 * i + 2 * q4 + (j & 1) + 8 * (j >> 1);
+          const int row = 16 * i + 8 * (j >> 1) + v_row[j & 1];
           if constexpr (D == 128) {
-            const uint2 x = ld_shared8(vbuf + 16 * fp4_v_place<D>(row, r >> 1) + 8 * (r & 1));
+            const uint2 x = step8(vbuf + row * C::kCB + 8 * r);
             w[j][0] = x.x;
             w[j][1] = x.y;
             sb[j] = ld_shared_u8(vsc + row * C::kSB + r);
           } else {
-            w[j][0] = ld_shared4(vbuf + 16 * fp4_v_place<D>(row, r >> 2) + 4 * (r & 3));
+            w[j][0] = ld_shared4(vbuf + row * C::kCB + 4 * r);
             sb[j] = ld_shared_u8(vsc + row * C::kSB + (r >> 1));
           }
         }
@@ -451,21 +538,28 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
           e2m1x8(odd(w[2][k], w[3][k]), a3);
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            const uint32_t f0 = mul_f16x2(a0[b], sc0), f1 = mul_f16x2(a1[b], sc0);
-            const uint32_t f2 = mul_f16x2(a2[b], sc1), f3 = mul_f16x2(a3[b], sc1);
+            a0[b] = mul_f16x2(a0[b], sc0);
+            a1[b] = mul_f16x2(a1[b], sc0);
+            a2[b] = mul_f16x2(a2[b], sc1);
+            a3[b] = mul_f16x2(a3[b], sc1);
+          }
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma16816<true>(o[n][4 * k + b], f0, f1, f2, f3, ps[n][t][0], ps[n][t][1]);
-          }
+                mma_f16(o[n][4 * k + b], a0[b], a1[b], a2[b], a3[b], ps[n][t][0], ps[n][t][1]);
         }
       }
     }
 
+    bad = __any_sync(0xFFFFFFFFu, bad);
+
     // the next piece's queries are on their way while this one is put together
+    const Piece cur = s_piece[warp];
     Piece nxt = cur;
-    const bool more = !ONE && next_piece<kTile>(a, run_end, nxt);
+    const bool more = !ONE && next_piece<kTile>(a, s_run[warp][0], nxt);
     if (more) load_q(nxt.b, nxt.g);
 
     // ---------------------------------------------------- the four warps' parts together
@@ -487,13 +581,20 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
       if (!cur.whole) {  // goes on in the next runs: the join's entry
         const int64_t end = cur.piece0 + (cur.len + kTile - 1) / kTile;
         // the last run of (b, g) is the one that holds tile end - 1
-        a.rec[cta] = DecodeRec{cur.b, cur.g, static_cast<int>((end * ctas - 1) / run_total),
-                               run_total < ctas ? static_cast<int>(run_total) : 0};
+        const int64_t total = s_run[warp][1];
+        a.rec[cta] = DecodeRec{cur.b, cur.g, static_cast<int>((end * ctas - 1) / total),
+                               total < ctas ? static_cast<int>(total) : 0};
       }
     };
     // d of tile t's row r; row r + 8 is the next d
     auto out_d = [&](int t) { return r * (D / 8) + 2 * t; };
     if constexpr (WARPS) {
+      if constexpr (FOLD) {
+#pragma unroll
+        for (int t = 0; t < C::kMT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[0][t][j] += __shfl_xor_sync(0xFFFFFFFFu, o[0][t][j], 2);
+      }
       if (lane == 0) note(bad);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -549,7 +650,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
               make_float4(o[n][t][j], o[n][t][2 + j], o[n][t + 1][j], o[n][t + 1][2 + j]);
       __syncthreads();
       const bool any_bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
-      const int heads = min(8, G - 8 * n);
+      const int heads = min(FOLD ? 4 : 8, G - 8 * n);
       for (int i = threadIdx.x; i < heads * D; i += kDecThreads) {
         const int h = i / D, d = i % D, hh = 8 * n + h;
         float top = s_m[0][hh];
@@ -560,7 +661,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
         for (int w = 0; w < kDecWarps; ++w) {
           const float f = s_m[w][hh] == -INFINITY ? 0.f : ex2(s_m[w][hh] - top);
           sum = fmaf(s_l[w][hh], f, sum);
-          acc = fmaf(s_o[w][h][d], f, acc);
+          acc = fmaf(FOLD ? s_o[w][h][d] + s_o[w][h + 4][d] : s_o[w][h][d], f, acc);
         }
         if (any_bad) sum = __int_as_float(0x7FFFFFFF);
         const int64_t row = static_cast<int64_t>(cur.b) * a.hq + cur.g * G + hh;
@@ -584,34 +685,40 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 3 : 2)
     }
     if constexpr (ONE) break;
     if (!more) break;
-    cur = nxt;
+    __syncwarp();
+    if (lane == 0) s_piece[warp] = nxt;
+    __syncwarp();
   }
+  if (late)  // what is still on its way lands before the memory is given up, or the limit passes
+    for (int i = 0; i < kStages; ++i) fp4_wait(full + 8 * i, i < stage ? parity : parity ^ 1, a.timeout_ns, a.err_word);
 
-  if constexpr (ONE) join_cluster<D>(a, cur, cluster, cta, s_part, s_pml, s_lse2, kShift, true);
+  if constexpr (ONE) join_cluster<D>(a, s_piece[warp], cluster, cta, s_part, s_pml, s_lse2, kShift, true);
 }
 
-template <int D, int NT>
+template <int D, int H>
 struct Fp4Kernel : Fp4Cfg<D> {
-  static constexpr int kDim = D, kPerSm = NT == 1 ? 3 : 2, kOneTiles = 8;
+  static constexpr int kDim = D, kPerSm = H <= 8 ? kFp4PerSm : 2, kOneTiles = 8;
   static constexpr float kShift = 14.f;
   static auto fn(DecMode mode) {
-    return mode == kOne ? fp4_decode_kernel<D, NT, kOne>
-           : mode == kWarps ? fp4_decode_kernel<D, NT, kWarps>
-                            : fp4_decode_kernel<D, NT, kSplit>;
+    return mode == kOne ? fp4_decode_kernel<D, H, kOne>
+           : mode == kWarps ? fp4_decode_kernel<D, H, kWarps>
+                            : fp4_decode_kernel<D, H, kSplit>;
   }
 };
+template <int D>
+cudaError_t launch_fp4_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.group <= 4) return launch_decode<Fp4Kernel<D, 4>>(a, num_sms, stream);
+  if (a.group <= 8) return launch_decode<Fp4Kernel<D, 8>>(a, num_sms, stream);
+  return launch_decode<Fp4Kernel<D, 16>>(a, num_sms, stream);
+}
 
 }  // namespace
 
-int fp4_decode_per_sm(int group) { return group > 8 ? 2 : 3; }
+int fp4_decode_per_sm(int group) { return group > 8 ? 2 : kFp4PerSm; }
 
 cudaError_t launch_fp4_decode(PagedDecodeArgs& a, int head_dim, int num_sms, cudaStream_t stream) {
-  const bool two = a.group > 8;
-  if (head_dim == 128)
-    return two ? launch_decode<Fp4Kernel<128, 2>>(a, num_sms, stream)
-               : launch_decode<Fp4Kernel<128, 1>>(a, num_sms, stream);
-  return two ? launch_decode<Fp4Kernel<64, 2>>(a, num_sms, stream)
-             : launch_decode<Fp4Kernel<64, 1>>(a, num_sms, stream);
+  return head_dim == 128 ? launch_fp4_decode_t<128>(a, num_sms, stream)
+                         : launch_fp4_decode_t<64>(a, num_sms, stream);
 }
 
 }  // namespace quail

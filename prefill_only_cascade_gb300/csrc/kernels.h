@@ -251,6 +251,9 @@ struct PagedDecodeArgs {
   float* raw;                       // [B, Hq, raw_stride] scores in log2 units, or NULL
   int64_t raw_stride;
   unsigned* err_word;
+  // fp4 pages: how long a wait for a step's copies may block; no copies, so that it does
+  uint64_t timeout_ns;
+  int inject_skip_loads;
 };
 constexpr int kDecodeMaxSms = 160;  // the workspace holds the parts of so many SMs' CTAs
 int decode_tile_keys(int head_dim, int kv_dtype);
