@@ -274,7 +274,10 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
 
   // Q of a piece as it is in memory: the D / 4 values from d = q4 D / 4 of head r (+ 8)
   uint4 qraw[NT][D / 32];
+  float k_scale, v_scale;                // of the same (sequence, head)
   auto load_q = [&](int b, int g) {
+    k_scale = __ldg(a.k_scale + static_cast<int64_t>(b) * a.hkv + g);
+    v_scale = __ldg(a.v_scale + static_cast<int64_t>(b) * a.hkv + g);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int h = FOLD ? r & 3 : r + 8 * n;
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     uint32_t qb[NT][C::kQS][2];
     float c_log2[NT][2];                 // of heads 2 q4, 2 q4 + 1 (+ 8 n)
     {
-      const float ks = __ldg(a.k_scale + static_cast<int64_t>(s_piece[warp].b) * a.hkv + s_piece[warp].g);
+      const float ks = k_scale;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint32_t top = 0;
@@ -558,12 +561,12 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
 
     // the next piece's queries are on their way while this one is put together
     const Piece cur = s_piece[warp];
+    const float vs = v_scale;
     Piece nxt = cur;
     const bool more = !ONE && next_piece<kTile>(a, s_run[warp][0], nxt);
     if (more) load_q(nxt.b, nxt.g);
 
     // ---------------------------------------------------- the four warps' parts together
-    const float vs = __ldg(a.v_scale + static_cast<int64_t>(cur.b) * a.hkv + cur.g);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -645,38 +648,49 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
 #pragma unroll
       for (int t = 0; t < C::kMT; t += 2)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<float4*>(&s_o[warp][2 * q4 + j][out_d(t)]) =
+        for (int j = 0; j < 2; ++j)  // 16-byte units, spread over the banks by the heads' pairs
+          *reinterpret_cast<float4*>(&s_o[warp][2 * q4 + j][4 * ((out_d(t) / 4) ^ q4)]) =
               make_float4(o[n][t][j], o[n][t][2 + j], o[n][t + 1][j], o[n][t + 1][2 + j]);
       __syncthreads();
       const bool any_bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
       const int heads = min(FOLD ? 4 : 8, G - 8 * n);
-      for (int i = threadIdx.x; i < heads * D; i += kDecThreads) {
-        const int h = i / D, d = i % D, hh = 8 * n + h;
+      const int d = 4 * (threadIdx.x % (D / 4));
+      for (int h = threadIdx.x / (D / 4); h < heads; h += 4 * kDecThreads / D) {
+        const int hh = 8 * n + h;
         float top = s_m[0][hh];
 #pragma unroll
         for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, s_m[w][hh]);
-        float sum = 0.f, acc = 0.f;
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](int w, int row, float f) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_o[w][row][4 * ((d / 4) ^ ((row >> 1) & 3))]);
+          acc.x = fmaf(x.x, f, acc.x);
+          acc.y = fmaf(x.y, f, acc.y);
+          acc.z = fmaf(x.z, f, acc.z);
+          acc.w = fmaf(x.w, f, acc.w);
+        };
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
           const float f = s_m[w][hh] == -INFINITY ? 0.f : ex2(s_m[w][hh] - top);
           sum = fmaf(s_l[w][hh], f, sum);
-          acc = fmaf(FOLD ? s_o[w][h][d] + s_o[w][h + 4][d] : s_o[w][h][d], f, acc);
+          add(w, h, f);
+          if constexpr (FOLD) add(w, h + 4, f);
         }
         if (any_bad) sum = __int_as_float(0x7FFFFFFF);
         const int64_t row = static_cast<int64_t>(cur.b) * a.hq + cur.g * G + hh;
         if constexpr (ONE) {  // over the ring: every warp has used its last step
-          s_part[hh * D + d] = acc;
+          *reinterpret_cast<float4*>(&s_part[hh * D + d]) = acc;
           if (d == 0) s_pml[hh] = make_float2(top, sum);
         } else if (cur.whole) {
-          a.out[row * D + d] = __float2bfloat16(acc / sum * vs);
+          *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(
+              pack2<false>(acc.x / sum * vs, acc.y / sum * vs), pack2<false>(acc.z / sum * vs, acc.w / sum * vs));
           if (d == 0) {
             const float lse2 = top + (log2f(sum) - kShift);
             if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
             if (a.lse2 != nullptr) a.lse2[row] = lse2;
           }
         } else {
-          a.part_o[(part * G + hh) * D + d] = acc;
+          *reinterpret_cast<float4*>(a.part_o + (part * G + hh) * D + d) = acc;
           if (d == 0) a.part_ml[part * G + hh] = make_float2(top, sum);
         }
       }
