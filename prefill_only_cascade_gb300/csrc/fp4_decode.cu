@@ -130,7 +130,8 @@ template <int D, int H, DecMode MODE>
 __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     fp4_decode_kernel(const PagedDecodeArgs a, int cluster) {
   using C = Fp4Cfg<D>;
-  constexpr bool ONE = MODE == kOne, WARPS = MODE == kWarps;
+  constexpr bool ONE = MODE == kOne, PAIRS = MODE == kPairs;
+  constexpr bool WARPS = MODE == kWarps || PAIRS;  // no warp waits for another
   constexpr int NT = H <= 8 ? 1 : 2;     // tiles of 8 heads
   constexpr bool FOLD = H == 4;          // columns 4 to 7 are the same heads: there P's second term
   constexpr int kTile = WARPS ? C::kKeys : C::kTile;  // keys that a run is counted in
@@ -153,8 +154,20 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
   const int cta = ONE ? static_cast<int>(blockIdx.x) % cluster
                       : WARPS ? static_cast<int>(blockIdx.x) * kDecWarps + warp : blockIdx.x;
   const int ctas = WARPS ? static_cast<int>(gridDim.x) * kDecWarps : gridDim.x;
+  // PAIRS: the next (sequence, head) with tokens of this warp's, from p.at on; what the others get
+  // is written on one of the two walks over them
+  auto next_pair = [&](Piece& p, bool write) {
+    for (; p.at < static_cast<int64_t>(a.num_seqs) * a.hkv; p.at += ctas) {
+      p.b = static_cast<int>(p.at / a.hkv);
+      p.g = static_cast<int>(p.at % a.hkv);
+      p.len = p.ke = checked_len(a, p.b);
+      if (p.len > 0) return true;
+      if (write) write_empty(a, p.b, p.len, p.g * G, (p.g + 1) * G, D, lane, 32);
+    }
+    return false;
+  };
   Piece first;
-  int64_t run_end, run_total = 0;
+  int64_t run_end = 0, run_total = 0;
   if constexpr (ONE) {
     const int pair = static_cast<int>(blockIdx.x) / cluster;
     first.b = pair / a.hkv;
@@ -168,6 +181,11 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     first.piece0 = 0;
     first.at = first_tile(cta, tiles, cluster);
     run_end = first_tile(cta + 1, tiles, cluster);
+  } else if constexpr (PAIRS) {
+    first.at = cta;
+    first.kb = 0;
+    first.whole = true;
+    if (!next_pair(first, true)) return;
   } else {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // sequences without tokens (0 and -inf) and with lengths out of range (NaN)
@@ -187,7 +205,7 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     run_end = run.end;
     run_total = run.total;
   }
-  set_piece<kTile>(a, run_end, first);
+  if constexpr (!PAIRS) set_piece<kTile>(a, run_end, first);
 
   // ------------------------------------------------------ loads: a cursor of their own
   // A step's keys of one page (all of them, or the page's 16 or 32) lie together in memory and in the
@@ -213,13 +231,18 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
   int ld_ke = first.ke;
   const int32_t* ld_table = a.table + static_cast<int64_t>(first.b) * a.max_pages;
   int64_t ld_head = first.g * head_bytes;
-  int page = 0;                          // page of ld_key
+  int page = 0;                          // page of ld_key; where a step has several, lane i has the i-th
   bool ld_more = true, late = false;     // late: a wait ran out, the results are NaN
   uint32_t bad_steps = 0;                // bit s: a page of the step in stage s is no page
   auto seek = [&]() {                    // on to a piece that has a step for this warp
     while (ld_key >= ld_ke) {
       Piece ld = s_ld[warp];
-      ld_more = next_piece<kTile>(a, s_run[warp][0], ld);
+      if constexpr (PAIRS) {
+        ld.at += ctas;
+        ld_more = next_pair(ld, false);
+      } else {
+        ld_more = next_piece<kTile>(a, s_run[warp][0], ld);
+      }
       if (!ld_more) return;
       __syncwarp();
       if (lane == 0) s_ld[warp] = ld;
@@ -229,7 +252,8 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
       ld_table = a.table + static_cast<int64_t>(ld.b) * a.max_pages;
       ld_head = ld.g * head_bytes;
     }
-    page = __ldg(ld_table + (ld_key >> a.page_shift));
+    const int last = (min(C::kKeys, ld_ke - ld_key) - 1 + (ld_key & page_mask)) >> a.page_shift;
+    page = __ldg(ld_table + (ld_key >> a.page_shift) + min(lane, last));
   };
   auto issue = [&](int stage) {          // the stage's last step has been read by every lane
     if (!ld_more) return;
@@ -245,26 +269,25 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
       bulk_load(scales, a.k_pages + sc, keys * C::kSB, bar);
       bulk_load(scales + C::kScales, a.v_pages + sc, keys * C::kSB, bar);
     };
-    bool bad = static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages);
-    if (page_mask >= C::kKeys - 1) {     // a step is in one page, whose end it may pass the keys' by
-      if (!bad && elect_one()) {
-        mbar_expect_tx(bar, C::kStep);
-        if (a.inject_skip_loads == 0) load(page, 0, C::kKeys);
+    const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages);
+    bool bad;
+    if (page_mask >= C::kKeys - 1) {     // a step is in one page (whose rows past the last key come too)
+      bad = !ok;
+      if (elect_one()) {
+        mbar_expect_tx(bar, ok ? C::kStep : 0);
+        if (ok && a.inject_skip_loads == 0) load(page, 0, C::kKeys);
       }
-      if (bad && elect_one()) mbar_expect_tx(bar, 0);
     } else {
       const int parts = (min(C::kKeys, ld_ke - ld_key) + page_mask) >> a.page_shift;
-      const int pg = lane < parts ? __ldg(ld_table + (ld_key >> a.page_shift) + lane) : 0;
-      const unsigned none = __ballot_sync(
-          0xFFFFFFFFu, static_cast<unsigned>(pg) >= static_cast<unsigned>(a.num_pages));
-      bad = none != 0;
+      unsigned todo = __ballot_sync(0xFFFFFFFFu, ok && lane < parts);
+      bad = __popc(todo) != parts;
       if (elect_one())
-        mbar_expect_tx(bar, static_cast<uint32_t>(parts - __popc(none)) * (2 * (C::kCB + C::kSB)) * (page_mask + 1));
+        mbar_expect_tx(bar, __popc(todo) * (2 * (C::kCB + C::kSB) << a.page_shift));
       __syncwarp();
-      for (int i = 0; i < parts; ++i) {
-        const int pg_i = __shfl_sync(0xFFFFFFFFu, pg, i);
-        if (((none >> i) & 1u) == 0 && a.inject_skip_loads == 0 && elect_one())
-          load(pg_i, i << a.page_shift, page_mask + 1);
+      if (a.inject_skip_loads != 0) todo = 0;
+      for (; todo != 0; todo &= todo - 1) {
+        const int i = __ffs(todo) - 1, pg = __shfl_sync(0xFFFFFFFFu, page, i);
+        if (elect_one()) load(pg, i << a.page_shift, page_mask + 1);
       }
     }
     bad_steps = bad ? bad_steps | (1u << stage) : bad_steps & ~(1u << stage);
@@ -563,7 +586,13 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     const Piece cur = s_piece[warp];
     const float vs = v_scale;
     Piece nxt = cur;
-    const bool more = !ONE && next_piece<kTile>(a, s_run[warp][0], nxt);
+    bool more = false;
+    if constexpr (PAIRS) {
+      nxt.at += ctas;
+      more = next_pair(nxt, true);
+    } else if constexpr (!ONE) {
+      more = next_piece<kTile>(a, s_run[warp][0], nxt);
+    }
     if (more) load_q(nxt.b, nxt.g);
 
     // ---------------------------------------------------- the four warps' parts together
@@ -578,7 +607,7 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     const int64_t part = 2 * static_cast<int64_t>(cta) + (cur.at == cur.piece0 ? 1 : 0);
     auto note = [&](bool any_bad) {      // by one thread, about (b, g)
       if (any_bad) atomicOr(a.err_word, kErrDeviceBounds);
-      if (ONE || cur.at != cur.piece0) return;
+      if (ONE || PAIRS || cur.at != cur.piece0) return;
       if (a.begun != nullptr)
         a.begun[static_cast<int64_t>(cur.b) * a.hkv + cur.g] = cur.whole ? -1 : cta;
       if (!cur.whole) {  // goes on in the next runs: the join's entry
@@ -611,7 +640,7 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
             if (cur.whole) {
               const float lse2 = m[n][j] + (log2f(sum) - kShift);
               if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
-              if (a.lse2 != nullptr) a.lse2[row] = lse2;
+              if (!PAIRS && a.lse2 != nullptr) a.lse2[row] = lse2;
             } else {
               a.part_ml[part * G + h] = make_float2(m[n][j], sum);
             }
@@ -634,6 +663,31 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
             }
           }
         }
+    }
+    if constexpr (PAIRS) {  // the weights of these keys, from the scores that the warp has stored
+      if (a.raw != nullptr) {
+        float lse2[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            lse2[n][j] = bad ? __int_as_float(0x7FFFFFFF) : m[n][j] + (log2f(l[n][j]) - kShift);
+        __syncwarp();
+        const int64_t pair = static_cast<int64_t>(cur.b) * a.hkv + cur.g;
+        const float* raw = a.raw + pair * G * a.raw_stride;
+        for (int k0 = 0; k0 < cur.len; k0 += 32) {
+          const int k = k0 + lane;
+          float w = 0.f;
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const float z = __shfl_sync(0xFFFFFFFFu, lse2[h >> 3][h & 1], (h & 7) >> 1);
+            if (h < G && k < cur.len && z > -INFINITY) w += ex2(raw[h * a.raw_stride + k] - z);
+          }
+          if (k < cur.len)
+            a.score_out[pair * a.score_stride + k] =
+                (a.score_in != nullptr ? a.score_in[pair * a.score_stride + k] : 0.f) + w;
+        }
+      }
     }
 #pragma unroll
     for (int n = 0; n < (WARPS ? 0 : NT); ++n) {
@@ -712,10 +766,12 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
 template <int D, int H>
 struct Fp4Kernel : Fp4Cfg<D> {
   static constexpr int kDim = D, kPerSm = H <= 8 ? kFp4PerSm : 2, kOneTiles = 8;
+  static constexpr int kPairSteps = 8;
   static constexpr float kShift = 14.f;
   static auto fn(DecMode mode) {
     return mode == kOne ? fp4_decode_kernel<D, H, kOne>
            : mode == kWarps ? fp4_decode_kernel<D, H, kWarps>
+           : mode == kPairs ? fp4_decode_kernel<D, H, kPairs>
                             : fp4_decode_kernel<D, H, kSplit>;
   }
 };

@@ -680,6 +680,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 template <int D, bool FP8, int NT>
 struct DecKernel : DecCfg<D, FP8> {
   static constexpr int kDim = D, kPerSm = 2, kOneTiles = 8;
+  static constexpr int kPairSteps = -1;  // no such launch
   static constexpr float kShift = FP8 ? 14.f : 0.f;
   static auto fn(DecMode mode) {
     return mode == kOne ? paged_decode_kernel<D, FP8, NT, kOne>

@@ -193,15 +193,20 @@ __device__ __forceinline__ bool next_piece(const PagedDecodeArgs& a, int64_t end
   return true;
 }
 
+// The outputs of heads h0 .. h1 of a sequence of n tokens: none, or fewer (a length out of range).
 __device__ __forceinline__ void write_empty(const PagedDecodeArgs& a, int b, int n, int h0, int h1,
-                                            int D) {
+                                            int D, int thread, int threads) {
   const float nan = __int_as_float(0x7FFFFFFF);
-  if (n < 0 && threadIdx.x == 0) atomicOr(a.err_word, kErrDeviceBounds);
+  if (n < 0 && thread == 0) atomicOr(a.err_word, kErrDeviceBounds);
   const int64_t row = static_cast<int64_t>(b) * a.hq;
-  for (int i = h0 * D + threadIdx.x; i < h1 * D; i += kDecThreads)
+  for (int i = h0 * D + thread; i < h1 * D; i += threads)
     a.out[row * D + i] = __float2bfloat16(n < 0 ? nan : 0.f);
   if (a.lse != nullptr)
-    for (int i = h0 + threadIdx.x; i < h1; i += kDecThreads) a.lse[row + i] = n < 0 ? nan : -INFINITY;
+    for (int i = h0 + thread; i < h1; i += threads) a.lse[row + i] = n < 0 ? nan : -INFINITY;
+}
+__device__ __forceinline__ void write_empty(const PagedDecodeArgs& a, int b, int n, int h0, int h1,
+                                            int D) {
+  write_empty(a, b, n, h0, h1, D, threadIdx.x, kDecThreads);
 }
 
 __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
@@ -276,7 +281,8 @@ __device__ __forceinline__ void join_cluster(const PagedDecodeArgs& a, const Pie
 enum DecMode {
   kSplit,  // runs of CTA tiles, a run per CTA
   kOne,    // one launch: a cluster per (sequence, head)
-  kWarps   // runs of a warp's steps, a run per warp: no warp waits for another
+  kWarps,  // runs of a warp's steps, a run per warp: no warp waits for another
+  kPairs   // one launch: a warp per (sequence, head), and on to the next
 };
 
 // Joins the partials of every (sequence, head) that more than one CTA worked on. Its CTAs
@@ -547,6 +553,14 @@ cudaError_t launch_decode(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) 
     one.attrs = &dims;
     one.numAttrs = 1;
     return cudaLaunchKernelEx(&one, K::fn(kOne), a, cluster);
+  }
+  if (K::kPairSteps * K::kKeys >= a.max_len) {
+    static std::atomic<uint64_t> pairs_ready{0};
+    e = allow_smem(reinterpret_cast<const void*>(K::fn(kPairs)), K::kRing, pairs_ready);
+    if (e != cudaSuccess) return e;
+    const int64_t all = (pairs + kDecWarps - 1) / kDecWarps, fit = static_cast<int64_t>(K::kPerSm) * num_sms;
+    K::fn(kPairs)<<<static_cast<unsigned>(all < fit ? all : fit), kDecThreads, K::kRing, stream>>>(a, 1);
+    return cudaGetLastError();
   }
   // runs of warps or of CTAs
   const bool warps = decode_by_warps(a.num_seqs, a.hkv, a.max_len, K::kTile);
