@@ -103,17 +103,28 @@ __device__ __forceinline__ void bulk_load(uint32_t smem, const uint8_t* p, uint3
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Waits for a step's copies; false (and the device error word is set) past the limit.
+// Waits for a phase; false past the limit (the device error word is set, and *abort), or once a wait
+// of another warp has set *abort.
 __device__ __noinline__ bool fp4_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
-                                      unsigned* err_word) {
+                                      unsigned* err_word, volatile int* abort) {
   const uint64_t deadline = global_timer_ns() + timeout_ns;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0 && global_timer_ns() > deadline) {
+    if ((i & 63u) != 0) continue;
+    if (abort != nullptr && *abort != 0) return false;
+    if (global_timer_ns() > deadline) {
       atomicOr(err_word, kErrTimeout);
+      if (abort != nullptr) *abort = 1;
       return false;
     }
   }
+}
+// The four warps that compute.
+__device__ __forceinline__ void team_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kDecThreads) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // An 8 x 8 matrix of 16-bit values, transposed: lane (r, q) gives row r's 2q, 2q + 1 and takes
 // column r's.
@@ -126,10 +137,19 @@ __device__ __forceinline__ uint32_t both(uint32_t h2, int high) {
   return __byte_perm(h2, h2, high ? 0x3232 : 0x1010);
 }
 
+// Runs of CTAs have a fifth warp that loads their tiles. With 16 heads the registers that it takes from
+// the others cost more than it saves (32 sequences of 1,000-4,096 tokens: 49.4 us against 45.5; with 4
+// and 8 heads 64 of 128-4,096: 44.1 against 45.9, 48.7 against 51.0).
+template <int H, DecMode MODE>
+constexpr bool kFp4Loader = MODE == kSplit && H <= 8;
+template <int H, DecMode MODE>
+constexpr int kFp4Threads = kDecThreads + (kFp4Loader<H, MODE> ? 32 : 0);
+
 template <int D, int H, DecMode MODE>
-__global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
+__global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
     fp4_decode_kernel(const PagedDecodeArgs a, int cluster) {
   using C = Fp4Cfg<D>;
+  constexpr bool PROD = kFp4Loader<H, MODE>;
   constexpr bool ONE = MODE == kOne, PAIRS = MODE == kPairs;
   constexpr bool WARPS = MODE == kWarps || PAIRS;  // no warp waits for another
   constexpr int NT = H <= 8 ? 1 : 2;     // tiles of 8 heads
@@ -138,11 +158,13 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
   constexpr float kShift = 14.f;
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ float s_m[kDecWarps][8 * NT], s_l[kDecWarps][8 * NT];
-  __shared__ int s_bad[kDecWarps];
+  __shared__ int s_bad[kDecWarps], s_bad_tile[C::kStages];
+  __shared__ volatile int s_abort;
   // pieces and run of each warp: read at their borders, not worth registers in between
   __shared__ Piece s_piece[kDecWarps], s_ld[kDecWarps];
   __shared__ int64_t s_run[kDecWarps][2];
-  __shared__ uint64_t s_full[kDecWarps][C::kStages];  // a step's copies have landed
+  // [warp][stage] a step's copies have landed; PROD: [0] a tile's have, [1] its warps have read it
+  __shared__ uint64_t s_full[kDecWarps][C::kStages];
   float(*s_o)[8][D] = reinterpret_cast<float(*)[8][D]>(dyn + C::kRing);  // [warp][head][d]
   float* s_part = reinterpret_cast<float*>(dyn);  // ONE, at the end: [head][d]
   __shared__ float2 s_pml[ONE ? 8 * NT : 1];
@@ -191,7 +213,7 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     // sequences without tokens (0 and -inf) and with lengths out of range (NaN)
     for (int b = blockIdx.x; b < a.num_seqs; b += gridDim.x) {
       const int n = checked_len(a, b);
-      if (n <= 0) write_empty(a, b, n, 0, a.hq, D);
+      if (n <= 0) write_empty(a, b, n, 0, a.hq, D, threadIdx.x, kFp4Threads<H, MODE>);
     }
     const RunStart run = find_run(a, kTile, cta, ctas);
     if (WARPS ? lane == 0 : threadIdx.x == 0) a.rec[cta] = DecodeRec{-1, 0, 0, 0};
@@ -207,25 +229,101 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
   }
   if constexpr (!PAIRS) set_piece<kTile>(a, run_end, first);
 
-  // ------------------------------------------------------ loads: a cursor of their own
-  // A step's keys of one page (all of them, or the page's 16 or 32) lie together in memory and in the
-  // ring: four copies, issued by one lane.
+  // ------------------------------------------------------ loads
+  // A tile's (PROD) or step's keys of one page lie together in memory and in the ring: four copies,
+  // issued by one lane.
   constexpr int kStages = C::kStages;
-  const uint32_t ring = smem_u32(dyn) + warp * (kStages * C::kStep);
-  const uint32_t full = smem_u32(&s_full[warp][0]);
-  if (lane == 0) {
+  constexpr int kShare = PROD ? kDecWarps : 1;  // warps whose steps a stage holds
+  const int slot = PROD ? 0 : warp;
+  const uint32_t ring = smem_u32(dyn) + slot * (kStages * C::kStep);
+  const uint32_t full = smem_u32(&s_full[slot][0]);
+  const uint32_t empty = smem_u32(&s_full[1][0]);  // PROD
+  if (PROD ? threadIdx.x == 0 : lane == 0) {
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s_full[slot][i], 1);
+      if constexpr (PROD) mbar_init(&s_full[1][i], kDecWarps);
+    }
     fence_mbar_init();
+  }
+  if (lane == 0 && warp < kDecWarps) {
     s_piece[warp] = s_ld[warp] = first;
     s_run[warp][0] = run_end;
     s_run[warp][1] = run_total;
   }
-  __syncwarp();
+  if (threadIdx.x == 0) s_abort = 0;
+  if constexpr (PROD || ONE) __syncthreads(); else __syncwarp();
   const int64_t head_bytes = static_cast<int64_t>(C::kCB + C::kSB) << a.page_shift;
   const int64_t page_bytes = head_bytes * a.hkv;
   const int64_t scales_at = static_cast<int64_t>(C::kCB) << a.page_shift;
   const int page_mask = (1 << a.page_shift) - 1;
+  // `keys` from key `pos` on, in page pg, to place `from` of the stage at `to`
+  auto load = [&](uint32_t to, uint32_t bar, int pg, int64_t head, int pos, int from, int keys) {
+    const int64_t base = pg * page_bytes + head;
+    const int at = pos & page_mask;
+    const int64_t c = base + at * C::kCB, sc = base + scales_at + at * C::kSB;
+    const uint32_t codes = to + from * C::kCB, scales = to + 2 * kShare * C::kCodes + from * C::kSB;
+    bulk_load(codes, a.k_pages + c, keys * C::kCB, bar);
+    bulk_load(codes + kShare * C::kCodes, a.v_pages + c, keys * C::kCB, bar);
+    bulk_load(scales, a.k_pages + sc, keys * C::kSB, bar);
+    bulk_load(scales + kShare * C::kScales, a.v_pages + sc, keys * C::kSB, bar);
+  };
+  if constexpr (PROD) {
+    if (warp == kDecWarps) {
+      const int part = min(page_mask + 1, C::kTile);  // keys of a tile in one page
+      Piece ld = first;
+      int key = ld.kb, st = 0;
+      uint32_t lap = 0;
+      auto page_of = [&]() {             // lane i: of the tile's i-th part
+        const int pos = key + lane * part;
+        return lane * part < C::kTile && pos < ld.ke
+                   ? __ldg(a.table + static_cast<int64_t>(ld.b) * a.max_pages + (pos >> a.page_shift)) : -1;
+      };
+      int page = page_of();
+      bool more = true;
+      while (more) {
+        const int keys = min(C::kTile, ld.ke - key), from_key = key, my_page = page;
+        const int64_t head = ld.g * head_bytes;
+        key += C::kTile;
+        if (key >= ld.ke) {
+          more = next_piece<kTile>(a, run_end, ld);
+          key = ld.kb;
+        }
+        if (more) page = page_of();      // the next tile's, on its way while the stage is waited for
+        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(empty + 8 * st, lap ^ 1)) &&
+            !__all_sync(0xFFFFFFFFu, fp4_wait(empty + 8 * st, lap ^ 1, a.timeout_ns, a.err_word, &s_abort)))
+          break;
+        const bool held = lane * part < keys;
+        const bool ok = held && static_cast<unsigned>(my_page) < static_cast<unsigned>(a.num_pages);
+        // whole 16s: a page holds no fewer
+        const int mine = ok ? min(part, (keys - lane * part + 15) / 16 * 16) : 0;
+        unsigned todo = __ballot_sync(0xFFFFFFFFu, ok);
+        const bool bad = todo != __ballot_sync(0xFFFFFFFFu, held);
+        const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine));
+        const uint32_t bar = full + 8 * st, to = ring + st * (kShare * C::kStep);
+        if (lane == 0) {
+          s_bad_tile[st] = bad;
+          mbar_expect_tx(bar, sum * (2 * (C::kCB + C::kSB)));
+        }
+        __syncwarp();
+        if (a.inject_skip_loads != 0) todo = 0;
+        for (; todo != 0; todo &= todo - 1) {
+          const int i = __ffs(todo) - 1;
+          const int pg = __shfl_sync(0xFFFFFFFFu, my_page, i), n = __shfl_sync(0xFFFFFFFFu, mine, i);
+          if (elect_one()) load(to, bar, pg, head, from_key + i * part, i * part, n);
+        }
+        if (++st == kStages) {
+          st = 0;
+          lap ^= 1;
+        }
+      }
+      // what is on its way lands before the CTA's memory is given up, or the limit passes
+      for (int i = 0; i < kStages; ++i)
+        fp4_wait(full + 8 * i, i < st ? lap : lap ^ 1, a.timeout_ns, a.err_word, nullptr);
+      return;
+    }
+  }
+  // the others: a cursor of their own
   const int own = WARPS ? 0 : warp * C::kKeys;  // the warp's first key in a tile
   int ld_key = first.kb + own;           // first key of the next step to load
   int ld_ke = first.ke;
@@ -258,24 +356,13 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
   auto issue = [&](int stage) {          // the stage's last step has been read by every lane
     if (!ld_more) return;
     const uint32_t bar = full + 8 * stage, to = ring + stage * C::kStep;
-    // `keys` from the step's `from` on, in one page
-    auto load = [&](int pg, int from, int keys) {
-      const int64_t base = pg * page_bytes + ld_head;
-      const int at = (ld_key + from) & page_mask;
-      const int64_t c = base + at * C::kCB, sc = base + scales_at + at * C::kSB;
-      const uint32_t codes = to + from * C::kCB, scales = to + 2 * C::kCodes + from * C::kSB;
-      bulk_load(codes, a.k_pages + c, keys * C::kCB, bar);
-      bulk_load(codes + C::kCodes, a.v_pages + c, keys * C::kCB, bar);
-      bulk_load(scales, a.k_pages + sc, keys * C::kSB, bar);
-      bulk_load(scales + C::kScales, a.v_pages + sc, keys * C::kSB, bar);
-    };
     const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages);
     bool bad;
     if (page_mask >= C::kKeys - 1) {     // a step is in one page (whose rows past the last key come too)
       bad = !ok;
       if (elect_one()) {
         mbar_expect_tx(bar, ok ? C::kStep : 0);
-        if (ok && a.inject_skip_loads == 0) load(page, 0, C::kKeys);
+        if (ok && a.inject_skip_loads == 0) load(to, bar, page, ld_head, ld_key, 0, C::kKeys);
       }
     } else {
       const int parts = (min(C::kKeys, ld_ke - ld_key) + page_mask) >> a.page_shift;
@@ -287,7 +374,8 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
       if (a.inject_skip_loads != 0) todo = 0;
       for (; todo != 0; todo &= todo - 1) {
         const int i = __ffs(todo) - 1, pg = __shfl_sync(0xFFFFFFFFu, page, i);
-        if (elect_one()) load(pg, i << a.page_shift, page_mask + 1);
+        const int from = i << a.page_shift;
+        if (elect_one()) load(to, bar, pg, ld_head, ld_key + from, from, page_mask + 1);
       }
     }
     bad_steps = bad ? bad_steps | (1u << stage) : bad_steps & ~(1u << stage);
@@ -318,10 +406,12 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
   const int kr = r ^ ((r >> 1) & 1);
   const int v_row[2] = {2 * q4 + (q4 & 1), 2 * q4 + (~q4 & 1)};
 
-  seek();
+  if constexpr (!PROD) seek();
   load_q(first.b, first.g);
+  if constexpr (!PROD) {
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue(s);
+    for (int s = 0; s < kStages - 1; ++s) issue(s);
+  }
   int stage = 0;
   uint32_t parity = 0;
 
@@ -374,18 +464,29 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     }
     bool bad = false;
 
-    for (int key0 = key_begin + own; key0 < key_end; key0 += kTile) {
-      __syncwarp();  // the stage before was read by every lane
-      issue(stage == 0 ? kStages - 1 : stage - 1);
-      if (!late && !__all_sync(0xFFFFFFFFu, mbar_try_wait(full + 8 * stage, parity)))
-        late = !__all_sync(0xFFFFFFFFu, fp4_wait(full + 8 * stage, parity, a.timeout_ns, a.err_word)),
+    // (PROD: every warp goes through all tiles, also one that has no keys in the last)
+    for (int key0 = key_begin + own; key0 - (PROD ? own : 0) < key_end; key0 += kTile) {
+      if constexpr (!PROD) {
+        __syncwarp();  // the stage before was read by every lane
+        issue(stage == 0 ? kStages - 1 : stage - 1);
+      }
+      if (!late && !__all_sync(0xFFFFFFFFu, mbar_try_wait(full + 8 * stage, parity))) {
+        late = !__all_sync(0xFFFFFFFFu,
+                           fp4_wait(full + 8 * stage, parity, a.timeout_ns, a.err_word, &s_abort));
         ld_more &= !late;
-      bad |= late || ((bad_steps >> stage) & 1u);
-      const uint32_t kbuf = ring + stage * C::kStep, vbuf = kbuf + C::kCodes;
-      const uint32_t ksc = kbuf + 2 * C::kCodes, vsc = ksc + C::kScales;
+      }
+      bad |= late || (PROD ? s_bad_tile[stage] != 0 : (bad_steps >> stage) & 1u);
+      const uint32_t step = ring + stage * (kShare * C::kStep), share = PROD ? warp : 0;
+      const uint32_t kbuf = step + share * C::kCodes, vbuf = kbuf + kShare * C::kCodes;
+      const uint32_t ksc = step + 2 * kShare * C::kCodes + share * C::kScales, vsc = ksc + kShare * C::kScales;
+      const uint32_t read = empty + 8 * stage;
       if (++stage == kStages) {
         stage = 0;
         parity ^= 1;
+      }
+      if (PROD && key0 >= key_end) {
+        if (lane == 0 && !late) mbar_arrive_at(read);
+        continue;
       }
       const bool tail = key0 + C::kKeys > key_end;
       if (tail) {  // what a page holds behind the last key may be no number: scales of zero
@@ -578,6 +679,10 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
                 mma_f16(o[n][4 * k + b], a0[b], a1[b], a2[b], a3[b], ps[n][t][0], ps[n][t][1]);
         }
       }
+      if constexpr (PROD) {
+        __syncwarp();
+        if (lane == 0 && !late) mbar_arrive_at(read);
+      }
     }
 
     bad = __any_sync(0xFFFFFFFFu, bad);
@@ -705,7 +810,7 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
         for (int j = 0; j < 2; ++j)  // 16-byte units, spread over the banks by the heads' pairs
           *reinterpret_cast<float4*>(&s_o[warp][2 * q4 + j][4 * ((out_d(t) / 4) ^ q4)]) =
               make_float4(o[n][t][j], o[n][t][2 + j], o[n][t + 1][j], o[n][t + 1][2 + j]);
-      __syncthreads();
+      team_sync();
       const bool any_bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
       const int heads = min(FOLD ? 4 : 8, G - 8 * n);
       const int d = 4 * (threadIdx.x % (D / 4));
@@ -749,7 +854,7 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
         }
       }
       if (n == 0 && threadIdx.x == 0) note(any_bad);
-      __syncthreads();  // the shared parts may be overwritten
+      team_sync();  // the shared parts may be overwritten
     }
     if constexpr (ONE) break;
     if (!more) break;
@@ -757,16 +862,16 @@ __global__ void __launch_bounds__(kDecThreads, H <= 8 ? kFp4PerSm : 2)
     if (lane == 0) s_piece[warp] = nxt;
     __syncwarp();
   }
-  if (late)  // what is still on its way lands before the memory is given up, or the limit passes
-    for (int i = 0; i < kStages; ++i) fp4_wait(full + 8 * i, i < stage ? parity : parity ^ 1, a.timeout_ns, a.err_word);
-
+  if (!PROD && late)  // what is still on its way lands before the memory is given up, or the limit passes
+    for (int i = 0; i < kStages; ++i)
+      fp4_wait(full + 8 * i, i < stage ? parity : parity ^ 1, a.timeout_ns, a.err_word, nullptr);
   if constexpr (ONE) join_cluster<D>(a, s_piece[warp], cluster, cta, s_part, s_pml, s_lse2, kShift, true);
 }
 
 template <int D, int H>
 struct Fp4Kernel : Fp4Cfg<D> {
   static constexpr int kDim = D, kPerSm = H <= 8 ? kFp4PerSm : 2, kOneTiles = 8;
-  static constexpr int kPairSteps = 8;
+  static constexpr int kPairSteps = 8, kSplitThreads = kFp4Threads<H, kSplit>;
   static constexpr float kShift = 14.f;
   static auto fn(DecMode mode) {
     return mode == kOne ? fp4_decode_kernel<D, H, kOne>

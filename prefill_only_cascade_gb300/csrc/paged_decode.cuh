@@ -572,7 +572,7 @@ cudaError_t launch_decode(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) 
   const auto fn = K::fn(warps ? kWarps : kSplit);
   e = allow_smem(reinterpret_cast<const void*>(fn), smem, ready[warps]);
   if (e != cudaSuccess) return e;
-  fn<<<ctas, kDecThreads, smem, stream>>>(a, 1);
+  fn<<<ctas, warps ? kDecThreads : K::kSplitThreads, smem, stream>>>(a, 1);
   e = cudaGetLastError();
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
