@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ float s_m[kDecWarps][8 * NT], s_l[kDecWarps][8 * NT];
   __shared__ int s_bad[kDecWarps], s_bad_tile[C::kStages];
-  __shared__ volatile int s_abort;
+  __shared__ volatile int s_abort;       // PROD: a wait ran out
   // pieces and run of each warp: read at their borders, not worth registers in between
   __shared__ Piece s_piece[kDecWarps], s_ld[kDecWarps];
   __shared__ int64_t s_run[kDecWarps][2];
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
     s_run[warp][0] = run_end;
     s_run[warp][1] = run_total;
   }
-  if (threadIdx.x == 0) s_abort = 0;
-  if constexpr (PROD || ONE) __syncthreads(); else __syncwarp();
+  if (PROD && threadIdx.x == 0) s_abort = 0;
+  if constexpr (PROD) __syncthreads(); else __syncwarp();
   const int64_t head_bytes = static_cast<int64_t>(C::kCB + C::kSB) << a.page_shift;
   const int64_t page_bytes = head_bytes * a.hkv;
   const int64_t scales_at = static_cast<int64_t>(C::kCB) << a.page_shift;
@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
       }
       if (!late && !__all_sync(0xFFFFFFFFu, mbar_try_wait(full + 8 * stage, parity))) {
         late = !__all_sync(0xFFFFFFFFu,
-                           fp4_wait(full + 8 * stage, parity, a.timeout_ns, a.err_word, &s_abort));
+                           fp4_wait(full + 8 * stage, parity, a.timeout_ns, a.err_word,
+                                    PROD ? &s_abort : nullptr));
         ld_more &= !late;
       }
       bad |= late || (PROD ? s_bad_tile[stage] != 0 : (bad_steps >> stage) & 1u);
