@@ -593,7 +593,8 @@ void quail_set_wait_timeout_ns(uint64_t ns);
  * next cascade launches never issue the load of their first KV tile, and the next
  * quail_attn_scores launches never that of a sequence's first keys (where a cluster of CTAs
  * shares its queries, in the last of them), so the consumer's bounded wait runs out and the
- * launch reports QUAIL_ERR_TIMEOUT. Nothing faults.
+ * launch reports QUAIL_ERR_TIMEOUT; quail_paged_decode_attn over fp4 pages loads nothing, reports
+ * the same and writes NaN. Nothing faults.
  */
 void quail_debug_inject(int32_t skip_first_kv_load);
 

@@ -132,7 +132,7 @@ DecodeLayout decode_layout(const quail_paged_desc& d, bool with_scores) {
   const size_t parts = 2 * static_cast<size_t>(quail::decode_ctas(
                                quail::kDecodeMaxSms, quail::decode_ctas_per_sm(d.kv_dtype, group), d.num_seqs, d.num_kv_heads, d.max_seq_len,
                                tile)) *
-                       (quail::decode_by_warps(d.num_seqs, d.num_kv_heads, d.max_seq_len, tile) ? 4 : 1);
+                       (quail::decode_by_warps(d.kv_dtype, group, d.num_seqs, d.num_kv_heads, d.max_seq_len, tile) ? 4 : 1);
   DecodeLayout l;
   l.raw_stride = (static_cast<int64_t>(d.max_seq_len) + tile - 1) / tile * tile;
   l.rec = 0;

@@ -4,22 +4,31 @@
 //
 //   out = S_v sum_j w_j v_j,  w_j = exp2(c S_k q.k_j - lse2),  k_j, v_j = code * block scale
 //
-// How the batch is divided and joined is as over the other forms of pages (see paged.cu); a warp
-// walks its keys with a running max and sum. What bounds it: 144 bytes of HBM per (token, KV head)
-// at d = 128, 24 issue slots of an SM's quarter at the measured copy rate, into which 256 codes
-// have to go through conversion, scaling and two products. So every step's instructions count:
+// How the batch is divided and joined is as over the other forms of pages (see paged.cu), but that short
+// sequences take a warp per head (kPairs). A warp walks its keys with a running max and sum. HBM gives
+// 144 bytes per (token, KV head) at d = 128, 24 issue slots of an SM's quarter at the measured copy rate,
+// into which 256 codes have to go through conversion (two cycles of the ALU for 32 pairs), scaling and
+// two products (eight cycles of the tensor pipe each); so every step's instructions count:
 //   S^T [16 keys x 8 heads]  A = K: keys fill the 16 rows (heads would fill 1 to 8 of them), half the
-//            products. Lane (r, q) holds pieces q of keys r and r + 8 as they lie in memory: sums
-//            over d may run in any order, so its codes ARE its fragments, and they belong to one
-//            (d = 64) or two block scales.
-//   O^T [16 d x 8 heads]     A = V^T: lane (r, q) holds one block (d = 64: half of one) of keys 2q, 2q + 1,
-//            2q + 8, 2q + 9. Their nibbles are interleaved before the conversion (4 operations for 8
-//            pairs; permuting the converted halves would take 8); B = P^T, the score fragment
-//            transposed in 8 x 8 blocks. The heads of a lane's scores are those of its outputs, so
-//            the running max needs no exchange while no score passes it.
+//            products. Lane (r, q) holds pieces q of two keys as they lie in memory: sums over d may run
+//            in any order, so its codes ARE its fragments, and they belong to one (d = 64) or two block
+//            scales.
+//   O^T [16 d x 8 heads]     A = V^T: lane (r, q) holds one block (d = 64: half of one) of four keys.
+//            Their nibbles are interleaved before the conversion (4 operations for 8 pairs; permuting the
+//            converted halves would take 8); B = P^T, the score fragment transposed in 8 x 8 blocks. The
+//            heads of a lane's scores are those of its outputs, so the running max needs no exchange
+//            while no score passes it.
+// With up to four heads the other four columns are the same heads again: their P^T holds the second term
+// of P's sum, and one product does both (64 sequences of 8,000-16,000 tokens: 189 -> 175 us).
+// Loads are bulk copies of whole pieces of pages into a ring of two steps, issued by a warp of its own or
+// by the warp that computes.
 // Products of code and block scale are exact in f16. Q is scaled per head by a power of two into
 // f16's range (bits below 2^-38 of the head's largest |q| are lost, under fp32's own rounding); P,
 // scaled by 2^14, is the sum of two f16 (22 bits, weights down to 2^-38 of the largest).
+// Measured (8 KV heads, G = 4, d = 128, in a graph, of the measured copy rate): one sequence of 131,007
+// tokens 38.6 us (58 %), 64 of 8,000-16,000 172 us (75 %), 64 of 128-4,096 44 us (51 %). About 650
+// instructions per warp and 32 keys, 0.6 a cycle and quarter with three CTAs on an SM; two took 206 us
+// instead of 189 for the second case, four (128 registers) 196, a ring of three steps the same as two.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -869,14 +878,25 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
   if constexpr (ONE) join_cluster<D>(a, s_piece[warp], cluster, cta, s_part, s_pml, s_lse2, kShift, true);
 }
 
+// Which way (see launch_decode), both sides measured in a graph (8 KV heads, d = 128, G = 4 unless said):
+//   one launch of clusters, up to four tiles a CTA: one sequence of 777 tokens 6.2 us, four of 2,000
+//       8.2 and 10.9, four of 4,000 10.6 and 13.4; past the rule (eight tiles) two of 8,000 15.1 and 14.1,
+//       one of 8,000 13.0 and 11.8
+//   a warp per (sequence, head), up to eight steps: 181 sequences of 20-83 tokens (4 KV heads, G = 16)
+//       10.3 and 20.8, 256 of 16-128 17.0 and 26.9, 256 of 200-256 26.4 and 34.9; past the rule (16 steps)
+//       64 of 256-512 19.2 and 17.8, 256 of 300-512 43.7 and 45.0
+//   runs of warps with 16 heads only: 100 of 300-600 36.9 and 43.3 (runs of CTAs); with fewer heads 128 of
+//       300-600 33.2 and 31.3, 100 of 300-900 with weights 37.8 and 33.5, 256 of 300-512 45.3 and 46.9
 template <int D, int H>
 struct Fp4Kernel : Fp4Cfg<D> {
-  static constexpr int kDim = D, kPerSm = H <= 8 ? kFp4PerSm : 2, kOneTiles = 8;
+  static constexpr int kDim = D, kForm = kFp4, kPerSm = H <= 8 ? kFp4PerSm : 2, kOneTiles = 4;
   static constexpr int kPairSteps = 8, kSplitThreads = kFp4Threads<H, kSplit>;
   static constexpr float kShift = 14.f;
   static auto fn(DecMode mode) {
+    if constexpr (H > 8) {
+      if (mode == kWarps) return fp4_decode_kernel<D, H, kWarps>;
+    }
     return mode == kOne ? fp4_decode_kernel<D, H, kOne>
-           : mode == kWarps ? fp4_decode_kernel<D, H, kWarps>
            : mode == kPairs ? fp4_decode_kernel<D, H, kPairs>
                             : fp4_decode_kernel<D, H, kSplit>;
   }
@@ -890,6 +910,7 @@ cudaError_t launch_fp4_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t st
 
 }  // namespace
 
+bool fp4_warp_runs(int group) { return group > 8; }
 int fp4_decode_per_sm(int group) { return group > 8 ? 2 : kFp4PerSm; }
 
 cudaError_t launch_fp4_decode(PagedDecodeArgs& a, int head_dim, int num_sms, cudaStream_t stream) {

@@ -260,12 +260,13 @@ int decode_tile_keys(int head_dim, int kv_dtype);
 int decode_ctas_per_sm(int kv_dtype, int group);
 int decode_ctas(int num_sms, int per_sm, int num_seqs, int hkv, int max_len, int tile);
 // Whether runs are dealt to warps, four per CTA (the workspace then holds four times the parts).
-bool decode_by_warps(int num_seqs, int hkv, int max_len, int tile);
+bool decode_by_warps(int kv_dtype, int group, int num_seqs, int hkv, int max_len, int tile);
 cudaError_t launch_paged_decode(PagedDecodeArgs& a, int head_dim, int kv_dtype, int num_sms,
                                 cudaStream_t stream);
 // Keys of a CTA's tile over fp4 pages: 8 KB of codes.
 constexpr int fp4_tile_keys(int head_dim) { return 16384 / head_dim; }
 int fp4_decode_per_sm(int group);
+bool fp4_warp_runs(int group);
 cudaError_t launch_fp4_decode(PagedDecodeArgs& a, int head_dim, int num_sms, cudaStream_t stream);
 
 struct AttnScoresArgs {

@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 // 2,000 39.5 and 30.4.
 template <int D, bool FP8, int NT>
 struct DecKernel : DecCfg<D, FP8> {
-  static constexpr int kDim = D, kPerSm = 2, kOneTiles = 8;
+  static constexpr int kDim = D, kForm = FP8 ? kE4m3 : kBf16, kPerSm = 2, kOneTiles = 8;
   static constexpr int kPairSteps = -1;  // no such launch
   static constexpr int kSplitThreads = kDecThreads;
   static constexpr float kShift = FP8 ? 14.f : 0.f;
@@ -710,7 +710,8 @@ int decode_ctas_per_sm(int kv_dtype, int group) {
 // (8 KV heads, G = 16, e4m3) 27.0 us and 40.8, 256 of 16-128 (8, G = 4) 29.2 and 38.7, 100 of
 // 100-500 (8, G = 8) 33.6 and 39.8, 128 of 300-600 (8, G = 4, e4m3) 35.0 and 37.8; past the rule,
 // 93 of 431-589 43.9 and 41.9, 128 of 500-1,000 73.6 and 70.7 (parts of more runs to join).
-bool decode_by_warps(int num_seqs, int hkv, int max_len, int tile) {
+bool decode_by_warps(int kv_dtype, int group, int num_seqs, int hkv, int max_len, int tile) {
+  if (kv_dtype == kFp4 && !fp4_warp_runs(group)) return false;
   return static_cast<int64_t>(num_seqs) * hkv >= 4 * kDecodeMaxSms && max_len <= 8 * tile;
 }
 

@@ -524,9 +524,10 @@ __global__ void __launch_bounds__(kFinishThreads, 4)
   }
 }
 
-// A kernel and how it is launched: K has the sizes that DecCfg has, the CTAs per SM (kPerSm), the
-// power of two by which its sums are scaled (kShift), tiles per CTA in one launch (kOneTiles) and
-// fn(mode), its instances.
+// A kernel and how it is launched: K has the sizes that DecCfg has, the pages' form (kForm), the CTAs
+// per SM (kPerSm), the power of two by which its sums are scaled (kShift), tiles per CTA in one launch
+// of clusters (kOneTiles), the steps up to which a warp takes a (sequence, head) alone (kPairSteps; < 0:
+// it has no such instance), the threads of a CTA with a run (kSplitThreads) and fn(mode), its instances.
 template <class K>
 cudaError_t launch_decode(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
   cudaError_t e;
@@ -563,7 +564,7 @@ cudaError_t launch_decode(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) 
     return cudaGetLastError();
   }
   // runs of warps or of CTAs
-  const bool warps = decode_by_warps(a.num_seqs, a.hkv, a.max_len, K::kTile);
+  const bool warps = decode_by_warps(K::kForm, a.group, a.num_seqs, a.hkv, a.max_len, K::kTile);
   const int tile = warps ? K::kKeys : K::kTile;
   const int ctas = decode_ctas(num_sms, K::kPerSm, a.num_seqs, a.hkv, a.max_len, K::kTile);
   const int runs = warps ? ctas * kDecWarps : ctas;
