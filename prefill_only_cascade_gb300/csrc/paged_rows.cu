@@ -28,8 +28,8 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kRowMaxTok = 64;
-constexpr int kAppendPerSm = 6, kAppendTok = 32;  // blocks on an SM, most tokens of one
+constexpr int kRowMaxTok = 16;  // most tokens of a block
+constexpr int kAppendPerSm = 6;
 
 // Slot of each of the block's token rows in the pool (page * page_size + place), kNoSlot where
 // its position or page is out of range, kNoSeq where no sequence holds it; and its sequence.
@@ -322,15 +322,15 @@ __global__ void __launch_bounds__(kRowThreads) paged_read_kernel(const PagedRows
 }
 
 // Token rows per block: 64 where there are enough, fewer so that two blocks per SM have some.
-int tokens_per_block(int64_t total, int num_sms, int most) {
+int tokens_per_block(int64_t total, int num_sms) {
   const int64_t spread = (total + 2 * num_sms - 1) / (2 * num_sms);
-  return static_cast<int>(spread < 1 ? 1 : spread < most ? spread : most);
+  return static_cast<int>(spread < 1 ? 1 : spread < kRowMaxTok ? spread : kRowMaxTok);
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_append(const PagedRows& p, int head_dim, int num_sms, cudaStream_t stream) {
-  const int tok = tokens_per_block(p.total, num_sms, kAppendTok);
+  const int tok = tokens_per_block(p.total, num_sms);
   const unsigned blocks = static_cast<unsigned>((p.total + tok - 1) / tok);
   if (head_dim == 128)
     fp4_append_kernel<128><<<blocks, kRowThreads, 0, stream>>>(p, tok);
@@ -341,7 +341,7 @@ cudaError_t launch_fp4_append(const PagedRows& p, int head_dim, int num_sms, cud
 
 cudaError_t launch_paged_read(const PagedRows& p, int head_dim, int kv_dtype, int num_sms,
                               cudaStream_t stream) {
-  const int tok = tokens_per_block(p.total, num_sms, kRowMaxTok);
+  const int tok = tokens_per_block(p.total, num_sms);
   const unsigned blocks = static_cast<unsigned>((p.total + tok - 1) / tok);
   auto run = [&](auto kernel) { kernel<<<blocks, kRowThreads, 0, stream>>>(p, tok); };
   if (head_dim == 128)
