@@ -427,8 +427,11 @@ def paged_page_bytes(desc: PagedDesc) -> int:
     return int(lib.quail_paged_page_bytes(ctypes.byref(desc)))
 
 
-# The paged calls run once per generated token, so their checks are written to be cheap: one
-# test per tensor, the reason worked out only when it fails, the stream's handle without a
+# The paged calls run once per generated token. Plain arguments on the current device and stream go
+# through one native pass (csrc/paged_calls.cpp, built beside the library where PyTorch's and Python's
+# headers are: 4-5 us a call on the host instead of 9-10); it answers None to anything else, and without
+# it, or with a stream given, the checks below do the same. They too are written to be cheap: one test
+# per tensor, the reason worked out only when it fails, the stream's handle without a
 # Stream object, the device switched only when it is not the current one.
 # (PyTorch's own short cuts where it has them: 0.08 us instead of 1.1 for the stream, 0.12
 # instead of 0.25 for the device.)
@@ -436,6 +439,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+try:
+    from . import _paged_calls as _calls
+    _calls.bind(PagedDesc, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.quail_paged_kv_append, lib.quail_paged_kv_read, lib.quail_paged_decode_attn,
+        lib.quail_paged_kv_evict)))
+except ImportError:
+    _calls = None
 _POOL_DTYPES = {QUAIL_BF16: (_BF16,), QUAIL_FP8_E4M3: (torch.float8_e4m3fn, torch.uint8),
                 QUAIL_FP4_E2M1: (torch.uint8,)}
 
@@ -567,6 +577,11 @@ def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pag
     pages at start_pos[b] + i; new_offsets ([B+1] int32) delimits the sequences' rows (None:
     one token each). With e4m3 and fp4 pages the rows become codes under the given scales (fp4:
     amax / 2688 uses the format whole)."""
+    if _calls is not None and stream is None:
+        code = _calls.append(desc, k_new, v_new, start_pos, block_table, k_pages, v_pages, new_offsets,
+                             k_scale, v_scale)
+        if code is not None:
+            return _check(code, "quail_paged_kv_append")
     B, pages = desc.num_seqs, desc.num_pages
     try:
         dev, shape = k_new.get_device(), (k_new.shape[0], desc.num_kv_heads, desc.head_dim)
@@ -590,6 +605,11 @@ def paged_kv_read(desc: PagedDesc, k_pages, v_pages, start_pos, block_table, k_o
     """quail_paged_kv_read: positions start_pos[b] + i of the sequences as bf16 rows into k_out /
     v_out ([T, Hkv, d] bf16, any row stride; None: not read); offsets ([B+1] int32) delimits the
     sequences' rows (None: one each)."""
+    if _calls is not None and stream is None:
+        code = _calls.read(desc, k_pages, v_pages, start_pos, block_table, k_out, v_out, offsets, k_scale,
+                           v_scale)
+        if code is not None:
+            return _check(code, "quail_paged_kv_read")
     B, pages = desc.num_seqs, desc.num_pages
     some = k_out if k_out is not None else v_out
     if some is None:
@@ -630,6 +650,11 @@ def paged_decode_attn(desc: PagedDesc, q, k_pages, v_pages, block_table, seq_len
     """quail_paged_decode_attn: attention of one new token per sequence (q [B, Hq, d] bf16, any
     row stride) over its cached tokens; with score_out ([B, Hkv, n] fp32) also score_in plus
     the weight that each cached token receives (score_in may be score_out)."""
+    if _calls is not None and stream is None:
+        code = _calls.decode(desc, q, k_pages, v_pages, block_table, seq_lens, out, workspace, lse, k_scale,
+                             v_scale, score_in, score_out)
+        if code is not None:
+            return _check(code, "quail_paged_decode_attn")
     if workspace is None:
         raise ValueError("workspace is required (size: paged_decode_workspace_size(...))")
     B, hq, pages = desc.num_seqs, desc.num_q_heads, desc.num_pages
@@ -702,6 +727,11 @@ def paged_kv_evict(desc: PagedDesc, budget, recent, k_pages, v_pages, block_tabl
     scored others, `budget` in all, copied in order into the pages that dst_table names (of
     the same pool or another); kept [B, Hkv, budget] and new_lens [B] int32 say which and how
     many, score_out [B, Hkv, n] takes their scores."""
+    if _calls is not None and stream is None:
+        code = _calls.evict(desc, budget, recent, k_pages, v_pages, block_table, seq_lens, score, dst_table,
+                            k_dst, v_dst, kept, new_lens, workspace, score_out)
+        if code is not None:
+            return _check(code, "quail_paged_kv_evict")
     if workspace is None:
         raise ValueError("workspace is required (size: paged_evict_workspace_size(...))")
     budget, recent = int(budget), int(recent)
