@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, q4 = lane & 3;
   const int G = a.group;
+  after_stream();
   // who takes a run (a CTA, a warp), or ONE: the rank
   const int cta = ONE ? static_cast<int>(blockIdx.x) % cluster
                       : WARPS ? static_cast<int>(blockIdx.x) * kDecWarps + warp : blockIdx.x;
@@ -218,7 +219,6 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
     first.whole = true;
     if (!next_pair(first, true)) return;
   } else {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // sequences without tokens (0 and -inf) and with lengths out of range (NaN)
     for (int b = blockIdx.x; b < a.num_seqs; b += gridDim.x) {
       const int n = checked_len(a, b);
@@ -891,6 +891,7 @@ template <int D, int H>
 struct Fp4Kernel : Fp4Cfg<D> {
   static constexpr int kDim = D, kForm = kFp4, kPerSm = H <= 8 ? kFp4PerSm : 2, kOneTiles = 4;
   static constexpr int kPairSteps = 8, kSplitThreads = kFp4Threads<H, kSplit>;
+  static constexpr bool kEarly = true;
   static constexpr float kShift = 14.f;
   static auto fn(DecMode mode) {
     if constexpr (H > 8) {

@@ -196,6 +196,27 @@ enum KvForm {
   kE4m3,  // codes, a scale per sequence and KV head
   kFp4    // e2m1 codes, an e4m3 scale per 16 values and a scale per sequence and KV head
 };
+// A launch that may begin before the kernel ahead of it in the stream has ended: the kernel itself waits
+// for that (after_stream) before it touches memory.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                         int cluster, A... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 // Token rows written into fp4 pages, or read back from pages of any form.
 struct PagedRows {
   int num_seqs, hkv;

@@ -682,6 +682,7 @@ struct DecKernel : DecCfg<D, FP8> {
   static constexpr int kDim = D, kForm = FP8 ? kE4m3 : kBf16, kPerSm = 2, kOneTiles = 8;
   static constexpr int kPairSteps = -1;  // no such launch
   static constexpr int kSplitThreads = kDecThreads;
+  static constexpr bool kEarly = false;
   static constexpr float kShift = FP8 ? 14.f : 0.f;
   static auto fn(DecMode mode) {
     return mode == kOne ? paged_decode_kernel<D, FP8, NT, kOne>

@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kRowThreads, kAppendPerSm) fp4_append_kernel(c
   __shared__ int64_t s_slot[kRowMaxTok];
   __shared__ int s_seq[kRowMaxTok];
   constexpr int kBlocks = D / 16, kGroup = 32 / kBlocks;
+  after_stream();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
   const int n = static_cast<int>(min(static_cast<int64_t>(tok), p.total - t0));
   const int lane = threadIdx.x & 31, blk = lane % kBlocks;
@@ -284,6 +285,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_read_kernel(const PagedRows
   constexpr int kBlocks = D / 16, kGroup = 32 / kBlocks;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
   const int n = static_cast<int>(min(static_cast<int64_t>(tok), p.total - t0));
+  after_stream();
   find_slots(p, t0, n, s_slot, s_seq);
   const int lane = threadIdx.x & 31, blk = lane % kBlocks;
   const int pairs = (n + kGroup - 1) / kGroup * p.hkv;
@@ -333,25 +335,20 @@ int tokens_per_block(int64_t total, int num_sms) {
 cudaError_t launch_fp4_append(const PagedRows& p, int head_dim, int num_sms, cudaStream_t stream) {
   const int tok = tokens_per_block(p.total, num_sms);
   const unsigned blocks = static_cast<unsigned>((p.total + tok - 1) / tok);
-  if (head_dim == 128)
-    fp4_append_kernel<128><<<blocks, kRowThreads, 0, stream>>>(p, tok);
-  else
-    fp4_append_kernel<64><<<blocks, kRowThreads, 0, stream>>>(p, tok);
-  return cudaGetLastError();
+  return launch_early(head_dim == 128 ? fp4_append_kernel<128> : fp4_append_kernel<64>, dim3(blocks),
+                      dim3(kRowThreads), 0, stream, 0, p, tok);
 }
 
 cudaError_t launch_paged_read(const PagedRows& p, int head_dim, int kv_dtype, int num_sms,
                               cudaStream_t stream) {
   const int tok = tokens_per_block(p.total, num_sms);
   const unsigned blocks = static_cast<unsigned>((p.total + tok - 1) / tok);
-  auto run = [&](auto kernel) { kernel<<<blocks, kRowThreads, 0, stream>>>(p, tok); };
-  if (head_dim == 128)
-    run(kv_dtype == kFp4 ? paged_read_kernel<128, kFp4>
-        : kv_dtype == kE4m3 ? paged_read_kernel<128, kE4m3> : paged_read_kernel<128, kBf16>);
-  else
-    run(kv_dtype == kFp4 ? paged_read_kernel<64, kFp4>
-        : kv_dtype == kE4m3 ? paged_read_kernel<64, kE4m3> : paged_read_kernel<64, kBf16>);
-  return cudaGetLastError();
+  const auto fn = head_dim == 128
+                      ? (kv_dtype == kFp4 ? paged_read_kernel<128, kFp4>
+                         : kv_dtype == kE4m3 ? paged_read_kernel<128, kE4m3> : paged_read_kernel<128, kBf16>)
+                      : (kv_dtype == kFp4 ? paged_read_kernel<64, kFp4>
+                         : kv_dtype == kE4m3 ? paged_read_kernel<64, kE4m3> : paged_read_kernel<64, kBf16>);
+  return launch_early(fn, dim3(blocks), dim3(kRowThreads), 0, stream, 0, p, tok);
 }
 
 }  // namespace quail

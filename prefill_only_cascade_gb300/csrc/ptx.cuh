@@ -155,6 +155,15 @@ __device__ __forceinline__ float absmax_bf16x2_value(uint32_t acc) {
   return __uint_as_float(m << 16);
 }
 
+// ------------------------------------------------------------------ order within a stream
+// For kernels launched early: what is ahead in the stream has ended and its writes are seen; the kernel
+// behind may be set up (it waits in the same way). Every block comes through here before it touches
+// memory, so the end of this kernel is also the end of all before it.
+__device__ __forceinline__ void after_stream() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ thread-block clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
