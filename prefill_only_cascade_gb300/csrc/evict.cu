@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   __shared__ uint32_t s_gt[kSelWarps], s_eq[kSelWarps];
   int* s_kept = reinterpret_cast<int*>(s_first);  // FUSED, after the passes: this CTA's kept ones
   __shared__ int s_to[FUSED ? kSmallPages : 1], s_bad[FUSED ? kSmallPages + 1 : 1];
-  if (!FUSED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_stream();
   if (!FUSED && static_cast<int>(blockIdx.x) < note_blocks) {
     write_notes(a, blockIdx.x * kSelWarps + (threadIdx.x >> 5), note_blocks * kSelWarps, note_chunks);
     return;
@@ -620,10 +620,12 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   const int64_t others = a.num_seqs * (own + (a.same_pool ? (a.max_len + page - 1) / page : 0));
   cudaError_t e = cudaSuccess;
   int cluster = 1;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -642,8 +644,8 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   // (every CTA compares its `own` pages with all the `others`)
   if (a.max_len <= kSmallKeys * cluster && (brief || most <= kSmallShare * cluster) &&
       (cluster == 1 || pairs * cluster <= 2 * num_sms) && others <= 1024 && own * others <= 65536) {
-    attr[0].val.clusterDim.x = cluster;
-    cfg.numAttrs = cluster > 1;
+    attr[1].val.clusterDim.x = cluster;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     cfg.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
     return cudaLaunchKernelEx(&cfg, evict_select_kernel<4, false, true>, a, cluster, 0, 0);
   }
@@ -655,8 +657,8 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
           (pairs * cluster * 2 <= num_sms && a.max_len > 2048 * cluster)))
     cluster *= 2;
   const int per = (a.max_len + cluster - 1) / cluster;
-  attr[0].val.clusterDim.x = cluster;
-  cfg.numAttrs = 1;
+  attr[1].val.clusterDim.x = cluster;
+  cfg.numAttrs = 2;
   // The notes have blocks of their own in front, up to 32 (the claims' fences and exchanges
   // would keep one head's selection, and so its cluster, 2 us longer).
   const int64_t places = a.same_pool ? (a.max_len + page - 1) / page : own;
@@ -684,8 +686,7 @@ cudaError_t launch_paged_evict(const PagedEvictArgs& a, int num_sms, cudaStream_
   if (e != cudaSuccess) return e;
   const int chunks = static_cast<int>(
       (static_cast<int64_t>(a.budget) * a.hkv + kCopyThreads - 1) / kCopyThreads);
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * chunks));
   cfg.blockDim = dim3(kCopyThreads);
   return cudaLaunchKernelEx(&cfg, evict_copy_kernel, a, chunks);
