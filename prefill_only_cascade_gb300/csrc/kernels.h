@@ -272,7 +272,9 @@ struct PagedDecodeArgs {
   float* raw;                       // [B, Hq, raw_stride] scores in log2 units, or NULL
   int64_t raw_stride;
   unsigned* err_word;
-  // fp4 pages: how long a wait for a step's copies may block; no copies, so that it does
+  // fp4 pages: a KV head counts as 2^split of them with a part of its group each; how long a wait for a
+  // step's copies may block; no copies, so that it does
+  int split;
   uint64_t timeout_ns;
   int inject_skip_loads;
 };

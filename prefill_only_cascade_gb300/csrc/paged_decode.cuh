@@ -529,18 +529,42 @@ __global__ void __launch_bounds__(kFinishThreads, 4)
 // A kernel and how it is launched: K has the sizes that DecCfg has, the pages' form (kForm), the CTAs
 // per SM (kPerSm), the power of two by which its sums are scaled (kShift), tiles per CTA in one launch
 // of clusters (kOneTiles), the steps up to which a warp takes a (sequence, head) alone (kPairSteps; < 0:
-// it has no such instance), the threads of a CTA with a run (kSplitThreads), whether it waits for the stream itself (kEarly)
-// and fn(mode), its instances.
+// it has no such instance), the threads of a CTA with a run (kSplitThreads), whether it waits for the
+// stream itself (kEarly) and fn(mode), its instances.
+
+// One launch where clusters of up to eight CTAs, a few tiles each at most, all fit the GPU
+// at once: there a launch less is worth more than an even division (measured beside kOneTiles).
 template <class K>
-cudaError_t launch_decode(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
-  cudaError_t e;
-  // One launch where clusters of up to eight CTAs, a few tiles each at most, all fit the GPU
-  // at once: there a launch less is worth more than an even division (measured beside kOneTiles).
-  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
+int one_cluster(const PagedDecodeArgs& a) {
   const int tiles = (a.max_len + K::kTile - 1) / K::kTile;
   int cluster = 1;
   while (cluster < kOneCluster && cluster < tiles) cluster *= 2;
-  if (tiles <= K::kOneTiles * cluster && pairs * cluster <= K::kPerSm * num_sms) {
+  return cluster;
+}
+template <class K>
+bool decode_in_one(const PagedDecodeArgs& a, int num_sms) {
+  const int tiles = (a.max_len + K::kTile - 1) / K::kTile, cluster = one_cluster<K>(a);
+  return tiles <= K::kOneTiles * cluster &&
+         static_cast<int64_t>(a.num_seqs) * a.hkv * cluster <= K::kPerSm * num_sms;
+}
+// A warp per (sequence, head).
+template <class K>
+cudaError_t launch_pairs(const PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(K::fn(kPairs)), K::kRing, ready);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * (a.hkv << a.split);
+  const int64_t all = (pairs + kDecWarps - 1) / kDecWarps, fit = static_cast<int64_t>(K::kPerSm) * num_sms;
+  return launch_early(K::fn(kPairs), dim3(static_cast<unsigned>(all < fit ? all : fit)), dim3(kDecThreads),
+                      K::kRing, stream, 0, a, 1);
+}
+
+template <class K>
+cudaError_t launch_decode(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) {
+  cudaError_t e;
+  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.hkv;
+  const int cluster = one_cluster<K>(a);
+  if (decode_in_one<K>(a, num_sms)) {
     static std::atomic<uint64_t> one_ready{0};
     e = allow_smem(reinterpret_cast<const void*>(K::fn(kOne)), K::kSmem, one_ready);
     if (e != cudaSuccess) return e;
@@ -561,13 +585,8 @@ cudaError_t launch_decode(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) 
     one.numAttrs = 1;
     return cudaLaunchKernelEx(&one, K::fn(kOne), a, cluster);
   }
-  if (K::kPairSteps * K::kKeys >= a.max_len) {
-    static std::atomic<uint64_t> pairs_ready{0};
-    e = allow_smem(reinterpret_cast<const void*>(K::fn(kPairs)), K::kRing, pairs_ready);
-    if (e != cudaSuccess) return e;
-    const int64_t all = (pairs + kDecWarps - 1) / kDecWarps, fit = static_cast<int64_t>(K::kPerSm) * num_sms;
-    return launch_early(K::fn(kPairs), dim3(static_cast<unsigned>(all < fit ? all : fit)), dim3(kDecThreads),
-                        K::kRing, stream, 0, a, 1);
+  if constexpr (K::kPairSteps > 0) {
+    if (a.max_len <= K::kPairSteps * K::kKeys) return launch_pairs<K>(a, num_sms, stream);
   }
   // runs of warps or of CTAs
   const bool warps = decode_by_warps(K::kForm, a.group, a.num_seqs, a.hkv, a.max_len, K::kTile);

@@ -24,10 +24,11 @@ def no_device_error():
 
 
 # lengths for each way (d = 128; half the steps at d = 64): one launch of clusters, a warp per
-# (sequence, head), runs of warps, runs of CTAs
+# (sequence, head) (few enough for two with 16 heads, and more), runs of warps, runs of CTAs
 WAYS = {
     "cluster": [700, 1, 128, 0, 129],
     "pairs": [1 + 37 * i % 256 for i in range(99)] + [0, 256, 32, 33, 31],
+    "many pairs": [1 + 5 * i % 64 for i in range(290)] + [0, 64],
     "warps": [1 + 331 * i % 1000 for i in range(100)] + [0, 1024, 257],
     "runs": [1025, 0, 4000, 127, 128, 129, 1, 2047, 2048, 3333] * 8,
 }
