@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   int* s_kept = reinterpret_cast<int*>(s_first);  // FUSED, after the passes: this CTA's kept ones
   __shared__ int s_to[FUSED ? kSmallPages : 1], s_bad[FUSED ? kSmallPages + 1 : 1];
   after_stream();
+  if (!FUSED) let_next_start();  // the copy
   if (!FUSED && static_cast<int>(blockIdx.x) < note_blocks) {
     write_notes(a, blockIdx.x * kSelWarps + (threadIdx.x >> 5), note_blocks * kSelWarps, note_chunks);
     return;

@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
   const int r = lane >> 2, q4 = lane & 3;
   const int G = a.group;
   after_stream();
+  if constexpr (!ONE && !PAIRS) let_next_start();  // the join
   // who takes a run (a CTA, a warp), or ONE: the rank
   const int cta = ONE ? static_cast<int>(blockIdx.x) % cluster
                       : WARPS ? static_cast<int>(blockIdx.x) * kDecWarps + warp : blockIdx.x;

@@ -156,11 +156,16 @@ __device__ __forceinline__ float absmax_bf16x2_value(uint32_t acc) {
 }
 
 // ------------------------------------------------------------------ order within a stream
-// For kernels launched early: what is ahead in the stream has ended and its writes are seen; the kernel
-// behind may be set up (it waits in the same way). Every block comes through here before it touches
-// memory, so the end of this kernel is also the end of all before it.
+// For kernels launched early: what is ahead in the stream has ended and its writes are seen. Every block
+// comes through here before it touches memory, so the end of such a kernel is also the end of all before it.
 __device__ __forceinline__ void after_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// The kernel behind may be set up beside this one (it waits in the same way). For the second launch of a
+// call; in the last one it costs more than it gives: the next call's blocks, placed beside the old ones,
+// crowd some SMs (attention over 4-bit pages, four sequences of 4,000 tokens, called: 12.3 us, without 10.4;
+// 777 rows read back 3.6 and 3.1).
+__device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
