@@ -894,7 +894,6 @@ template <int D, int H>
 struct Fp4Kernel : Fp4Cfg<D> {
   static constexpr int kDim = D, kForm = kFp4, kPerSm = H <= 8 ? kFp4PerSm : 2, kOneTiles = 4;
   static constexpr int kPairSteps = 8, kSplitThreads = kFp4Threads<H, kSplit>;
-  static constexpr bool kEarly = true;
   static constexpr float kShift = 14.f;
   static auto fn(DecMode mode) {
     if constexpr (H > 8) {

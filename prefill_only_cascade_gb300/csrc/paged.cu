@@ -217,6 +217,8 @@ __global__ void __launch_bounds__(kDecThreads, 2)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, q4 = lane & 3;
   const int G = a.group;
+  after_stream();
+  if constexpr (!ONE) let_next_start();  // the join
   // who takes a run (a CTA, a warp), or ONE: the rank
   const int cta = ONE ? static_cast<int>(blockIdx.x) % cluster
                       : WARPS ? static_cast<int>(blockIdx.x) * kDecWarps + warp : blockIdx.x;
@@ -237,7 +239,6 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     cur.at = first_tile(cta, tiles, cluster);
     run_end = first_tile(cta + 1, tiles, cluster);
   } else {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // sequences without tokens (0 and -inf) and with lengths out of range (NaN)
     for (int b = blockIdx.x; b < a.num_seqs; b += gridDim.x) {
       const int n = checked_len(a, b);
@@ -682,7 +683,6 @@ struct DecKernel : DecCfg<D, FP8> {
   static constexpr int kDim = D, kForm = FP8 ? kE4m3 : kBf16, kPerSm = 2, kOneTiles = 8;
   static constexpr int kPairSteps = -1;  // no such launch
   static constexpr int kSplitThreads = kDecThreads;
-  static constexpr bool kEarly = false;
   static constexpr float kShift = FP8 ? 14.f : 0.f;
   static auto fn(DecMode mode) {
     return mode == kOne ? paged_decode_kernel<D, FP8, NT, kOne>

@@ -530,8 +530,7 @@ __global__ void __launch_bounds__(kFinishThreads, 4)
 // A kernel and how it is launched: K has the sizes that DecCfg has, the pages' form (kForm), the CTAs
 // per SM (kPerSm), the power of two by which its sums are scaled (kShift), tiles per CTA in one launch
 // of clusters (kOneTiles), the steps up to which a warp takes a (sequence, head) alone (kPairSteps; < 0:
-// it has no such instance), the threads of a CTA with a run (kSplitThreads), whether it waits for the
-// stream itself (kEarly) and fn(mode), its instances.
+// it has no such instance), the threads of a CTA with a run (kSplitThreads) and fn(mode), its instances.
 
 // One launch where clusters of up to eight CTAs, a few tiles each at most, all fit the GPU
 // at once: there a launch less is worth more than an even division (measured beside kOneTiles).
@@ -569,22 +568,8 @@ cudaError_t launch_decode(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) 
     static std::atomic<uint64_t> one_ready{0};
     e = allow_smem(reinterpret_cast<const void*>(K::fn(kOne)), K::kSmem, one_ready);
     if (e != cudaSuccess) return e;
-    if constexpr (K::kEarly)
-      return launch_early(K::fn(kOne), dim3(static_cast<unsigned>(pairs * cluster)), dim3(kDecThreads),
-                          K::kSmem, stream, cluster, a, cluster);
-    cudaLaunchAttribute dims;
-    dims.id = cudaLaunchAttributeClusterDimension;
-    dims.val.clusterDim.x = cluster;
-    dims.val.clusterDim.y = 1;
-    dims.val.clusterDim.z = 1;
-    cudaLaunchConfig_t one{};
-    one.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
-    one.blockDim = dim3(kDecThreads);
-    one.dynamicSmemBytes = K::kSmem;
-    one.stream = stream;
-    one.attrs = &dims;
-    one.numAttrs = 1;
-    return cudaLaunchKernelEx(&one, K::fn(kOne), a, cluster);
+    return launch_early(K::fn(kOne), dim3(static_cast<unsigned>(pairs * cluster)), dim3(kDecThreads),
+                        K::kSmem, stream, cluster, a, cluster);
   }
   if constexpr (K::kPairSteps > 0) {
     if (a.max_len <= K::kPairSteps * K::kKeys) return launch_pairs<K>(a, num_sms, stream);
@@ -599,13 +584,7 @@ cudaError_t launch_decode(PagedDecodeArgs& a, int num_sms, cudaStream_t stream) 
   const auto fn = K::fn(warps ? kWarps : kSplit);
   e = allow_smem(reinterpret_cast<const void*>(fn), smem, ready[warps]);
   if (e != cudaSuccess) return e;
-  const int threads = warps ? kDecThreads : K::kSplitThreads;
-  if constexpr (K::kEarly) {
-    e = launch_early(fn, dim3(ctas), dim3(threads), smem, stream, 0, a, 1);
-  } else {
-    fn<<<ctas, threads, smem, stream>>>(a, 1);
-    e = cudaGetLastError();
-  }
+  e = launch_early(fn, dim3(ctas), dim3(warps ? kDecThreads : K::kSplitThreads), smem, stream, 0, a, 1);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
