@@ -5,7 +5,8 @@ import torch
 
 import prefill_only_cascade_gb300 as q
 
-pytestmark = pytest.mark.gpu
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(q._calls is None, reason="built without PyTorch's or Python's headers")]
 DEV, BF, I32, F32, U8 = "cuda", torch.bfloat16, torch.int32, torch.float32, torch.uint8
 NATIVE = {"append": q.paged_kv_append, "read": q.paged_kv_read, "decode": q.paged_decode_attn,
           "evict": q.paged_kv_evict}
