@@ -37,6 +37,7 @@
 #include "kernels.h"
 #include "paged_decode.cuh"
 #include "ptx.cuh"
+#include "step_ring.cuh"
 
 namespace quail {
 
@@ -424,8 +425,7 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue(s);
   }
-  int stage = 0;
-  uint32_t parity = 0;
+  StepRing<kStages> due;                 // the step that is waited for
 
   while (true) {
     // ---------------------------------------------------- one piece
@@ -478,25 +478,32 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
 
     // (PROD: every warp goes through all tiles, also one that has no keys in the last)
     for (int key0 = key_begin + own; key0 - (PROD ? own : 0) < key_end; key0 += kTile) {
+      const bool next_too = ld_more;     // the next step is issued as well
       if constexpr (!PROD) {
         __syncwarp();  // the stage before was read by every lane
-        issue(stage == 0 ? kStages - 1 : stage - 1);
+        issue(due.ahead());
       }
-      if (!late && !__all_sync(0xFFFFFFFFu, mbar_try_wait(full + 8 * stage, parity))) {
+      const int stage = due.stage;
+      if (!late && !__all_sync(0xFFFFFFFFu, mbar_try_wait(full + 8 * stage, due.parity))) {
         late = !__all_sync(0xFFFFFFFFu,
-                           fp4_wait(full + 8 * stage, parity, a.timeout_ns, a.err_word,
+                           fp4_wait(full + 8 * stage, due.parity, a.timeout_ns, a.err_word,
                                     PROD ? &s_abort : nullptr));
-        ld_more &= !late;
+        if (!PROD && late) {
+          // Nothing more is loaded, and what is on its way lands before the ring's memory is used for
+          // anything else or given up, or the limit passes.
+          static_assert(kStages == 2, "this step and the next one are all that can be on their way");
+          ld_more = false;
+          due.drain(next_too ? 2 : 1, [&](int s, uint32_t parity) {
+            fp4_wait(full + 8 * s, parity, a.timeout_ns, a.err_word, nullptr);
+          });
+        }
       }
       bad |= late || (PROD ? s_bad_tile[stage] != 0 : (bad_steps >> stage) & 1u);
       const uint32_t step = ring + stage * (kShare * C::kStep), share = PROD ? warp : 0;
       const uint32_t kbuf = step + share * C::kCodes, vbuf = kbuf + kShare * C::kCodes;
       const uint32_t ksc = step + 2 * kShare * C::kCodes + share * C::kScales, vsc = ksc + kShare * C::kScales;
       const uint32_t read = empty + 8 * stage;
-      if (++stage == kStages) {
-        stage = 0;
-        parity ^= 1;
-      }
+      due.next();
       if (PROD && key0 >= key_end) {
         if (lane == 0 && !late) mbar_arrive_at(read);
         continue;
@@ -875,9 +882,6 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
     if (lane == 0) s_piece[warp] = nxt;
     __syncwarp();
   }
-  if (!PROD && late)  // what is still on its way lands before the memory is given up, or the limit passes
-    for (int i = 0; i < kStages; ++i)
-      fp4_wait(full + 8 * i, i < stage ? parity : parity ^ 1, a.timeout_ns, a.err_word, nullptr);
   if constexpr (ONE) join_cluster<D>(a, s_piece[warp], cluster, cta, s_part, s_pml, s_lse2, kShift, true);
 }
 
