@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
       const uint32_t read = empty + 8 * stage;
       due.next();
       if (PROD && key0 >= key_end) {
+        __syncwarp();  // every lane has read s_bad_tile
         if (lane == 0 && !late) mbar_arrive_at(read);
         continue;
       }
