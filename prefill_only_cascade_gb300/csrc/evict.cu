@@ -32,7 +32,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxKeys = 32;                         // keys a thread holds at most
 
 __device__ __forceinline__ int evict_len(const PagedEvictArgs& a, int b) {
-  const int n = __ldg(a.lens + b);
+  const int n = a.lens[b];
   return n >= 0 && n <= a.max_len ? n : -1;
 }
 
@@ -73,13 +73,13 @@ __device__ __forceinline__ int pages_of(const PagedEvictArgs& a, int tokens) {
 //   dup[p]    -1 once claimed; the entry that found p claimed by another
 //   hold[p]   an entry of block_table that names p (same pool only; any of them)
 __device__ __forceinline__ bool is_claim(const PagedEvictArgs& a, int entry, int p) {
-  if (entry < 0 || entry >= a.num_seqs * a.dst_max_pages || __ldg(a.dst_table + entry) != p)
+  if (entry < 0 || entry >= a.num_seqs * a.dst_max_pages || a.dst_table[entry] != p)
     return false;
   const int n = evict_len(a, entry / a.dst_max_pages);
   return entry % a.dst_max_pages < pages_of(a, min(n, a.budget));
 }
 __device__ __forceinline__ bool is_held(const PagedEvictArgs& a, int entry, int p) {
-  if (entry < 0 || entry >= a.num_seqs * a.max_pages || __ldg(a.table + entry) != p) return false;
+  if (entry < 0 || entry >= a.num_seqs * a.max_pages || a.table[entry] != p) return false;
   return entry % a.max_pages < pages_of(a, evict_len(a, entry / a.max_pages));
 }
 
@@ -127,12 +127,12 @@ __device__ void write_notes(const PagedEvictArgs& a, int warp, int warps, int ch
     const int b = static_cast<int>(item / chunks), j = static_cast<int>(item % chunks) * 32 + lane;
     const int n = evict_len(a, b);
     if (a.same_pool && j < pages_of(a, n)) {
-      const int p = __ldg(a.table + b * a.max_pages + j);
+      const int p = a.table[b * a.max_pages + j];
       if (p >= 0 && p < a.num_pages) a.hold[p] = b * a.max_pages + j;
     }
     if (j < pages_of(a, min(n, a.budget))) {
       const int entry = b * a.dst_max_pages + j;
-      const int p = __ldg(a.dst_table + entry);
+      const int p = a.dst_table[entry];
       if (p < 0 || p >= a.dst_num_pages) continue;
       // of several entries that claim p the last one to do so sees another's claim, and its
       // note follows every clearing
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int at = w0 + 32 * (i0 + i) + lane;
-        x[i] = at < w1 ? __ldg(score + e0 + at) : 0.f;
+        x[i] = at < w1 ? score[e0 + at] : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -228,10 +228,12 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   float* score_out =
       a.score_out != nullptr ? a.score_out + static_cast<int64_t>(pair) * a.score_out_stride : nullptr;
   const int tid = rank * kSelThreads + threadIdx.x, threads = cluster * kSelThreads;
+  // the first recent token's score comes with the others, not after the barrier below
+  const float recent_score = score_out != nullptr && tid < recent ? score[elig + tid] : 0.f;
   if constexpr (FUSED) {
     const int mine = pages_of(a, fresh);
     for (int j = threadIdx.x; j <= mine; j += kSelThreads) {
-      const int p = j < mine ? __ldg(a.dst_table + b * a.dst_max_pages + j) : 0;
+      const int p = j < mine ? a.dst_table[b * a.dst_max_pages + j] : 0;
       if (j < mine) s_to[j] = p;
       s_bad[j] = j < mine && (p < 0 || p >= a.dst_num_pages);  // the last: the source pages
     }
@@ -244,18 +246,18 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     for (int e = threadIdx.x; e < a.num_seqs * claims; e += kSelThreads) {
       const int seq = e / claims, j = e % claims, len = evict_len(a, seq);
       if (j < pages_of(a, min(len, a.budget)))
-        meet(__ldg(a.dst_table + seq * a.dst_max_pages + j), seq * a.dst_max_pages + j);
+        meet(a.dst_table[seq * a.dst_max_pages + j], seq * a.dst_max_pages + j);
     }
     if (a.same_pool) {
       const int held = pages_of(a, a.max_len);
       for (int e = threadIdx.x; e < a.num_seqs * held; e += kSelThreads) {
         const int seq = e / held, j = e % held;
-        if (j < pages_of(a, evict_len(a, seq))) meet(__ldg(a.table + seq * a.max_pages + j), -1);
+        if (j < pages_of(a, evict_len(a, seq))) meet(a.table[seq * a.max_pages + j], -1);
       }
     }
     if (g == 0 && rank == 0)
       for (int j = threadIdx.x; j < pages_of(a, n); j += kSelThreads) {
-        const int p = __ldg(a.table + b * a.max_pages + j);
+        const int p = a.table[b * a.max_pages + j];
         if (p < 0 || p >= a.num_pages) s_bad[mine] = 1;
       }
   } else if (g == 0 && tid == 0) {  // the new length, once
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   // the recent tokens, and what follows the last kept one
   for (int i = tid; i < recent; i += threads) {
     kept[k + i] = elig + i;
-    if (score_out != nullptr) score_out[k + i] = __ldg(score + elig + i);
+    if (score_out != nullptr) score_out[k + i] = i == tid ? recent_score : score[elig + i];
   }
   for (int i = fresh + tid; i < a.budget; i += threads) kept[i] = -1;
   if (score_out != nullptr)
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         const int pos = e0 + w0 + 32 * i + bit;
         kept[at] = pos;
         if (FUSED) s_kept[at - first_kept] = pos;
-        if (score_out != nullptr) score_out[at] = __ldg(score + pos);
+        if (score_out != nullptr) score_out[at] = score[pos];
       }
     }
   }
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       const int i = old ? first_kept + at : k + r0 + at - kept_here;
       const int pos = old ? s_kept[at] : elig + r0 + at - kept_here;
       if (pos < 0 || pos >= n) continue;  // only if the scores changed meanwhile
-      const int from = __ldg(a.table + b * a.max_pages + (pos >> a.page_shift));
+      const int from = a.table[b * a.max_pages + (pos >> a.page_shift)];
       if (s_bad[i >> a.page_shift] || from < 0 || from >= a.num_pages) continue;
       const int to = s_to[i >> a.page_shift];
       const int64_t src = row_at(a, from, pos & mask, g) + 16 * c;
@@ -544,8 +546,7 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const Paged
   const int fresh = min(n, a.budget);
   const int64_t rows = static_cast<int64_t>(fresh) * a.hkv;
   if (r0 >= rows) {
-    // also where nothing is to be moved: the call ends with its selection
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_stream();  // also where nothing is to be moved: the call ends with its selection
     return;
   }
   const int count = static_cast<int>(min(static_cast<int64_t>(kCopyThreads), rows - r0));
@@ -553,9 +554,8 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const Paged
   const int64_t r = r0 + threadIdx.x;
   const int i = static_cast<int>(r / a.hkv), g = static_cast<int>(r % a.hkv);
   // what the selection does not write is read before its end
-  const int to = has ? __ldg(a.dst_table + static_cast<int64_t>(b) * a.dst_max_pages +
-                             (i >> a.page_shift)) : -1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int to = has ? a.dst_table[static_cast<int64_t>(b) * a.dst_max_pages + (i >> a.page_shift)] : -1;
+  after_stream();
   if (has) {
     const int mask = (1 << a.page_shift) - 1;
     const bool to_ok = to >= 0 && to < a.dst_num_pages;
@@ -564,8 +564,8 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const Paged
     const int dup = to_ok ? a.dup[to] : 0;
     const int hold = to_ok && a.same_pool ? a.hold[to] : -1;
     const bool pos_ok = pos >= 0 && pos < n;
-    const int from = pos_ok ? __ldg(a.table + static_cast<int64_t>(b) * a.max_pages +
-                                    (pos >> a.page_shift)) : -1;
+    const int from =
+        pos_ok ? a.table[static_cast<int64_t>(b) * a.max_pages + (pos >> a.page_shift)] : -1;
     // the destination page is written once, by this sequence, and held by none
     const bool ok = to_ok && dup == -1 && pos_ok && from >= 0 && from < a.num_pages &&
                     !is_held(a, hold, to);

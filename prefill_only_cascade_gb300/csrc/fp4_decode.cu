@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
       auto page_of = [&]() {             // lane i: of the tile's i-th part
         const int pos = key + lane * part;
         return lane * part < C::kTile && pos < ld.ke
-                   ? __ldg(a.table + static_cast<int64_t>(ld.b) * a.max_pages + (pos >> a.page_shift)) : -1;
+                   ? a.table[static_cast<int64_t>(ld.b) * a.max_pages + (pos >> a.page_shift)] : -1;
       };
       int page = page_of();
       bool more = true;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
       ld_head = (ld.g >> split) * head_bytes;
     }
     const int last = (min(C::kKeys, ld_ke - ld_key) - 1 + (ld_key & page_mask)) >> a.page_shift;
-    page = __ldg(ld_table + (ld_key >> a.page_shift) + min(lane, last));
+    page = ld_table[(ld_key >> a.page_shift) + min(lane, last)];
   };
   auto issue = [&](int stage) {          // the stage's last step has been read by every lane
     if (!ld_more) return;
@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
   uint4 qraw[NT][D / 32];
   float k_scale, v_scale;                // of the same (sequence, head)
   auto load_q = [&](int b, int g) {
-    k_scale = __ldg(a.k_scale + static_cast<int64_t>(b) * a.hkv + (g >> split));
-    v_scale = __ldg(a.v_scale + static_cast<int64_t>(b) * a.hkv + (g >> split));
+    k_scale = a.k_scale[static_cast<int64_t>(b) * a.hkv + (g >> split)];
+    v_scale = a.v_scale[static_cast<int64_t>(b) * a.hkv + (g >> split)];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int h = FOLD ? r & 3 : r + 8 * n;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
           q4 * (D / 4));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
-        qraw[n][i] = h < G ? __ldg(qp + i) : make_uint4(0u, 0u, 0u, 0u);
+        qraw[n][i] = h < G ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
     }
   };
 

@@ -197,7 +197,7 @@ enum KvForm {
   kFp4    // e2m1 codes, an e4m3 scale per 16 values and a scale per sequence and KV head
 };
 // A launch that may begin before the kernel ahead of it in the stream has ended: the kernel itself waits
-// for that (after_stream) before it touches memory.
+// for that (after_stream, with the rules beside it).
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                          int cluster, A... args) {

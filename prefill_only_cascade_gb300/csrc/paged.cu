@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       const int32_t* table = a.table + static_cast<int64_t>(ld.b) * a.max_pages;
 #pragma unroll
       for (int i = 0; i < C::kSteps16; ++i)
-        page[i] = ld_key + 16 * i < ld.ke ? __ldg(table + ((ld_key + 16 * i) >> a.page_shift)) : 0;
+        page[i] = ld_key + 16 * i < ld.ke ? table[(ld_key + 16 * i) >> a.page_shift] : 0;
     }
   };
   auto issue = [&](int stage) {
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
 #pragma unroll
       for (int ks = 0; ks < C::kQS; ++ks) {
         const int off = (q4 + 4 * (ks / (EC / 4))) * EC + 4 * (ks % (EC / 4));
-        qraw[n][ks] = h < G ? __ldg(reinterpret_cast<const uint2*>(qp + off)) : make_uint2(0u, 0u);
+        qraw[n][ks] = h < G ? *reinterpret_cast<const uint2*>(qp + off) : make_uint2(0u, 0u);
       }
     }
   };
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         e = min(e, 126);  // a power of two that is a normal float, as is its inverse
         const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
         c_log2[n] *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        c_log2[n] *= __ldg(a.k_scale + static_cast<int64_t>(cur.b) * a.hkv + cur.g);
+        c_log2[n] *= a.k_scale[static_cast<int64_t>(cur.b) * a.hkv + cur.g];
 #pragma unroll
         for (int ks = 0; ks < C::kQS; ++ks) {
           const uint2 w = qraw[n][ks];
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     if (more) load_q(nxt.b, nxt.g);
 
     // ---------------------------------------------------- the four warps' parts together
-    const float vs = FP8 ? __ldg(a.v_scale + static_cast<int64_t>(cur.b) * a.hkv + cur.g) : 1.f;
+    const float vs = FP8 ? a.v_scale[static_cast<int64_t>(cur.b) * a.hkv + cur.g] : 1.f;
     // slot 0: the run began inside this (b, g); slot 1: the run's last, begun here
     const int64_t part = 2 * static_cast<int64_t>(cta) + (cur.at == cur.piece0 ? 1 : 0);
     auto note = [&](bool any_bad) {      // by one thread, about (b, g)

@@ -111,7 +111,7 @@ __device__ __forceinline__ int64_t first_tile(int c, int64_t total, int n) {
 
 // The length of sequence b if it is one the call allows, else -1.
 __device__ __forceinline__ int checked_len(const PagedDecodeArgs& a, int b) {
-  const int n = __ldg(a.lens + b);
+  const int n = a.lens[b];
   return n >= 0 && n <= a.max_len ? n : -1;
 }
 
@@ -223,7 +223,7 @@ __device__ __forceinline__ void join_cluster(const PagedDecodeArgs& a, const Pie
                                              float* s_lse2, float l_shift, bool scaled) {
   const int G = a.group;
   if (cluster > 1) cluster_sync(); else __syncthreads();
-  const float vs = scaled ? __ldg(a.v_scale + static_cast<int64_t>(cur.b) * a.hkv + cur.g) : 1.f;
+  const float vs = scaled ? a.v_scale[static_cast<int64_t>(cur.b) * a.hkv + cur.g] : 1.f;
   const int64_t row0 = static_cast<int64_t>(cur.b) * a.hq + cur.g * G;
   for (int h = cta; h < G; h += cluster) {
     float2 ml[kOneCluster];
@@ -401,7 +401,7 @@ __device__ __forceinline__ void join_parts(const PagedDecodeArgs& a, int ctas, f
       const int seq = j ? job_seq[1] : job_seq[0], head = j ? job_head[1] : job_head[0];
       const int64_t row = static_cast<int64_t>(seq) * a.hq + head * G + h;
       const float vs = a.v_scale != nullptr
-                           ? __ldg(a.v_scale + static_cast<int64_t>(seq) * a.hkv + head) : 1.f;
+                           ? a.v_scale[static_cast<int64_t>(seq) * a.hkv + head] : 1.f;
       uint32_t packed[V / 2];
 #pragma unroll
       for (int v = 0; v < V; v += 2)
@@ -434,8 +434,11 @@ __device__ __forceinline__ void add_weights(const PagedDecodeArgs& a, int ctas, 
   const int64_t row = static_cast<int64_t>(pair) * a.group;  // = b * Hq + g * G
   const int64_t out_row = static_cast<int64_t>(pair) * a.score_stride;
   const int64_t first = static_cast<int64_t>(chunk) * kWeightKeys;
-  if (first >= n) return;
-  // the inputs of the call and what does not depend on lse2 first
+  if (first >= n) {
+    after_stream();
+    return;
+  }
+  // the inputs of the call, which the attention does not write, and what does not depend on lse2 first
   float base[kWeightPer];
 #pragma unroll
   for (int k = 0; k < kWeightPer; ++k) {

@@ -46,19 +46,19 @@ __device__ __forceinline__ void find_slots(const PagedRows& p, int64_t t0, int n
       int lo = 0, hi = p.num_seqs;  // the last sequence that begins at or before t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(p.offsets + mid) <= t) lo = mid; else hi = mid;
+        if (p.offsets[mid] <= t) lo = mid; else hi = mid;
       }
       b = lo;
-      const int64_t o0 = __ldg(p.offsets + b);
+      const int64_t o0 = p.offsets[b];
       i = t - o0;
-      ok = o0 <= t && t < __ldg(p.offsets + b + 1);
+      ok = o0 <= t && t < p.offsets[b + 1];
     }
     if (ok) {
       slot = kNoSlot;
-      const int64_t start = __ldg(p.start_pos + b);
+      const int64_t start = p.start_pos[b];
       const int64_t pos = start + i;
       if (start >= 0 && pos < p.max_len) {
-        const int page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + (pos >> p.page_shift));
+        const int page = p.table[static_cast<int64_t>(b) * p.max_pages + (pos >> p.page_shift)];
         if (page >= 0 && page < p.num_pages)
           slot = (static_cast<int64_t>(page) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
       }
@@ -70,8 +70,8 @@ __device__ __forceinline__ void find_slots(const PagedRows& p, int64_t t0, int n
   // the offsets as a whole: increasing from 0 to the number of rows
   if (blockIdx.x == 0 && p.offsets != nullptr) {
     for (int b = threadIdx.x; b <= p.num_seqs; b += kRowThreads) {
-      const int64_t o = __ldg(p.offsets + b);
-      const int64_t next = b < p.num_seqs ? __ldg(p.offsets + b + 1) : p.total;
+      const int64_t o = p.offsets[b];
+      const int64_t next = b < p.num_seqs ? p.offsets[b + 1] : p.total;
       if ((b == 0 && o != 0) || (b < p.num_seqs ? next < o : next != o))
         atomicOr(p.err_word, kErrDeviceBounds);
     }
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kRowThreads, kAppendPerSm) fp4_append_kernel(c
   auto load_k = [&]() {
     if (t >= n) return;
     const uint4* x = reinterpret_cast<const uint4*>(p.k_new + (t0 + t) * p.k_stride + g * D + 16 * blk);
-    k0 = __ldg(x);
-    k1 = __ldg(x + 1);
+    k0 = x[0];
+    k1 = x[1];
   };
   load_k();
   find_slots(p, t0, n, s_slot, s_seq);
@@ -197,11 +197,11 @@ __global__ void __launch_bounds__(kRowThreads, kAppendPerSm) fp4_append_kernel(c
     int64_t code, scale;
     if (slot >= 0) {
       const uint4* x = reinterpret_cast<const uint4*>(p.v_new + (t0 + t) * p.v_stride + g * D + 16 * blk);
-      v0 = __ldg(x);
-      v1 = __ldg(x + 1);
+      v0 = x[0];
+      v1 = x[1];
       const int64_t sc = static_cast<int64_t>(s_seq[t]) * p.hkv + g;
-      sk = __ldg(p.k_scale + sc);
-      sv = __ldg(p.v_scale + sc);
+      sk = p.k_scale[sc];
+      sv = p.v_scale[sc];
       fp4_place(p, D, slot, g, blk, code, scale);
     }
     auto ordinary = [](float S) { return S >= 8.673617379884035e-19f && S <= 1.152921504606847e18f; };
@@ -238,13 +238,13 @@ struct Held {
     if constexpr (F == kFp4) {
       int64_t code, scale;
       fp4_place(p, D, slot, g, blk, code, scale);
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(pages + code));
-      a = make_uint4(x.x, x.y, __ldg(pages + scale), 0u);
+      const uint2 x = *reinterpret_cast<const uint2*>(pages + code);
+      a = make_uint4(x.x, x.y, pages[scale], 0u);
     } else {
       const uint4* x = reinterpret_cast<const uint4*>(
           pages + (F == kBf16 ? 2 : 1) * ((slot * p.hkv + g) * D + 16 * blk));
-      a = __ldg(x);
-      if constexpr (F == kBf16) b = __ldg(x + 1);
+      a = x[0];
+      if constexpr (F == kBf16) b = x[1];
     }
   }
   __device__ __forceinline__ void decode(float S) {
@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_read_kernel(const PagedRows
     if (slot >= 0) {
       if (p.k_out != nullptr) k.load(p, p.k_pages, slot, g, blk);
       if (p.v_out != nullptr) v.load(p, p.v_pages, slot, g, blk);
-      k.decode(F == kBf16 || p.k_out == nullptr ? 1.f : __ldg(p.k_scale + sc));
-      v.decode(F == kBf16 || p.v_out == nullptr ? 1.f : __ldg(p.v_scale + sc));
+      k.decode(F == kBf16 || p.k_out == nullptr ? 1.f : p.k_scale[sc]);
+      v.decode(F == kBf16 || p.v_out == nullptr ? 1.f : p.v_scale[sc]);
     }
     if (p.k_out != nullptr) {
       uint4* to = reinterpret_cast<uint4*>(p.k_out + (t0 + t) * p.k_stride + col);

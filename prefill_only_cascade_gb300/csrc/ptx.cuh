@@ -156,15 +156,23 @@ __device__ __forceinline__ float absmax_bf16x2_value(uint32_t acc) {
 }
 
 // ------------------------------------------------------------------ order within a stream
-// For kernels launched early: what is ahead in the stream has ended and its writes are seen. Every block
-// comes through here before it touches memory, so the end of such a kernel is also the end of all before it.
+// For kernels launched early (set up, and their blocks placed, while the kernel ahead still runs):
+//  - Every block waits here once, also one that has nothing to do: the end of such a kernel is then the end
+//    of all before it.
+//  - A kernel lets the next one start only behind its own wait. All before this kernel has then ended when
+//    the next one's blocks begin, and these may read what this kernel does not write before their own wait:
+//    the finish of the attention the lengths and score_in, the eviction's copy the lengths and dst_table.
+//    Where the kernel ahead is not known, nothing is touched before the wait.
+//  - Loads are plain ones: __ldg is for memory that nothing writes while the kernel lives, and here its life
+//    begins before the writes ahead of it end.
+// What is ahead in the stream has ended and its writes are seen.
 __device__ __forceinline__ void after_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 // The kernel behind may be set up beside this one (it waits in the same way). For the second launch of a
-// call; in the last one it costs more than it gives: the next call's blocks, placed beside the old ones,
-// crowd some SMs (attention over 4-bit pages, four sequences of 4,000 tokens, called: 12.3 us, without 10.4;
-// 777 rows read back 3.6 and 3.1).
+// call; in the last one it mostly costs more than it gives: the next call's blocks, placed beside the old
+// ones, crowd some SMs (attention over 4-bit pages, four sequences of 4,000 tokens, called: 12.3 us, without
+// 10.4; 777 rows read back 3.6 and 3.1). The blocks that add up weights do it too (see there).
 __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
