@@ -28,7 +28,9 @@ decltype(&quail_paged_kv_read) read_fn = nullptr;
 decltype(&quail_paged_decode_attn) decode_fn = nullptr;
 decltype(&quail_paged_kv_evict) evict_fn = nullptr;
 
-// The checks of one call; `ok` falls with the first that fails.
+// The checks of one call; `ok` falls with the first that fails. Addresses are taken as the binding's own
+// checks take them, for writing: a tensor that shares its memory with a lazy clone gets its own first
+// (inputs too: an eviction may name one pool as both).
 struct Call {
   quail_paged_desc d{};
   int index = -1;
@@ -62,7 +64,7 @@ struct Call {
     const at::Tensor* t = tensor(o, type);
     if (t == nullptr) return nullptr;
     ok = t->sizes() == shape && t->is_contiguous();
-    return ok ? const_cast<void*>(t->const_data_ptr()) : nullptr;
+    return ok ? t->mutable_data_ptr() : nullptr;
   }
   // bf16 rows [n, heads, d] any distance apart; n < 0: as many as there are.
   void* rows(PyObject* o, int64_t& n, int64_t heads, int64_t& stride) {
@@ -74,7 +76,7 @@ struct Call {
     n = t->size(0);
     ok = n == 0 || (t->stride(2) == 1 && (t->stride(1) == width || heads <= 1));
     stride = n > 1 ? t->stride(0) : heads * width;
-    return ok ? const_cast<void*>(t->const_data_ptr()) : nullptr;
+    return ok ? t->mutable_data_ptr() : nullptr;
   }
   void* pool(PyObject* o, int64_t pages) {
     const int64_t hkv = d.num_kv_heads, page = d.page_size, width = d.head_dim;
@@ -111,14 +113,14 @@ struct Call {
          t->size(2) >= least && t->is_contiguous();
     if (!ok) return nullptr;
     width = t->size(2);
-    return static_cast<float*>(const_cast<void*>(t->const_data_ptr()));
+    return static_cast<float*>(t->mutable_data_ptr());
   }
   void* workspace(PyObject* o, size_t& bytes) {
     const at::Tensor* t = tensor(o, ScalarType::Byte);
     if (t == nullptr) return nullptr;
     ok = t->dim() == 1 && t->is_contiguous();
     bytes = static_cast<size_t>(t->numel());
-    return ok ? const_cast<void*>(t->const_data_ptr()) : nullptr;
+    return ok ? t->mutable_data_ptr() : nullptr;
   }
   int32_t number(PyObject* o) {  // of a non-negative 32-bit value
     if (!PyLong_CheckExact(o)) {
