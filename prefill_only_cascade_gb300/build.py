@@ -38,25 +38,36 @@ def _flags(extra=()):
             "-I" + os.path.join(ROOT, "include"), "-I" + CSRC, *extra]
 
 
+def _torch_home() -> str:
+    """Where PyTorch is installed, found without loading it."""
+    import importlib.util
+
+    try:
+        spec = importlib.util.find_spec("torch")
+    except ValueError as e:  # a stand-in among the loaded modules
+        raise ImportError(str(e)) from e
+    if spec is None or spec.origin is None:
+        raise ImportError("PyTorch is not installed")
+    return os.path.dirname(spec.origin)
+
+
 def build_calls(nvcc: str) -> str | None:
     """_paged_calls.so; None (and why, on stderr) where it cannot be built."""
     import sysconfig
 
-    import torch
-
-    home = os.path.dirname(torch.__file__)
-    includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
-                sysconfig.get_paths()["include"],
-                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
-                os.path.join(ROOT, "include")]
     tmp = CALLS + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *["-I" + x for x in includes],
-           os.path.join(CSRC, "paged_calls.cpp"), "-o", tmp, "-L" + os.path.join(home, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     try:
+        home = _torch_home()
+        includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                    sysconfig.get_paths()["include"],
+                    os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
+                    os.path.join(ROOT, "include")]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *["-I" + x for x in includes],
+               os.path.join(CSRC, "paged_calls.cpp"), "-o", tmp, "-L" + os.path.join(home, "lib"),
+               "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         log = r.stderr if r.returncode != 0 else ""
-    except OSError as e:
+    except (ImportError, OSError) as e:
         log = str(e)
     if log:
         print(f"_paged_calls.so not built, the binding checks arguments in Python:\n{log[-2000:]}", file=sys.stderr)
