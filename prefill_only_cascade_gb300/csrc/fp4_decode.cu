@@ -883,7 +883,11 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
     if (lane == 0) s_piece[warp] = nxt;
     __syncwarp();
   }
-  if constexpr (ONE) join_cluster<D>(a, s_piece[warp], cluster, cta, s_part, s_pml, s_lse2, kShift, true);
+  if constexpr (ONE) {
+    const Piece cur = s_piece[warp];
+    constexpr bool kScaled = true;
+#include "join_cluster.inc"
+  }
 }
 
 // Which way (see launch_decode), both sides measured in a graph (8 KV heads, d = 128, G = 4 unless said):

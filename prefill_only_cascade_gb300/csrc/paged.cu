@@ -670,8 +670,11 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     cur = nxt;
   }
 
-  if constexpr (ONE)
-    join_cluster<D>(a, cur, cluster, cta, s_part, s_pml, s_lse2, FP8 ? 14.f : 0.f, FP8);
+  if constexpr (ONE) {
+    constexpr float kShift = FP8 ? 14.f : 0.f;
+    constexpr bool kScaled = FP8;
+#include "join_cluster.inc"
+  }
 }
 
 // One launch (see launch_decode), both sides measured (8 KV heads, d = 128): one sequence of 777

@@ -215,68 +215,6 @@ __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
   return v;
 }
 
-// One launch, at the end: the parts (s_part [head][d], s_pml [head]) of a cluster's CTAs for its
-// (sequence, head) joined through distributed shared memory, and the weights of each CTA's keys.
-template <int D>
-__device__ __forceinline__ void join_cluster(const PagedDecodeArgs& a, const Piece& cur, int cluster,
-                                             int cta, const float* s_part, const float2* s_pml,
-                                             float* s_lse2, float l_shift, bool scaled) {
-  const int G = a.group;
-  if (cluster > 1) cluster_sync(); else __syncthreads();
-  const float vs = scaled ? a.v_scale[static_cast<int64_t>(cur.b) * a.hkv + cur.g] : 1.f;
-  const int64_t row0 = static_cast<int64_t>(cur.b) * a.hq + cur.g * G;
-  for (int h = cta; h < G; h += cluster) {
-    float2 ml[kOneCluster];
-    float x[kOneCluster];
-    const int d = threadIdx.x;
-    float top = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < kOneCluster; ++c) {
-      ml[c] = make_float2(-INFINITY, 0.f);
-      x[c] = 0.f;
-      if (c < cluster) {
-        ml[c] = ld_cluster_f32x2(cluster_map(&s_pml[h], c));
-        if (d < D) x[c] = ld_cluster_f32(cluster_map(&s_part[h * D + d], c));
-        top = fmaxf(top, ml[c].x);
-      }
-    }
-    float sum = 0.f, acc = 0.f;
-#pragma unroll
-    for (int c = 0; c < kOneCluster; ++c) {
-      const float f = ml[c].x == -INFINITY ? 0.f : ex2(ml[c].x - top);
-      sum = fmaf(ml[c].y, f, sum);
-      acc = fmaf(x[c], f, acc);
-    }
-    if (d < D) a.out[(row0 + h) * D + d] = __float2bfloat16(acc / sum * vs);
-    if (d == 0 && a.lse != nullptr)
-      a.lse[row0 + h] = (top + (log2f(sum) - l_shift)) * 0.6931471805599453f;
-  }
-  if (a.raw != nullptr) {
-    if (threadIdx.x < G) {
-      float top = -INFINITY, sum = 0.f;
-      for (int c = 0; c < cluster; ++c)
-        top = fmaxf(top, ld_cluster_f32x2(cluster_map(&s_pml[threadIdx.x], c)).x);
-      for (int c = 0; c < cluster; ++c) {
-        const float2 ml = ld_cluster_f32x2(cluster_map(&s_pml[threadIdx.x], c));
-        sum = fmaf(ml.y, ml.x == -INFINITY ? 0.f : ex2(ml.x - top), sum);
-      }
-      s_lse2[threadIdx.x] = top + (log2f(sum) - l_shift);
-    }
-    __syncthreads();
-    const int64_t out_row = (static_cast<int64_t>(cur.b) * a.hkv + cur.g) * a.score_stride;
-    for (int j = cur.kb + threadIdx.x; j < cur.ke; j += kDecThreads) {  // this CTA's own keys
-      float w = 0.f;
-      for (int h = 0; h < G; ++h) {
-        const float lse2 = s_lse2[h];
-        const float x = a.raw[(row0 + h) * a.raw_stride + j];
-        if (lse2 > -INFINITY) w += ex2(x - lse2);
-      }
-      a.score_out[out_row + j] = (a.score_in != nullptr ? a.score_in[out_row + j] : 0.f) + w;
-    }
-  }
-  if (cluster > 1) cluster_sync();  // no CTA leaves while others read its part
-}
-
 // How the tiles are dealt out.
 enum DecMode {
   kSplit,  // runs of CTA tiles, a run per CTA

@@ -19,7 +19,7 @@ def code(name):
     return text
 
 
-@pytest.mark.parametrize("name", EARLY)
+@pytest.mark.parametrize("name", EARLY + ["join_cluster.inc"])
 def test_loads_are_plain(name):
     assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", code(name))
 
