@@ -771,15 +771,17 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
               a.part_ml[part * G + h] = make_float2(m[n][j], sum);
             }
           }
-          const float inv = vs / sum;
+          // (small scales apart: the quotient could have few bits left, or none, where the output has all)
+          const bool small = fabsf(vs) < 8.673617379884035e-19f;  // 2^-60
+          const float inv = (small ? 1.f : vs) / sum, rest = small ? vs : 1.f;
 #pragma unroll
           for (int t = 0; t < C::kMT; t += 4) {  // eight neighbouring d
             if (cur.whole) {
               uint4 x;
-              x.x = pack2<false>(o[n][t][j] * inv, o[n][t][2 + j] * inv);
-              x.y = pack2<false>(o[n][t + 1][j] * inv, o[n][t + 1][2 + j] * inv);
-              x.z = pack2<false>(o[n][t + 2][j] * inv, o[n][t + 2][2 + j] * inv);
-              x.w = pack2<false>(o[n][t + 3][j] * inv, o[n][t + 3][2 + j] * inv);
+              x.x = pack2<false>(o[n][t][j] * inv * rest, o[n][t][2 + j] * inv * rest);
+              x.y = pack2<false>(o[n][t + 1][j] * inv * rest, o[n][t + 1][2 + j] * inv * rest);
+              x.z = pack2<false>(o[n][t + 2][j] * inv * rest, o[n][t + 2][2 + j] * inv * rest);
+              x.w = pack2<false>(o[n][t + 3][j] * inv * rest, o[n][t + 3][2 + j] * inv * rest);
               *reinterpret_cast<uint4*>(a.out + row * D + out_d(t)) = x;
             } else {
               float4* to = reinterpret_cast<float4*>(a.part_o + (part * G + h) * D + out_d(t));

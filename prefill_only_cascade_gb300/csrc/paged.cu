@@ -594,16 +594,18 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           const float sum = __shfl_sync(0xFFFFFFFFu, l[n], 8 * q4 + 4 * h);
           const int hh = 2 * q4 + h;
           if (8 * n + hh >= G) continue;
-          const float inv = vs / sum;
+          // (small scales apart: the quotient could have few bits left, or none, where the output has all)
+          const bool small = fabsf(vs) < 8.673617379884035e-19f;  // 2^-60
+          const float inv = (small ? 1.f : vs) / sum, rest = small ? vs : 1.f;
 #pragma unroll
           for (int t = 0; t < C::kMT; t += 4) {  // eight neighbouring d
             const int d = out_d<D, FP8>(r, t);
             if (cur.whole) {
               uint4 x;
-              x.x = pack2<false>(o[n][t][h] * inv, o[n][t][h + 2] * inv);
-              x.y = pack2<false>(o[n][t + 1][h] * inv, o[n][t + 1][h + 2] * inv);
-              x.z = pack2<false>(o[n][t + 2][h] * inv, o[n][t + 2][h + 2] * inv);
-              x.w = pack2<false>(o[n][t + 3][h] * inv, o[n][t + 3][h + 2] * inv);
+              x.x = pack2<false>(o[n][t][h] * inv * rest, o[n][t][h + 2] * inv * rest);
+              x.y = pack2<false>(o[n][t + 1][h] * inv * rest, o[n][t + 1][h + 2] * inv * rest);
+              x.z = pack2<false>(o[n][t + 2][h] * inv * rest, o[n][t + 2][h + 2] * inv * rest);
+              x.w = pack2<false>(o[n][t + 3][h] * inv * rest, o[n][t + 3][h + 2] * inv * rest);
               *reinterpret_cast<uint4*>(a.out + (row + hh) * D + d) = x;
             } else {
               float4* to = reinterpret_cast<float4*>(a.part_o + (part * G + 8 * n + hh) * D + d);
