@@ -417,10 +417,11 @@ typedef struct {
  * prefill read) or one token per sequence. Row i of sequence b goes to position
  * start_pos[b] + i. With e4m3 pages the code is e4m3(x / scale), x / scale rounded to fp32
  * first, then to nearest even with saturation at +-448 - quail_quantize_kv_fp8's codes when
- * the scales are. With fp4 pages, per 16 values x and with scale S = amax / 2688 using both
- * formats whole: the block scale is b = e4m3(max|x| / (6 S)), the codes are e2m1(x / (b S)),
+ * the scales are. With fp4 pages, per 16 values x and with scale S = amax / 2688 (1 when 0) using
+ * both formats whole: the block scale is b = e4m3(max|x| / (6 S)), the codes are e2m1(x / (b S)),
  * products and quotients rounded to fp32 first, then to nearest even with saturation at +-448
- * and +-6. A block whose scale rounds to 0 holds zeros, one that holds a NaN is all NaN.
+ * and +-6. A block whose scale rounds to 0 holds zeros, one that holds a NaN is all NaN; under a
+ * scale of 0, zeros become 0 / 0, NaN (e4m3 pages too).
  *   num_new     T, new tokens of all sequences
  *   k_new, v_new [T, Hkv, d] bf16, rows k_row_stride / v_row_stride elements apart (>=
  *               Hkv * d, a multiple of 8; e.g. columns of a fused projection), 16-byte

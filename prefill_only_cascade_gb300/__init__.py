@@ -576,7 +576,7 @@ def paged_kv_append(desc: PagedDesc, k_new, v_new, start_pos, block_table, k_pag
     """quail_paged_kv_append: rows k_new / v_new ([T, Hkv, d] bf16, any row stride) into the
     pages at start_pos[b] + i; new_offsets ([B+1] int32) delimits the sequences' rows (None:
     one token each). With e4m3 and fp4 pages the rows become codes under the given scales (fp4:
-    amax / 2688 uses the format whole)."""
+    amax / 2688, or 1 where amax is 0, uses the format whole)."""
     if _calls is not None and stream is None:
         code = _calls.append(desc, k_new, v_new, start_pos, block_table, k_pages, v_pages, new_offsets,
                              k_scale, v_scale)

@@ -40,3 +40,20 @@ def test_v_scales(form, way, exponent):
     out, lse, _ = util.run_decode(c, qt, hq)
     util.check_decode(c, qt, hq, out, lse, only={0, 1, 3, 28, len(lens) - 1} & set(range(len(lens))))
     assert q.get_device_error() == q.QUAIL_OK
+
+
+@pytest.mark.parametrize("form", ["fp8", "fp4"])
+def test_rows_of_zeros(form):
+    """Under the scale that a head of zeros has (1) they come back as zeros, under a scale of 0 as NaN."""
+    desc = q.make_paged_desc(1, 20, 2, 16, 2, 2, 2, 64, kv_fp8=form == "fp8", kv_fp4=form == "fp4")
+    pools = [torch.full(q.paged_pool_shape(desc), 0x31, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    rows = torch.zeros(20, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out = [torch.full_like(rows, 3.0) for _ in range(2)]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    scale = torch.tensor([[1.0, 0.0]], device="cuda")
+    kw = dict(k_scale=scale, v_scale=scale)
+    q.paged_kv_append(desc, rows, -rows, i32(0), i32(1, 0).view(1, 2), *pools, new_offsets=i32(0, 20), **kw)
+    q.paged_kv_read(desc, *pools, i32(0), i32(1, 0).view(1, 2), *out, offsets=i32(0, 20), **kw)
+    for x in out:
+        assert (x[:, 0] == 0).all() and torch.isnan(x[:, 1].float()).all()
+    assert q.get_device_error() == q.QUAIL_OK
