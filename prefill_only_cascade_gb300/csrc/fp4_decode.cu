@@ -893,8 +893,8 @@ __global__ void __launch_bounds__(kFp4Threads<H, MODE>, H <= 8 ? kFp4PerSm : 2)
 }
 
 // Which way (see launch_decode), both sides measured in a graph (8 KV heads, d = 128, G = 4 unless said):
-//   one launch of clusters, up to four tiles a CTA: one sequence of 777 tokens 6.2 us, four of 2,000
-//       8.2 and 10.9, four of 4,000 10.6 and 13.4; past the rule (eight tiles) two of 8,000 15.1 and 14.1,
+//   one launch of clusters, up to four tiles a CTA: one sequence of 777 tokens 5.5 us, four of 2,000
+//       7.5 and 10.9, four of 4,000 9.8 and 13.4; past the rule (eight tiles) two of 8,000 15.1 and 14.1,
 //       one of 8,000 13.0 and 11.8
 //   a warp per (sequence, head), up to eight steps: 181 sequences of 20-83 tokens (4 KV heads, G = 16)
 //       10.3 and 20.8, 256 of 16-128 17.0 and 26.9, 256 of 200-256 26.4 and 34.9; past the rule (16 steps)
@@ -920,7 +920,7 @@ cudaError_t launch_fp4_decode_t(PagedDecodeArgs& a, int num_sms, cudaStream_t st
   if (a.group <= 4) return launch_decode<Fp4Kernel<D, 4>>(a, num_sms, stream);
   if (a.group <= 8) return launch_decode<Fp4Kernel<D, 8>>(a, num_sms, stream);
   // Short sequences with 16 heads: two warps with 8 each, who both read the pages, are done sooner than
-  // one where all run at once (181 sequences of 20-83 tokens, 4 KV heads, 9.3 us and 10.2; 100 of 100-256,
+  // one where all run at once (181 sequences of 20-83 tokens, 4 KV heads, 9.4 us and 10.2; 100 of 100-256,
   // 8 KV heads, 17.5 and 18.7; past the rule, 300 of 150-256 46.9 and 36.3). The weights need all heads in
   // one warp.
   using Half = Fp4Kernel<D, 8>;

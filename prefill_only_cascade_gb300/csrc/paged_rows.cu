@@ -132,8 +132,8 @@ __device__ __noinline__ uint2 divide_block(uint4 lo, uint4 hi, float D) {
 //   the codes   the borders are odd multiples m = 1, 3, 5, 7 of powers of two; a bf16 x can be within
 //               16 units of m D only where the last 16 bits of m D are: D decides for the whole block
 // Random scales send one block in 500 there, scales that are powers of two all of them.
-// (Divisions everywhere, by one FMA correction each: 187 us for 96 prompts of 128-2,048 tokens, 8
-// heads, d = 128; this way 102, with 64 tokens per block and five blocks an SM 125.)
+// (Divisions everywhere, by one FMA correction each: 186 us for 96 prompts of 128-2,048 tokens, 8
+// heads, d = 128; this way 100, with 64 tokens per block and five blocks an SM 125.)
 __device__ __forceinline__ void encode_block(const uint4& lo, const uint4& hi, float S, float r6, bool plain,
                                              uint2& codes, uint8_t& scale) {
   const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
